@@ -411,6 +411,102 @@ hq_status hq_moe_silu_mul_quantize(int32_t act_fmt, int64_t R, int64_t I, const 
 hq_status hq_moe_combine(int64_t T, int32_t topk, int32_t E, int64_t N, const int32_t* topk_ids,
                          const void* y, void* out, hq_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * The decode step: calls for one to a few tokens, where reading the weights once is the whole cost
+ * and every launch shows. Three operators that follow each other in an MoE block:
+ *   hq_moe_route   router logits -> topk_ids, topk_weights
+ *   hq_moe_decode  the routed experts, whole layer, two launches
+ *   hq_gemv        a projection, or the gate and up projections of a dense (shared-expert) gated MLP
+ *                  with the activation in the epilogue
+ * hq_gemv and hq_moe_decode take every weight format with bf16 activations except the 2- and 3-bit
+ * ones (INT4_SYM, UINT4_ASYM, FP4_E2M1 group 32, INT8_SYM and FP8_E4M3 per channel), and INT4_SYM and
+ * UINT4_ASYM with group_size 32 or 64 as well, which hq_gemm and the grouped GEMMs do not; out_fmt
+ * HQ_OUT_BF16, compute_flags 0.
+ * ------------------------------------------------------------------------------------------- */
+
+/* hq_prepacked_bytes / hq_prepack_weights for the descriptions of the decode calls (host; the same
+ * inputs, with scales and zeros [E, N, K/group_size]). For a description that hq_prepack_weights
+ * takes too the result is the same, byte for byte, and serves hq_gemm, the grouped GEMMs and the
+ * decode calls alike; INT4 weights with groups of 32 or 64 are for the decode calls alone. */
+size_t hq_decode_prepacked_bytes(const hq_quant_desc* desc, int64_t E, int64_t N, int64_t K);
+hq_status hq_decode_prepack_weights(const hq_quant_desc* desc, int64_t E, int64_t N, int64_t K,
+                                    const void* wq, const void* scales, const void* zeros,
+                                    void* out, size_t out_bytes);
+
+typedef enum { HQ_LOGITS_FP32 = 0, HQ_LOGITS_BF16 = 1 } hq_logits_fmt;
+typedef enum { HQ_SCORE_SOFTMAX = 0, HQ_SCORE_SIGMOID = 1 } hq_score_fn;
+
+/* ---------------------------------------------------------------------------------------------
+ * MoE router (device): per token t the topk experts of its logits row and their weights, the
+ * topk_ids / topk_weights of the MoE calls.
+ *   s[e] = softmax over e of logits[t, :], or sigmoid(logits[t, e])   (score_fn)
+ *   v[e] = s[e] + bias[e]                                             (bias NULL: s[e])
+ *   The experts form n_group groups of E / n_group neighbours. A group's value is the sum of its
+ *   group_top (1 or 2) largest v; only the experts of the topk_group groups of largest value can be
+ *   chosen (ties: the lower group). n_group = 1: no groups.
+ *   topk_ids[t, :]     the experts of the topk largest v, largest first, ties to the lower id
+ *   topk_weights[t, j] = scale * s[id_j], divided by the sum over j of s[id_j] if renormalize is not 0
+ * v is compared unrounded in effect: by the logits where neither bias nor groups enter, in binary64
+ * otherwise. An expert whose logit or bias is -infinity or NaN is switched off: never chosen, not
+ * counted in its group's value (a group with none left is never kept). A switched-off logit has score
+ * 0; a switched-off bias leaves the expert's score in the softmax. Where fewer than topk
+ * experts can be chosen, the rest of the row is id -1 with weight 0, which the MoE calls route
+ * nowhere; a sum of zero gives weights of 0. Logits of +infinity: softmax shares the whole between
+ * them, sigmoid gives 1.
+ *   logits        [T, E] fp32 or bf16 (logits_fmt), row-major (device, 16-byte aligned)
+ *   bias          fp32 [E] or NULL (device)
+ *   topk_ids      int32 [T, topk], topk_weights fp32 [T, topk] (device)
+ * E 1..512, topk 1..64 and at most topk_group * E / n_group, E % n_group == 0, n_group 1..64, scale
+ * finite, T at most 2^24. T == 0 is a no-op. One launch, no workspace.
+ * ------------------------------------------------------------------------------------------- */
+hq_status hq_moe_route(int32_t score_fn, int64_t T, int32_t E, int32_t topk, const void* logits,
+                       int32_t logits_fmt, const float* bias, int32_t n_group, int32_t topk_group,
+                       int32_t group_top, int32_t renormalize, float scale, int32_t* topk_ids,
+                       float* topk_weights, hq_stream_t stream);
+
+typedef enum {
+  HQ_GEMV_LINEAR = 0,  /* y[m, n] = bf16( sum_k x[m, k] w[n, k] ), 0 <= n < N                     */
+  HQ_GEMV_SILU_MUL = 1 /* w: N/2 gate rows, then N/2 up rows; g, u the two fp32 products of row n
+                          and n + N/2: y[m, n] = bf16( silu(g) * u ), 0 <= n < N/2; N % 32 == 0 */
+} hq_gemv_op;
+
+/* ---------------------------------------------------------------------------------------------
+ * Matrix-vector products with packed weights (device): x [M, K] bf16 row-major, w_packed one
+ * layer's weights of N rows (E = 1), y bf16 [M, N] (or [M, N/2], see op). fp32 accumulation, one
+ * rounding at the end (silu(g) * u never passes through bf16). Made for M of 1 to 16; more rows run
+ * in blocks of 16 that each read the weights again. M <= 65536, N <= 2^24, M * N < 2^31.
+ * x, w_packed and y 16-byte aligned; y must not overlap x. M == 0 is a no-op. No workspace.
+ * ------------------------------------------------------------------------------------------- */
+hq_status hq_gemv(const hq_quant_desc* desc, int32_t op, int64_t M, int64_t N, int64_t K, const void* x,
+                  const void* w_packed, void* y, hq_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * The MoE layer for a few tokens (device), what the calls hq_moe_align .. hq_moe_combine compute in
+ * five launches, in two:
+ *   act[t, j] = bf16( silu(g) * u ),  (g, u) = x[t] . dequant(Wgu_e)^T in fp32,  e = topk_ids[t, j]
+ *   out[t]    = bf16( sum_j topk_weights[t, j] * (act[t, j] . dequant(Wd_e)^T) ),  fp32 sums
+ * Only act and out are rounded (the five calls also round gate_up and each expert's output).
+ * Entries whose id is outside [0, E) contribute nothing; a token with none left gets zeros. The same
+ * expert may stand in a token's row more than once.
+ *   x             bf16 [T, H], out bf16 [T, H] (out may be x)
+ *   topk_ids      int32 [T, topk], topk_weights fp32 [T, topk] or NULL (all 1)
+ *   w_gate_up     E experts of 2I rows (I gate rows, then I up rows) by H, prepacked with desc
+ *   w_down        E experts of H rows by I, prepacked with desc
+ *   ws            hq_moe_decode_workspace_bytes(...) bytes, contents irrelevant on entry. Calls that
+ *                 may run at the same time (other streams, replays of captured graphs) each need
+ *                 their own.
+ * T 1..HQ_MOE_DECODE_MAX_TOKENS (more: HQ_ERR_UNSUPPORTED; use the grouped GEMMs), topk 1..64,
+ * E 1..512, H and I multiples of 128. Pointers 16-byte aligned (ids and weights 4). T == 0 is a no-op.
+ * The result does not depend on the order in which workgroups run.
+ * ------------------------------------------------------------------------------------------- */
+#define HQ_MOE_DECODE_MAX_TOKENS 16
+size_t hq_moe_decode_workspace_bytes(const hq_quant_desc* desc, int64_t T, int32_t topk, int32_t E,
+                                     int64_t H, int64_t I);
+hq_status hq_moe_decode(const hq_quant_desc* desc, int64_t T, int32_t topk, int32_t E, int64_t H,
+                        int64_t I, const void* x, const int32_t* topk_ids, const float* topk_weights,
+                        const void* w_gate_up, const void* w_down, void* out, void* ws,
+                        size_t ws_bytes, hq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -39,3 +39,4 @@ from .actquant import (  # noqa: F401
     encode_e4m3, quantize_per_token, encode_e2m1, quantize_mxfp4_act, quantize_mxfp8_act,
     quantize_fp8_block_act,
 )
+from .decode import dequant_int4_groups, ref_route, ref_gemv, ref_moe_decode  # noqa: F401

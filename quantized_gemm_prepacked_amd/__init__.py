@@ -31,6 +31,10 @@ HQ_W_INT4_SYM, HQ_W_UINT4_ASYM, HQ_W_INT8_SYM, HQ_W_FP4_E2M1, HQ_W_FP8_E4M3, HQ_
 HQ_SCALE_BF16, HQ_SCALE_FP32, HQ_SCALE_E8M0 = range(3)
 HQ_ACT_BF16, HQ_ACT_INT8_PER_TOKEN, HQ_ACT_FP8E4M3_PER_TOKEN, HQ_ACT_MXFP4, HQ_ACT_MXFP8, HQ_ACT_FP8E4M3_BLOCK128 = range(6)
 HQ_OUT_BF16, HQ_OUT_INT32_ACC = range(2)
+HQ_LOGITS_FP32, HQ_LOGITS_BF16 = range(2)
+HQ_SCORE_SOFTMAX, HQ_SCORE_SIGMOID = range(2)
+HQ_GEMV_LINEAR, HQ_GEMV_SILU_MUL = range(2)
+HQ_MOE_DECODE_MAX_TOKENS = 16
 
 EXPORTED = (
     "hq_prepacked_bytes", "hq_prepack_weights", "hq_gemm_workspace_bytes", "hq_gemm", "hq_gemm_noalloc",
@@ -39,6 +43,8 @@ EXPORTED = (
     "hq_moe_silu_mul", "hq_moe_silu_mul_quantize", "hq_moe_combine", "hq_grouped_gemm_workspace_bytes",
     "hq_grouped_gemm",
     "hq_load_tuning_table", "hq_gemm_plan", "hq_kernel_config_count",
+    "hq_decode_prepacked_bytes", "hq_decode_prepack_weights", "hq_moe_route", "hq_gemv",
+    "hq_moe_decode_workspace_bytes", "hq_moe_decode",
     "hq_last_error", "hq_version",
 )
 
@@ -86,6 +92,11 @@ DESC_W8A16_INT8 = make_desc(HQ_W_INT8_SYM, 0, HQ_SCALE_FP32, 0, HQ_ACT_BF16)
 DESC_W8A16_FP8 = make_desc(HQ_W_FP8_E4M3, 0, HQ_SCALE_FP32, 0, HQ_ACT_BF16)
 DESC_W2A16_ASYM = make_desc(HQ_W_UINT2_ASYM, 128, HQ_SCALE_BF16, 1, HQ_ACT_BF16)
 DESC_W3A16_ASYM = make_desc(HQ_W_UINT3_ASYM, 128, HQ_SCALE_BF16, 1, HQ_ACT_BF16)
+# INT4 with finer groups: the decode calls (hq_gemv, hq_moe_decode) only
+DESC_W4A16_SYM_G32 = make_desc(HQ_W_INT4_SYM, 32, HQ_SCALE_BF16, 0, HQ_ACT_BF16)
+DESC_W4A16_SYM_G64 = make_desc(HQ_W_INT4_SYM, 64, HQ_SCALE_BF16, 0, HQ_ACT_BF16)
+DESC_W4A16_ASYM_G32 = make_desc(HQ_W_UINT4_ASYM, 32, HQ_SCALE_BF16, 1, HQ_ACT_BF16)
+DESC_W4A16_ASYM_G64 = make_desc(HQ_W_UINT4_ASYM, 64, HQ_SCALE_BF16, 1, HQ_ACT_BF16)
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -125,6 +136,14 @@ _c = {
     "hq_moe_silu_mul": _sig("hq_moe_silu_mul", ctypes.c_int, _I64, _I64, _P, _P, _P),
     "hq_moe_silu_mul_quantize": _sig("hq_moe_silu_mul_quantize", ctypes.c_int, _I32, _I64, _I64, _P, _P, _P, _P),
     "hq_moe_combine": _sig("hq_moe_combine", ctypes.c_int, _I64, _I32, _I32, _I64, _P, _P, _P, _P),
+    "hq_decode_prepacked_bytes": _sig("hq_decode_prepacked_bytes", _SZ, _D, _I64, _I64, _I64),
+    "hq_decode_prepack_weights": _sig("hq_decode_prepack_weights", ctypes.c_int, _D, _I64, _I64, _I64, _P, _P, _P, _P, _SZ),
+    "hq_moe_route": _sig("hq_moe_route", ctypes.c_int, _I32, _I64, _I32, _I32, _P, _I32, _P, _I32, _I32, _I32, _I32,
+                         ctypes.c_float, _P, _P, _P),
+    "hq_gemv": _sig("hq_gemv", ctypes.c_int, _D, _I32, _I64, _I64, _I64, _P, _P, _P, _P),
+    "hq_moe_decode_workspace_bytes": _sig("hq_moe_decode_workspace_bytes", _SZ, _D, _I64, _I32, _I32, _I64, _I64),
+    "hq_moe_decode": _sig("hq_moe_decode", ctypes.c_int, _D, _I64, _I32, _I32, _I64, _I64, _P, _P, _P, _P, _P, _P, _P,
+                          _SZ, _P),
     "hq_last_error": _sig("hq_last_error", ctypes.c_char_p),
     "hq_version": _sig("hq_version", _I32),
 }
@@ -276,3 +295,57 @@ def hq_moe_silu_mul_quantize(act_fmt, R, I, gate_up, act_q, act_scale, stream=No
 
 def hq_moe_combine(T, topk, E, N, topk_ids, y, out, stream=None):
     _check(_c["hq_moe_combine"](T, topk, E, N, _ptr(topk_ids), _ptr(y), _ptr(out), _stream(stream)))
+
+
+# ---- decode step ------------------------------------------------------------------------------
+def _buf(x, nbytes, what):
+    """Device address of a decode call's buffer. A tensor has to be contiguous, on the current device
+    and hold nbytes (None: not checked): what the C side cannot see, and would read past."""
+    if x is None or isinstance(x, int):
+        return x
+    if not x.is_contiguous():
+        raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} must be contiguous")
+    if nbytes is not None and x.nbytes < nbytes:
+        raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} holds {x.nbytes} bytes, {nbytes} are needed")
+    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
+        raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} must be on the current device")
+    return x.data_ptr()
+
+
+def hq_decode_prepacked_bytes(desc, E, N, K) -> int:
+    return _c["hq_decode_prepacked_bytes"](_d(desc), E, N, K)
+
+
+def hq_decode_prepack_weights(desc, E, N, K, wq: np.ndarray, scales: np.ndarray, zeros, out: np.ndarray):
+    """Host prepack for the decode calls into ``out`` (uint8, hq_decode_prepacked_bytes bytes)."""
+    arrs = [np.ascontiguousarray(a) for a in (wq, scales)]
+    z = None if zeros is None else np.ascontiguousarray(zeros)
+    _check(_c["hq_decode_prepack_weights"](_d(desc), E, N, K, _ptr(arrs[0]), _ptr(arrs[1]), _ptr(z), _ptr(out),
+                                           out.nbytes))
+    return out
+
+
+def hq_moe_route(score_fn, T, E, topk, logits, logits_fmt, bias, n_group, topk_group, group_top, renormalize, scale,
+                 topk_ids, topk_weights, stream=None):
+    _check(_c["hq_moe_route"](score_fn, T, E, topk, _buf(logits, T * E * (2 if logits_fmt == HQ_LOGITS_BF16 else 4), "logits"),
+                              logits_fmt, _buf(bias, 4 * E, "bias"), n_group, topk_group, group_top, int(renormalize), scale,
+                              _buf(topk_ids, 4 * T * topk, "topk_ids"), _buf(topk_weights, 4 * T * topk, "topk_weights"),
+                              _stream(stream)))
+
+
+def hq_gemv(desc, op, M, N, K, x, w_packed, y, stream=None):
+    outs = N // 2 if op == HQ_GEMV_SILU_MUL else N
+    _check(_c["hq_gemv"](_d(desc), op, M, N, K, _buf(x, 2 * M * K, "x"), _buf(w_packed, None, "w_packed"),
+                         _buf(y, 2 * M * outs, "y"), _stream(stream)))
+
+
+def hq_moe_decode_workspace_bytes(desc, T, topk, E, H, I) -> int:
+    return _c["hq_moe_decode_workspace_bytes"](_d(desc), T, topk, E, H, I)
+
+
+def hq_moe_decode(desc, T, topk, E, H, I, x, topk_ids, topk_weights, w_gate_up, w_down, out, ws=None, ws_bytes=0,
+                  stream=None):
+    _check(_c["hq_moe_decode"](_d(desc), T, topk, E, H, I, _buf(x, 2 * T * H, "x"), _buf(topk_ids, 4 * T * topk, "topk_ids"),
+                               _buf(topk_weights, 4 * T * topk, "topk_weights"), _buf(w_gate_up, None, "w_gate_up"),
+                               _buf(w_down, None, "w_down"), _buf(out, 2 * T * H, "out"), _buf(ws, ws_bytes, "ws"), ws_bytes,
+                               _stream(stream)))

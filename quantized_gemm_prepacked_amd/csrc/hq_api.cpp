@@ -8,6 +8,7 @@
 #include <hip/hip_runtime_api.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <string>
@@ -135,6 +136,23 @@ hq_status check_shape(const hq::Combo& c, int64_t N, int64_t K) {
   if (N % 16 != 0 || K % ku != 0)
     return fail(HQ_ERR_UNSUPPORTED, "N must be a multiple of 16 and K of %d (N=%lld K=%lld)", ku,
                 (long long)N, (long long)K);
+  return HQ_OK;
+}
+
+// Map a description onto a combination of the decode calls: the formats with bf16 activations but the
+// 2- and 3-bit ones, and INT4 with groups of 32 or 64.
+hq_status resolve_decode(const hq_quant_desc* d, hq::Combo* c) {
+  if (!d) return fail(HQ_ERR_INVALID_ARGUMENT, "desc is NULL");
+  hq_quant_desc as128 = *d;
+  const bool fine = (d->weight_fmt == HQ_W_INT4_SYM || d->weight_fmt == HQ_W_UINT4_ASYM) &&
+                    (d->group_size == 32 || d->group_size == 64);
+  if (fine) as128.group_size = 128;
+  const hq_status s = resolve(&as128, c);
+  if (s != HQ_OK) return s;
+  if (d->compute_flags != 0) return fail(HQ_ERR_UNSUPPORTED, "the decode calls take no compute_flags");
+  if (!hq::family_bf16_act(c->fam) || c->fam == hq::FAM_WNA2 || c->fam == hq::FAM_WNA3)
+    return fail(HQ_ERR_UNSUPPORTED, "the decode calls take 4- and 8-bit weights with BF16 activations");
+  c->fine_group = fine ? d->group_size : 0;
   return HQ_OK;
 }
 
@@ -514,6 +532,156 @@ hq_status hq_moe_grouped_gemm(const hq_quant_desc* desc, int64_t T, int32_t topk
   call.block_m = block_m;
   call.max_blocks = int64_t(hq_moe_align_capacity(T, topk, E, block_m)) / block_m;
   return check_hip(hq::launch_gemm(call, plan), "hq_moe_grouped_gemm launch");
+}
+
+size_t hq_decode_prepacked_bytes(const hq_quant_desc* desc, int64_t E, int64_t N, int64_t K) {
+  hq::Combo c{};
+  if (resolve_decode(desc, &c) != HQ_OK || E <= 0 || E > 65536 || check_shape(c, N, K) != HQ_OK) return 0;
+  return hq::decode_prepacked_bytes(c, E, N, K);
+}
+
+hq_status hq_decode_prepack_weights(const hq_quant_desc* desc, int64_t E, int64_t N, int64_t K, const void* wq,
+                                    const void* scales, const void* zeros, void* out, size_t out_bytes) {
+  hq::Combo c{};
+  hq_status s = resolve_decode(desc, &c);
+  if (s != HQ_OK) return s;
+  if (E <= 0 || E > 65536) return fail(HQ_ERR_INVALID_ARGUMENT, "E=%lld out of range", (long long)E);
+  if ((s = check_shape(c, N, K)) != HQ_OK) return s;
+  if (!wq || !scales || !out) return fail(HQ_ERR_INVALID_ARGUMENT, "wq, scales and out must be non-NULL");
+  if (c.asym != (zeros != nullptr))
+    return fail(HQ_ERR_INVALID_ARGUMENT, c.asym ? "zeros must be non-NULL for UINT4_ASYM" : "zeros must be NULL without zero-points");
+  const size_t need = hq::decode_prepacked_bytes(c, E, N, K);
+  if (out_bytes < need) return fail(HQ_ERR_WORKSPACE, "out_bytes %zu < required %zu", out_bytes, need);
+  hq::decode_prepack(c, E, N, K, wq, scales, zeros, out);
+  return ok();
+}
+
+hq_status hq_moe_route(int32_t score_fn, int64_t T, int32_t E, int32_t topk, const void* logits, int32_t logits_fmt,
+                       const float* bias, int32_t n_group, int32_t topk_group, int32_t group_top, int32_t renormalize,
+                       float scale, int32_t* topk_ids, float* topk_weights, hq_stream_t stream) {
+  if (score_fn != HQ_SCORE_SOFTMAX && score_fn != HQ_SCORE_SIGMOID)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "unknown score_fn %d", score_fn);
+  if (logits_fmt != HQ_LOGITS_FP32 && logits_fmt != HQ_LOGITS_BF16)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "unknown logits_fmt %d", logits_fmt);
+  if (T < 0 || T > (int64_t(1) << 24)) return fail(HQ_ERR_INVALID_ARGUMENT, "T=%lld out of range", (long long)T);
+  if (E <= 0 || E > 512) return fail(HQ_ERR_UNSUPPORTED, "E=%d: 1..512 experts supported", E);
+  if (n_group <= 0 || n_group > 64 || E % n_group != 0)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "n_group=%d must be 1..64 and divide E=%d", n_group, E);
+  if (topk_group <= 0 || topk_group > n_group)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "topk_group=%d must be 1..n_group=%d", topk_group, n_group);
+  if (group_top != 1 && group_top != 2) return fail(HQ_ERR_INVALID_ARGUMENT, "group_top=%d must be 1 or 2", group_top);
+  if (topk <= 0 || topk > 64 || topk > E / n_group * topk_group)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "topk=%d must be 1..64 and at most topk_group * E / n_group = %d", topk,
+                E / n_group * topk_group);
+  if (!std::isfinite(scale)) return fail(HQ_ERR_INVALID_ARGUMENT, "scale must be finite");
+  if (T == 0) return ok();
+  if (!logits || !topk_ids || !topk_weights)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "logits, topk_ids and topk_weights must be non-NULL");
+  if (!aligned16(logits) || ((reinterpret_cast<uintptr_t>(bias) | reinterpret_cast<uintptr_t>(topk_ids) |
+                              reinterpret_cast<uintptr_t>(topk_weights)) & 3u))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "logits must be 16-byte aligned; bias, topk_ids and topk_weights 4-byte aligned");
+  hq::RouteCall r{};
+  r.logits = logits;
+  r.bias = bias;
+  r.topk_ids = topk_ids;
+  r.topk_weights = topk_weights;
+  r.T = T;
+  r.E = E;
+  r.topk = topk;
+  r.score_fn = score_fn;
+  r.bf16 = logits_fmt == HQ_LOGITS_BF16;
+  r.n_group = n_group;
+  r.topk_group = topk_group;
+  r.group_top = group_top;
+  r.renormalize = renormalize != 0;
+  r.scale = scale;
+  return check_hip(hq::launch_moe_route(r, static_cast<hipStream_t>(stream)), "hq_moe_route launch");
+}
+
+hq_status hq_gemv(const hq_quant_desc* desc, int32_t op, int64_t M, int64_t N, int64_t K, const void* x,
+                  const void* w_packed, void* y, hq_stream_t stream) {
+  hq::Combo c{};
+  hq_status s = resolve_decode(desc, &c);
+  if (s != HQ_OK) return s;
+  if (op != HQ_GEMV_LINEAR && op != HQ_GEMV_SILU_MUL) return fail(HQ_ERR_INVALID_ARGUMENT, "unknown op %d", op);
+  if ((s = check_shape(c, N, K)) != HQ_OK) return s;
+  if (op == HQ_GEMV_SILU_MUL && N % 32 != 0)
+    return fail(HQ_ERR_UNSUPPORTED, "HQ_GEMV_SILU_MUL needs N %% 32 == 0 (N=%lld)", (long long)N);
+  if (M < 0 || M > 65536) return fail(HQ_ERR_INVALID_ARGUMENT, "M=%lld out of range", (long long)M);
+  if (N > (int64_t(1) << 24) || M * N >= (int64_t(1) << 31))
+    return fail(HQ_ERR_UNSUPPORTED, "N must be at most 2^24 and M*N below 2^31 (M=%lld N=%lld)", (long long)M, (long long)N);
+  if (M == 0) return ok();
+  if (!x || !w_packed || !y) return fail(HQ_ERR_INVALID_ARGUMENT, "x, w_packed and y must be non-NULL");
+  if (!aligned16(x) || !aligned16(w_packed) || !aligned16(y))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "x, w_packed and y must be 16-byte aligned");
+  hq::GemvCall g{};
+  g.c = c;
+  g.gated = op == HQ_GEMV_SILU_MUL;
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.x = x;
+  g.w = static_cast<const uint8_t*>(w_packed);
+  g.y = y;
+  return check_hip(hq::launch_gemv(g, static_cast<hipStream_t>(stream)), "hq_gemv launch");
+}
+
+namespace {
+// The sizes of an hq_moe_decode call (T > 0 included).
+hq_status check_moe_decode(const hq_quant_desc* desc, int64_t T, int32_t topk, int32_t E, int64_t H, int64_t I,
+                           hq::Combo* c) {
+  hq_status s = resolve_decode(desc, c);
+  if (s != HQ_OK) return s;
+  if (T < 0) return fail(HQ_ERR_INVALID_ARGUMENT, "T=%lld out of range", (long long)T);
+  if (T > HQ_MOE_DECODE_MAX_TOKENS)
+    return fail(HQ_ERR_UNSUPPORTED, "T=%lld: hq_moe_decode takes up to %d tokens (use the grouped GEMMs)", (long long)T,
+                HQ_MOE_DECODE_MAX_TOKENS);
+  if (topk <= 0 || topk > 64 || E <= 0 || E > 512)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "topk=%d E=%d out of range", topk, E);
+  if (H <= 0 || I <= 0 || H > (int64_t(1) << 23) || I > (int64_t(1) << 23))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "H=%lld I=%lld out of range", (long long)H, (long long)I);
+  if (H % 128 != 0 || I % 128 != 0)
+    return fail(HQ_ERR_UNSUPPORTED, "H and I must be multiples of 128 (H=%lld I=%lld)", (long long)H, (long long)I);
+  return HQ_OK;
+}
+}  // namespace
+
+size_t hq_moe_decode_workspace_bytes(const hq_quant_desc* desc, int64_t T, int32_t topk, int32_t E, int64_t H, int64_t I) {
+  hq::Combo c{};
+  if (check_moe_decode(desc, T, topk, E, H, I, &c) != HQ_OK || T == 0) return 0;
+  return hq::moe_decode_ws_bytes(c, T, topk, E, H, I);
+}
+
+hq_status hq_moe_decode(const hq_quant_desc* desc, int64_t T, int32_t topk, int32_t E, int64_t H, int64_t I,
+                        const void* x, const int32_t* topk_ids, const float* topk_weights, const void* w_gate_up,
+                        const void* w_down, void* out, void* ws, size_t ws_bytes, hq_stream_t stream) {
+  hq::Combo c{};
+  const hq_status s = check_moe_decode(desc, T, topk, E, H, I, &c);
+  if (s != HQ_OK) return s;
+  if (T == 0) return ok();
+  if (!x || !topk_ids || !w_gate_up || !w_down || !out)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "x, topk_ids, w_gate_up, w_down and out must be non-NULL");
+  if (!aligned16(x) || !aligned16(w_gate_up) || !aligned16(w_down) || !aligned16(out) || !aligned16(ws))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "x, w_gate_up, w_down, out and ws must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(topk_ids) | reinterpret_cast<uintptr_t>(topk_weights)) & 3u)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "topk_ids and topk_weights must be 4-byte aligned");
+  const size_t need = hq::moe_decode_ws_bytes(c, T, topk, E, H, I);
+  if (!ws || ws_bytes < need) return fail(HQ_ERR_WORKSPACE, "workspace %zu < required %zu", ws ? ws_bytes : size_t(0), need);
+  hq::MoeDecodeCall m{};
+  m.c = c;
+  m.T = int(T);
+  m.topk = topk;
+  m.E = E;
+  m.H = H;
+  m.I = I;
+  m.x = x;
+  m.topk_ids = topk_ids;
+  m.topk_weights = topk_weights;
+  m.w_gate_up = static_cast<const uint8_t*>(w_gate_up);
+  m.w_down = static_cast<const uint8_t*>(w_down);
+  m.out = out;
+  m.ws = ws;
+  return check_hip(hq::launch_moe_decode(m, static_cast<hipStream_t>(stream)), "hq_moe_decode launch");
 }
 
 }  // extern "C"

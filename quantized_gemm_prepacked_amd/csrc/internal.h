@@ -19,11 +19,17 @@ struct Combo {
   bool out_i32;  // W8A8 raw accumulator output
   bool invariant;  // HQ_COMPUTE_BATCH_INVARIANT: one fixed kernel configuration for every M
   bool stream_k;   // HQ_COMPUTE_STREAM_K: small-M calls balanced over the CUs (Stream-K)
+  int fine_group;  // decode calls only: INT4 weights with groups of 32 or 64 k (0: the format's own)
 };
 
 size_t prepacked_bytes(const Combo& c, int64_t E, int64_t N, int64_t K);
 void prepack(const Combo& c, int64_t E, int64_t N, int64_t K, const void* wq, const void* scales,
              const void* zeros, void* out);
+
+// The decode calls' layout (the format's own, or the fine-group one) and its prepack.
+size_t decode_prepacked_bytes(const Combo& c, int64_t E, int64_t N, int64_t K);
+void decode_prepack(const Combo& c, int64_t E, int64_t N, int64_t K, const void* wq, const void* scales,
+                    const void* zeros, void* out);
 
 // Kernel choice for one call (see dispatch in gemm_kernels.hip).
 struct Plan {
@@ -85,6 +91,44 @@ hipError_t launch_act_quant(int act_fmt, int64_t M, int64_t K, const void* x, vo
                             hipStream_t stream);
 hipError_t launch_silu_mul_quant(int act_fmt, int64_t R, int64_t I, const void* gate_up, void* act_q,
                                  float* act_scale, hipStream_t stream);
+
+// hq_moe_route, validated.
+struct RouteCall {
+  const void* logits;
+  const float* bias;
+  int32_t* topk_ids;
+  float* topk_weights;
+  int64_t T;
+  int E, topk, score_fn, bf16, n_group, topk_group, group_top, renormalize;
+  float scale;
+};
+hipError_t launch_moe_route(const RouteCall& c, hipStream_t s);
+
+// hq_gemv / hq_moe_decode, validated.
+struct GemvCall {
+  Combo c;
+  bool gated;
+  int64_t M, N, K;
+  const void* x;
+  const uint8_t* w;
+  void* y;
+};
+hipError_t launch_gemv(const GemvCall& g, hipStream_t s);
+struct MoeDecodeCall {
+  Combo c;
+  int T, topk, E;
+  int64_t H, I;
+  const void* x;
+  const int32_t* topk_ids;
+  const float* topk_weights;
+  const uint8_t* w_gate_up;
+  const uint8_t* w_down;
+  void* out;
+  void* ws;
+};
+size_t moe_decode_ws_bytes(const Combo& c, int64_t T, int32_t topk, int32_t E, int64_t H, int64_t I);
+hipError_t launch_moe_decode(const MoeDecodeCall& m, hipStream_t s);
+
 hipError_t launch_moe_align(const int32_t* topk_ids, int64_t T, int32_t topk, int32_t E,
                             int32_t block_m, int32_t* sorted_ids, int32_t* block_expert,
                             int32_t* expert_offsets, int32_t* num_padded, void* ws,

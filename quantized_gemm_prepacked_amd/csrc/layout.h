@@ -41,6 +41,15 @@
 //                 the zero of channel 2i (low nibble) and 2i+1 (high nibble)
 //   W8A8, W8A16, F8A16 scales: [N] fp32 per channel
 //   W4A8  scales: [N/16][K/128][64] e8m0 bytes, byte l = scale of lane l's block
+//
+// INT4 with groups of 32 or 64 k (the decode calls, hq_gemv and hq_moe_decode): the same 1 KiB units,
+// but lane l's dword d holds k = 128*kt + 32*d + 8*(l>>4) + j (same nibble order inside), so that MFMA d
+// of a unit contracts exactly the 32 k of [32 d, 32 d + 32) and the sums of the groups stay apart: one
+// MFMA a group at 32, two at 64. (In WNA16's order every MFMA reaches over all four 32-k runs of the
+// unit.) Scales and zeros of a unit stand together, channel by channel, so a lane reads its channel's
+// with one load each:
+//   meta  : [N/16][K/128] blocks of [16 channels][128/G] bf16 scales, then (asym) [16 channels] zeros,
+//           4 bits each, group 0 in the low bits: 2 bytes a channel at 32, 1 byte at 64
 #pragma once
 #include <stdint.h>
 #include <stddef.h>
@@ -116,6 +125,28 @@ inline PackedLayout make_layout(Family fam, bool asym, int64_t N, int64_t K) {
   L.zeros_off = align256(L.scales_off + L.scales_bytes);
   L.zeros_bytes = (family_int_groups(fam) && asym) ? size_t(L.n_tiles) * L.k_units * 8 : 0;
   L.expert_stride = align256(L.zeros_off + L.zeros_bytes);
+  return L;
+}
+
+// Fine groups (G = 32 or 64): bytes of one unit's meta block.
+inline constexpr int fine_scale_bytes(int G) { return 16 * (128 / G) * 2; }
+inline constexpr int fine_zero_bytes(int G) { return 16 * (128 / G) / 2; }
+inline constexpr int fine_meta_bytes(int G, bool asym) { return fine_scale_bytes(G) + (asym ? fine_zero_bytes(G) : 0); }
+
+// Layout of INT4 weights with groups of G = 32 or 64 k: scales_off is the meta region.
+inline PackedLayout make_fine_layout(int G, bool asym, int64_t N, int64_t K) {
+  PackedLayout L{};
+  L.fam = FAM_WNA16;
+  L.asym = asym;
+  L.N = N;
+  L.K = K;
+  L.n_tiles = N / kTileN;
+  L.k_units = K / 128;
+  L.codes_bytes = size_t(L.n_tiles) * size_t(L.k_units) * kUnitBytes;
+  L.scales_off = align256(L.codes_bytes);
+  L.scales_bytes = size_t(L.n_tiles) * size_t(L.k_units) * fine_meta_bytes(G, asym);
+  L.zeros_off = align256(L.scales_off + L.scales_bytes);
+  L.expert_stride = L.zeros_off;
   return L;
 }
 

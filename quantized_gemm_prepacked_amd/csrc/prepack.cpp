@@ -5,7 +5,6 @@
 #include <algorithm>
 #include <cstring>
 #include <thread>
-#include <vector>
 
 #include "internal.h"
 #include "layout.h"
@@ -22,14 +21,18 @@ void parallel_for(int64_t n, F&& f) {
     for (int64_t i = 0; i < n; ++i) f(i);
     return;
   }
-  std::vector<std::thread> th;
-  th.reserve(workers);
-  for (int64_t w = 0; w < workers; ++w) {
-    th.emplace_back([&, w] {
-      for (int64_t i = w; i < n; i += workers) f(i);
-    });
+  auto share = [&](int64_t w) {
+    for (int64_t i = w; i < n; i += workers) f(i);
+  };
+  std::thread th[32];
+  int64_t started = 0;
+  try {
+    for (; started < workers; ++started) th[started] = std::thread(share, started);
+  } catch (...) {
+    // no more threads to be had: the caller does the remaining shares (no exception may leave a C entry)
   }
-  for (auto& t : th) t.join();
+  for (int64_t w = started; w < workers; ++w) share(w);
+  for (int64_t w = 0; w < started; ++w) th[w].join();
 }
 
 // Nibble j (0..7) of an 8-code group moves to slot p with j = 2*(p&3) + (p>>2).
@@ -210,7 +213,62 @@ void pack_w4a8(const PackedLayout& L, const uint8_t* wq, const uint8_t* scales, 
   });
 }
 
+// INT4 with groups of G = 32 or 64 k (layout.h): dword d of a lane holds 8 of the 32 k of run d.
+void pack_fine(const PackedLayout& L, int G, const uint8_t* wq, const uint16_t* scales, const uint8_t* zeros,
+               uint8_t* out) {
+  const int64_t K = L.K, groups = K / G;
+  const int per = 128 / G, meta = fine_meta_bytes(G, L.asym);
+  parallel_for(L.n_tiles, [&](int64_t nt) {
+    uint8_t codes[8];
+    for (int64_t kt = 0; kt < L.k_units; ++kt) {
+      const size_t at = size_t(nt) * L.k_units + kt;
+      uint8_t* unit = out + L.codes_off + at * kUnitBytes;
+      for (int l = 0; l < 64; ++l) {
+        const uint8_t* row = wq + size_t(nt * 16 + (l & 15)) * (K / 2);
+        uint32_t* dst = reinterpret_cast<uint32_t*>(unit + 16 * l);
+        for (int d = 0; d < 4; ++d) {
+          const int64_t k0 = kt * 128 + 32 * d + 8 * (l >> 4);
+          for (int j = 0; j < 8; ++j) {
+            const uint8_t b = row[(k0 + j) >> 1];
+            const uint8_t c = (j & 1) ? (b >> 4) : (b & 0xF);
+            codes[j] = L.asym ? c : uint8_t(c ^ 0x8);
+          }
+          dst[d] = interleave8(codes);
+        }
+      }
+      uint8_t* m = out + L.scales_off + at * meta;
+      for (int i = 0; i < 16; ++i) {
+        const size_t g0 = size_t(nt * 16 + i) * groups + kt * per;
+        std::memcpy(m + i * per * 2, scales + g0, size_t(per) * 2);
+        if (L.asym) {
+          uint32_t z = 0;
+          for (int g = 0; g < per; ++g) z |= uint32_t(zeros[g0 + g] & 0xF) << (4 * g);
+          std::memcpy(m + fine_scale_bytes(G) + i * (per / 2), &z, size_t(per / 2));   // little endian
+        }
+      }
+    }
+  });
+}
+
 }  // namespace
+
+size_t decode_prepacked_bytes(const Combo& c, int64_t E, int64_t N, int64_t K) {
+  if (!c.fine_group) return prepacked_bytes(c, E, N, K);
+  return make_fine_layout(c.fine_group, c.asym, N, K).expert_stride * size_t(E);
+}
+
+void decode_prepack(const Combo& c, int64_t E, int64_t N, int64_t K, const void* wq, const void* scales,
+                    const void* zeros, void* out) {
+  if (!c.fine_group) return prepack(c, E, N, K, wq, scales, zeros, out);
+  const PackedLayout L = make_fine_layout(c.fine_group, c.asym, N, K);
+  std::memset(out, 0, L.expert_stride * size_t(E));
+  const size_t wq_stride = size_t(N) * (K / 2), s_stride = size_t(N) * (K / c.fine_group);
+  for (int64_t e = 0; e < E; ++e)
+    pack_fine(L, c.fine_group, static_cast<const uint8_t*>(wq) + e * wq_stride,
+              static_cast<const uint16_t*>(scales) + e * s_stride,
+              c.asym ? static_cast<const uint8_t*>(zeros) + e * s_stride : nullptr,
+              static_cast<uint8_t*>(out) + L.expert_stride * size_t(e));
+}
 
 size_t prepacked_bytes(const Combo& c, int64_t E, int64_t N, int64_t K) {
   PackedLayout L = make_layout(c.fam, c.asym, N, K);

@@ -1,0 +1,223 @@
+"""CPU checks of the decode-step calls: oracle pins, the fine-group layout, and every refusal (made on
+the host before any launch, so they run without a GPU)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import quantized_gemm_prepacked_amd as hq
+import synth
+
+from decode_harness import FORMATS, dequant, prepack_host, random_weights, route_case
+
+INV, UNS, WSP = hq.HQ_ERR_INVALID_ARGUMENT, hq.HQ_ERR_UNSUPPORTED, hq.HQ_ERR_WORKSPACE
+G32 = hq.DESC_W4A16_SYM_G32
+
+
+# ---- oracle pins ------------------------------------------------------------------------------
+def test_route_oracle_against_torch():
+    g = np.random.default_rng(1)
+    l = route_case(g, 9, 24, False)
+    t = torch.from_numpy(l).double()
+    ids, w = oracle.ref_route(l, None, "softmax", 5, renormalize=False, scale=2.0)
+    top = torch.softmax(t, 1).topk(5, 1)
+    assert np.array_equal(ids, top.indices.numpy()) and np.allclose(w, 2.0 * top.values.numpy(), rtol=1e-14)
+    ids, w = oracle.ref_route(l, None, "sigmoid", 5)
+    top = torch.sigmoid(t).topk(5, 1)
+    assert np.array_equal(ids, top.indices.numpy())
+    assert np.allclose(w, (top.values / top.values.sum(1, keepdim=True)).numpy(), rtol=1e-14)
+
+
+def test_route_oracle_by_hand():
+    l = np.log(np.array([[1.0, 3.0, 2.0, 2.0], [1.0, 1.0, 1.0, 1.0]]))
+    ids, w = oracle.ref_route(l, None, "softmax", 2, renormalize=False)
+    assert ids.tolist() == [[1, 2], [0, 1]] and np.allclose(w, [[3 / 8, 2 / 8], [1 / 4, 1 / 4]])
+    # groups {0,1} and {2,3}: sums of two 4/8 and 4/8 -> the lower group
+    ids, _ = oracle.ref_route(l[:1], None, "softmax", 2, n_group=2, topk_group=1)
+    assert ids.tolist() == [[1, 0]]
+    # by the largest alone group 0 wins too; a bias on expert 3 turns it
+    ids, w = oracle.ref_route(l[:1], np.array([0, 0, 0, 0.5], np.float32), "softmax", 2, n_group=2, topk_group=1, group_top=1)
+    assert ids.tolist() == [[3, 2]] and np.allclose(w, [[0.5, 0.5]])
+    off = np.array([[-math.inf, math.nan, 1.0, -math.inf]])
+    ids, w = oracle.ref_route(off, None, "softmax", 3)
+    assert ids.tolist() == [[2, -1, -1]] and w.tolist() == [[1.0, 0.0, 0.0]]
+
+
+def test_moe_oracle_is_the_layer_chain():
+    """Without the chain's own roundings the layer is the framework's exact five-stage layer."""
+    g = np.random.default_rng(2)
+    T, topk, E, H, I = 3, 2, 4, 128, 128
+    gu = [random_weights(g, "int4_g128", 2 * I, H) for _ in range(E)]
+    dn = [random_weights(g, "int4_g128", H, I) for _ in range(E)]
+    x = synth.normal_bf16(g, (T, H))
+    ids = np.array([[0, 3], [1, -1], [2, 2]], np.int32)
+    w = g.random((T, topk)).astype(np.float32)
+    got = oracle.ref_moe_decode(x, ids, w, lambda e: dequant(gu[e], "int4_g128"), lambda e: dequant(dn[e], "int4_g128"))
+    xf = oracle.decode_bf16(x)
+    for t in range(T):
+        want = np.zeros(H)
+        for j in range(topk):
+            if ids[t, j] < 0:
+                continue
+            y = dequant(gu[ids[t, j]], "int4_g128") @ xf[t]
+            a = y[:I] / (1 + np.exp(-y[:I])) * y[I:]
+            want += float(w[t, j]) * (dequant(dn[ids[t, j]], "int4_g128") @ a)
+        # the one rounding between: half a step of 2^-8 relative per activation
+        assert np.linalg.norm(got[t] - want) <= 2.0 ** -8 * np.linalg.norm(want) * 4
+    assert np.allclose(oracle.ref_gemv(x, dequant(gu[0], "int4_g128"), False), xf @ dequant(gu[0], "int4_g128").T)
+
+
+def test_int4_groups_oracle_matches_the_128_group_one():
+    g = np.random.default_rng(3)
+    for fmt in ("int4_g128", "uint4_g128"):
+        w = random_weights(g, fmt, 16, 256)
+        assert np.array_equal(dequant(w, fmt), oracle.dequant_wna16(w["wq"], w["scales"], w["zeros"], 128))
+    w = random_weights(g, "uint4_g32", 16, 128)
+    v = dequant(w, "uint4_g32")
+    code = lambda n, k: (int(w["wq"][n, k // 2]) >> (4 * (k % 2))) & 15  # noqa: E731
+    for n, k in ((0, 0), (3, 31), (3, 32), (15, 127)):
+        s = oracle.decode_bf16(w["scales"][n, k // 32:k // 32 + 1])[0]
+        assert v[n, k] == (code(n, k) - int(w["zeros"][n, k // 32])) * s
+
+
+# ---- prepack ----------------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt", [f for f in FORMATS if f.endswith(("128", "mxfp4", "int8", "fp8"))])
+def test_prepack_of_shared_formats_is_the_ordinary_one(fmt):
+    desc = FORMATS[fmt][0]
+    g = np.random.default_rng(4)
+    w = [random_weights(g, fmt, 48, 256) for _ in range(2)]
+    out = np.zeros(hq.hq_prepacked_bytes(desc, 2, 48, 256), np.uint8)
+    z = None if w[0]["zeros"] is None else np.stack([e["zeros"] for e in w])
+    hq.hq_prepack_weights(desc, 2, 48, 256, np.stack([e["wq"] for e in w]), np.stack([e["scales"] for e in w]), z, out)
+    assert np.array_equal(prepack_host(desc, w, 48, 256), out)
+
+
+@pytest.mark.parametrize("fmt", ["int4_g32", "uint4_g32", "int4_g64", "uint4_g64"])
+@pytest.mark.parametrize("E,N,K", [(1, 16, 128), (3, 48, 384)])
+def test_fine_layout_round_trip(fmt, E, N, K):
+    """Codes, scales and zeros read back from the documented positions of the layout."""
+    desc, G, asym = FORMATS[fmt]
+    g = np.random.default_rng(5)
+    ws = [random_weights(g, fmt, N, K) for _ in range(E)]
+    packed = prepack_host(desc, ws, N, K).reshape(E, -1)
+    units, per = K // 128, 128 // G
+    meta = 16 * per * 2 + (16 * per // 2 if asym else 0)
+    align = lambda v: (v + 255) // 256 * 256  # noqa: E731
+    m0 = align(N // 16 * units * 1024)
+    assert packed.shape[1] == m0 + align(N // 16 * units * meta)
+    for e, w in enumerate(ws):
+        codes = np.zeros((N, K), np.uint8)
+        for nt in range(N // 16):
+            for kt in range(units):
+                unit = packed[e, (nt * units + kt) * 1024:][:1024].view(np.uint32).reshape(64, 4)
+                for l in range(64):
+                    for d in range(4):
+                        for p in range(8):
+                            k = 128 * kt + 32 * d + 8 * (l >> 4) + 2 * (p & 3) + (p >> 2)
+                            codes[16 * nt + (l & 15), k] = (int(unit[l, d]) >> (4 * p)) & 15
+                m = packed[e, m0 + (nt * units + kt) * meta:][:meta]
+                s = m[:32 * per].view(np.uint16).reshape(16, per)
+                assert np.array_equal(s, w["scales"][16 * nt:16 * nt + 16, kt * per:(kt + 1) * per])
+                if asym:
+                    z = m[32 * per:].reshape(16, per // 2)
+                    z = np.stack([z & 15, z >> 4], -1).reshape(16, per)
+                    assert np.array_equal(z, w["zeros"][16 * nt:16 * nt + 16, kt * per:(kt + 1) * per])
+        want = oracle.unpack_nibbles(w["wq"])
+        assert np.array_equal(codes, want if asym else want ^ 8)
+
+
+# ---- refusals ---------------------------------------------------------------------------------
+def _status(f, *a, **k):
+    with pytest.raises(hq.HQError) as ei:
+        f(*a, **k)
+    return ei.value.status
+
+
+def test_descriptions():
+    ok = hq.hq_decode_prepacked_bytes
+    for desc, *_ in FORMATS.values():
+        assert ok(desc, 1, 256, 512) > 0
+        assert ok(hq.with_flags(desc, hq.HQ_COMPUTE_BATCH_INVARIANT), 1, 256, 512) == 0
+        assert ok(desc, 1, 250, 512) == ok(desc, 1, 256, 448) == ok(desc, 0, 256, 512) == ok(desc, 1, 0, 512) == 0
+    mk = hq.make_desc
+    for bad in (mk(hq.HQ_W_INT4_SYM, 16, hq.HQ_SCALE_BF16, 0, hq.HQ_ACT_BF16),
+                mk(hq.HQ_W_INT4_SYM, 32, hq.HQ_SCALE_BF16, 1, hq.HQ_ACT_BF16),
+                mk(hq.HQ_W_UINT4_ASYM, 32, hq.HQ_SCALE_BF16, 0, hq.HQ_ACT_BF16),
+                mk(hq.HQ_W_INT4_SYM, 32, hq.HQ_SCALE_FP32, 0, hq.HQ_ACT_BF16),
+                mk(hq.HQ_W_FP4_E2M1, 64, hq.HQ_SCALE_E8M0, 0, hq.HQ_ACT_BF16),
+                hq.DESC_W2A16_ASYM, hq.DESC_W3A16_ASYM, hq.DESC_W8A8, hq.DESC_W8A8_I32, hq.DESC_W4A8_MXFP4,
+                hq.DESC_W4A4_MXFP4, hq.DESC_W4A8_MXFP8, hq.DESC_W8A8_FP8_BLOCK):
+        assert ok(bad, 1, 256, 512) == 0
+        assert _status(hq.hq_gemv, bad, 0, 1, 256, 512, 16, 16, 16, stream=0) == UNS
+        assert hq.hq_moe_decode_workspace_bytes(bad, 1, 8, 16, 256, 512) == 0
+    # the other calls still refuse the fine groups
+    assert hq.hq_prepacked_bytes(hq.DESC_W4A16_ASYM_G32, 1, 256, 512) == 0
+    assert _status(hq.hq_gemm, hq.DESC_W4A16_ASYM_G32, 4, 256, 512, 16, None, 16, 16, stream=0) == UNS
+
+
+def test_prepack_refusals():
+    g = np.random.default_rng(6)
+    w = random_weights(g, "uint4_g32", 32, 256)
+    out = np.zeros(hq.hq_decode_prepacked_bytes(hq.DESC_W4A16_ASYM_G32, 1, 32, 256), np.uint8)
+    a = (1, 32, 256, w["wq"], w["scales"])
+    assert _status(hq.hq_decode_prepack_weights, hq.DESC_W4A16_ASYM_G32, *a, None, out) == INV
+    assert _status(hq.hq_decode_prepack_weights, hq.DESC_W4A16_SYM_G32, *a, w["zeros"], out) == INV
+    assert _status(hq.hq_decode_prepack_weights, hq.DESC_W4A16_ASYM_G32, *a, w["zeros"], out[:-1]) == WSP
+    assert _status(hq.hq_decode_prepack_weights, hq.DESC_W4A16_ASYM_G32, 0, 32, 256, w["wq"], w["scales"], w["zeros"], out) == INV
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(op=2), INV), (dict(M=-1), INV), (dict(M=65537), INV), (dict(N=250), UNS), (dict(K=500), UNS), (dict(N=0), INV),
+    (dict(op=1, N=272), UNS), (dict(M=1024, N=1 << 22), UNS), (dict(x=None), INV), (dict(w=None), INV), (dict(y=None), INV),
+    (dict(x=8), INV), (dict(w=24), INV), (dict(y=8), INV), (dict(N=(1 << 24) + 16), UNS),
+])
+def test_gemv_refusals(change, status):
+    a = dict(op=0, M=4, N=256, K=512, x=16, w=16, y=16) | change
+    assert _status(hq.hq_gemv, G32, a["op"], a["M"], a["N"], a["K"], a["x"], a["w"], a["y"], stream=0) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(T=-1), INV), (dict(T=17), UNS), (dict(topk=0), INV), (dict(topk=65), INV), (dict(E=0), INV), (dict(E=513), INV),
+    (dict(H=200), UNS), (dict(I=64), UNS), (dict(I=0), INV), (dict(x=None), INV), (dict(ids=None), INV), (dict(gu=None), INV),
+    (dict(dn=None), INV), (dict(out=None), INV), (dict(x=8), INV), (dict(gu=8), INV), (dict(dn=8), INV), (dict(out=8), INV),
+    (dict(ids=18), INV), (dict(w=18), INV), (dict(ws=8), INV), (dict(ws=None), WSP), (dict(short=1), WSP),
+])
+def test_moe_decode_refusals(change, status):
+    a = dict(T=4, topk=8, E=16, H=256, I=512, x=16, ids=16, w=16, gu=16, dn=16, out=16, ws=16, short=0) | change
+    need = hq.hq_moe_decode_workspace_bytes(G32, 4, 8, 16, 256, 512)
+    assert need >= 4 * 8 * 512 * 2
+    assert _status(hq.hq_moe_decode, G32, a["T"], a["topk"], a["E"], a["H"], a["I"], a["x"], a["ids"], a["w"], a["gu"], a["dn"],
+                   a["out"], a["ws"], need - a["short"], stream=0) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(score=2), INV), (dict(fmt=2), INV), (dict(T=-1), INV), (dict(T=(1 << 24) + 1), INV), (dict(E=0), UNS), (dict(E=513), UNS),
+    (dict(groups=0), INV), (dict(groups=65), INV), (dict(groups=3), INV), (dict(keep=0), INV), (dict(keep=5), INV),
+    (dict(top=0), INV), (dict(top=3), INV), (dict(topk=0), INV), (dict(topk=65), INV), (dict(topk=33), INV),
+    (dict(scale=math.inf), INV), (dict(scale=math.nan), INV), (dict(logits=None), INV), (dict(ids=None), INV),
+    (dict(weights=None), INV), (dict(logits=8), INV), (dict(bias=18), INV), (dict(ids=18), INV), (dict(weights=18), INV),
+])
+def test_route_refusals(change, status):
+    a = dict(score=0, T=2, E=64, topk=8, logits=16, fmt=0, bias=None, groups=4, keep=2, top=2, scale=1.0, ids=16, weights=16) | change
+    assert _status(hq.hq_moe_route, a["score"], a["T"], a["E"], a["topk"], a["logits"], a["fmt"], a["bias"], a["groups"], a["keep"],
+                   a["top"], True, a["scale"], a["ids"], a["weights"], stream=0) == status
+
+
+def test_nothing_to_do():
+    hq.hq_gemv(G32, 0, 0, 256, 512, None, None, None, stream=0)
+    hq.hq_moe_decode(G32, 0, 8, 16, 256, 512, None, None, None, None, None, None, stream=0)
+    hq.hq_moe_route(0, 0, 64, 8, None, 0, None, 1, 1, 2, True, 1.0, None, None, stream=0)
+    assert hq.hq_moe_decode_workspace_bytes(G32, 0, 8, 16, 256, 512) == 0
+
+
+def test_buffers_are_checked():
+    """What only the binding can see: host tensors, views that are not contiguous, short buffers."""
+    x = torch.zeros((4, 512), dtype=torch.bfloat16)
+    assert _status(hq.hq_gemv, G32, 0, 4, 256, 512, x, 16, 16, stream=0) == INV                       # on the host
+    assert _status(hq.hq_gemv, G32, 0, 4, 256, 512, x.T, 16, 16, stream=0) == INV                     # not contiguous
+    assert _status(hq.hq_gemv, G32, 0, 5, 256, 512, x, 16, 16, stream=0) == INV                       # four rows, five asked
+    assert _status(hq.hq_moe_route, 0, 4, 512, 8, x, 0, None, 1, 1, 2, True, 1.0, 16, 16, stream=0) == INV   # bf16 held, fp32 asked
+    ws = torch.zeros(8, dtype=torch.uint8)
+    assert _status(hq.hq_moe_decode, G32, 1, 8, 16, 256, 512, 16, 16, None, 16, 16, 16, ws, 1 << 20, stream=0) == INV
