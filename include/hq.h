@@ -474,7 +474,7 @@ typedef enum {
  * Matrix-vector products with packed weights (device): x [M, K] bf16 row-major, w_packed one
  * layer's weights of N rows (E = 1), y bf16 [M, N] (or [M, N/2], see op). fp32 accumulation, one
  * rounding at the end (silu(g) * u never passes through bf16). Made for M of 1 to 16; more rows run
- * in blocks of 16 that each read the weights again. M <= 65536, N <= 2^24, M * N < 2^31.
+ * in blocks of 16 that each read the weights again. M <= 65536, N and K <= 2^24, M * N < 2^31.
  * x, w_packed and y 16-byte aligned; y must not overlap x. M == 0 is a no-op. No workspace.
  * ------------------------------------------------------------------------------------------- */
 hq_status hq_gemv(const hq_quant_desc* desc, int32_t op, int64_t M, int64_t N, int64_t K, const void* x,
@@ -483,9 +483,10 @@ hq_status hq_gemv(const hq_quant_desc* desc, int32_t op, int64_t M, int64_t N, i
 /* ---------------------------------------------------------------------------------------------
  * The MoE layer for a few tokens (device), what the calls hq_moe_align .. hq_moe_combine compute in
  * five launches, in two:
- *   act[t, j] = bf16( silu(g) * u ),  (g, u) = x[t] . dequant(Wgu_e)^T in fp32,  e = topk_ids[t, j]
+ *   act[t, j] = silu(g) * u,  (g, u) = x[t] . dequant(Wgu_e)^T in fp32,  e = topk_ids[t, j]
  *   out[t]    = bf16( sum_j topk_weights[t, j] * (act[t, j] . dequant(Wd_e)^T) ),  fp32 sums
- * Only act and out are rounded (the five calls also round gate_up and each expert's output).
+ * act is kept to 16 significant bits (a high and a low bf16), out is rounded once; the five calls round
+ * gate_up, act and each expert's output to bf16 on the way.
  * Entries whose id is outside [0, E) contribute nothing; a token with none left gets zeros. The same
  * expert may stand in a token's row more than once.
  *   x             bf16 [T, H], out bf16 [T, H] (out may be x)
@@ -496,7 +497,7 @@ hq_status hq_gemv(const hq_quant_desc* desc, int32_t op, int64_t M, int64_t N, i
  *                 may run at the same time (other streams, replays of captured graphs) each need
  *                 their own.
  * T 1..HQ_MOE_DECODE_MAX_TOKENS (more: HQ_ERR_UNSUPPORTED; use the grouped GEMMs), topk 1..64,
- * E 1..512, H and I multiples of 128. Pointers 16-byte aligned (ids and weights 4). T == 0 is a no-op.
+ * E 1..512, H and I multiples of 128, T * topk * I < 2^29. Pointers 16-byte aligned (ids and weights 4). T == 0 is a no-op.
  * The result does not depend on the order in which workgroups run.
  * ------------------------------------------------------------------------------------------- */
 #define HQ_MOE_DECODE_MAX_TOKENS 16

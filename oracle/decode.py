@@ -10,7 +10,7 @@ import math
 
 import numpy as np
 
-from .codecs import decode_bf16, decode_int4_sym, decode_uint4, round_to_bf16, unpack_nibbles
+from .codecs import decode_bf16, decode_int4_sym, decode_uint4, unpack_nibbles
 
 
 
@@ -76,7 +76,7 @@ def _silu(g: np.ndarray) -> np.ndarray:
 def ref_moe_decode(x_bits: np.ndarray, ids: np.ndarray, weights, gate_up, down) -> np.ndarray:
     """x bf16 bits [T, H], ids [T, topk], weights [T, topk] or None, gate_up(e) / down(e): fp64 weights
     of expert e ([2I, H] / [H, I]), E experts = len of the id range the caller allows (ids outside are
-    given as -1) -> unrounded fp64 [T, H]. The activations between the products are rounded to bf16."""
+    given as -1) -> unrounded fp64 [T, H]."""
     T, topk = ids.shape
     x = decode_bf16(x_bits)
     out = np.zeros(x.shape)
@@ -84,8 +84,7 @@ def ref_moe_decode(x_bits: np.ndarray, ids: np.ndarray, weights, gate_up, down) 
         rows = [t for t in range(T) if e in ids[t]]
         gu = x[rows] @ gate_up(e).T
         n = gu.shape[1] // 2
-        act = decode_bf16(round_to_bf16(_silu(gu[:, :n]) * gu[:, n:]))
-        y = act @ down(e).T
+        y = (_silu(gu[:, :n]) * gu[:, n:]) @ down(e).T
         for i, t in enumerate(rows):
             for j in range(topk):
                 if ids[t, j] == e:

@@ -608,8 +608,9 @@ hq_status hq_gemv(const hq_quant_desc* desc, int32_t op, int64_t M, int64_t N, i
   if (op == HQ_GEMV_SILU_MUL && N % 32 != 0)
     return fail(HQ_ERR_UNSUPPORTED, "HQ_GEMV_SILU_MUL needs N %% 32 == 0 (N=%lld)", (long long)N);
   if (M < 0 || M > 65536) return fail(HQ_ERR_INVALID_ARGUMENT, "M=%lld out of range", (long long)M);
-  if (N > (int64_t(1) << 24) || M * N >= (int64_t(1) << 31))
-    return fail(HQ_ERR_UNSUPPORTED, "N must be at most 2^24 and M*N below 2^31 (M=%lld N=%lld)", (long long)M, (long long)N);
+  if (N > (int64_t(1) << 24) || K > (int64_t(1) << 24) || M * N >= (int64_t(1) << 31))
+    return fail(HQ_ERR_UNSUPPORTED, "N and K must be at most 2^24 and M*N below 2^31 (M=%lld N=%lld K=%lld)", (long long)M,
+                (long long)N, (long long)K);
   if (M == 0) return ok();
   if (!x || !w_packed || !y) return fail(HQ_ERR_INVALID_ARGUMENT, "x, w_packed and y must be non-NULL");
   if (!aligned16(x) || !aligned16(w_packed) || !aligned16(y))
@@ -642,6 +643,8 @@ hq_status check_moe_decode(const hq_quant_desc* desc, int64_t T, int32_t topk, i
     return fail(HQ_ERR_INVALID_ARGUMENT, "H=%lld I=%lld out of range", (long long)H, (long long)I);
   if (H % 128 != 0 || I % 128 != 0)
     return fail(HQ_ERR_UNSUPPORTED, "H and I must be multiples of 128 (H=%lld I=%lld)", (long long)H, (long long)I);
+  if (T * topk * I >= (int64_t(1) << 29))   // the activations' 32-bit offsets
+    return fail(HQ_ERR_UNSUPPORTED, "T*topk*I must stay below 2^29 (T=%lld topk=%d I=%lld)", (long long)T, topk, (long long)I);
   return HQ_OK;
 }
 }  // namespace

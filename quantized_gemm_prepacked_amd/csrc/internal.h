@@ -114,6 +114,9 @@ struct GemvCall {
   void* y;
 };
 hipError_t launch_gemv(const GemvCall& g, hipStream_t s);
+struct DecW;
+DecW dec_weights(const Combo& c, const uint8_t* w, int64_t N, int64_t K);
+int dec_format(const Combo& c);
 struct MoeDecodeCall {
   Combo c;
   int T, topk, E;

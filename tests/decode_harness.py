@@ -63,13 +63,13 @@ def magnitude(w: dict, fmt: str) -> np.ndarray:
     return np.abs(dequant(w, fmt))
 
 
-def product_bound(x_bits: np.ndarray, w: dict, fmt: str) -> np.ndarray:
-    """fp32 error of x . w^T before its rounding to bf16. Every partial sum is at most A = sum_k |x_k|
+def product_bound(x: np.ndarray, w: dict, fmt: str) -> np.ndarray:
+    """fp32 error of x . w^T (x: bf16 bits or fp64 values) before its rounding to bf16. Every partial sum is at most A = sum_k |x_k|
     |w_k|'s accumulated size; a product passes through at most 128 additions inside its scale group's
     matrix instructions, K/128 over the units, 16 waves, and 8 more for scaling, channel scales and
     router weights, each off by 2^-24 relative (2^-23 here: a matrix instruction may truncate)."""
-    K = x_bits.shape[1]
-    a = np.abs(oracle.decode_bf16(x_bits)) @ magnitude(w, fmt).T
+    K = x.shape[1]
+    a = np.abs(oracle.decode_bf16(x) if x.dtype == np.uint16 else x) @ magnitude(w, fmt).T
     return 2.0 ** -23 * (128 + K // 128 + 16 + 8) * a
 
 

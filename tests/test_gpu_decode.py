@@ -252,10 +252,10 @@ class Layer:
         return oracle.ref_moe_decode(x_bits, ok, weights, lambda e: dequant(self.gu[e], self.fmt), lambda e: dequant(self.dn[e], self.fmt))
 
     def bound(self, x_bits, ids, weights):
-        """The down product's fp32 bound on the exact activations, summed over the experts, and what an
-        activation that is rounded the other way (its fp32 value within a bound of a tie) moves: a whole
-        bf16 step, 2^-7 relative, of the activations where that can be."""
-        x = x_bits
+        """Before the output's rounding: the down product's fp32 bound on the exact activations, and what
+        the activations' own errors move -- their fp32 bound, and 2^-16 of each (a high and a low bf16: the
+        low one is at most 2^-8 of the value and off by half a step, 2^-8, of itself; below bf16's range the
+        low half is off by 2^-134) -- summed over the experts with their weights."""
         T, topk = ids.shape
         total = np.zeros((T, self.H))
         for t in range(T):
@@ -264,15 +264,11 @@ class Layer:
                 if not 0 <= e < self.E:
                     continue
                 wt = 1.0 if weights is None else abs(float(weights[t, j]))
-                xr = x[t:t + 1]
+                xr = x_bits[t:t + 1]
                 a64 = oracle.ref_gemv(xr, dequant(self.gu[e], self.fmt), True)
-                da = _gated_bound(xr, self.gu[e], self.fmt, 2 * self.I)
-                ab = oracle.round_to_bf16(a64)
-                half = np.ldexp(1.0, np.frexp(np.maximum(np.abs(a64), 2.0 ** -126))[1] - 9)   # half a step at a64
-                flips = np.abs(oracle.decode_bf16(ab) - a64) + da >= half
-                moved = np.where(flips, 2.0 ** -7 * np.abs(a64) + da, 0.0)
+                moved = _gated_bound(xr, self.gu[e], self.fmt, 2 * self.I) + 2.0 ** -16 * np.abs(a64) + 2.0 ** -134
                 d = np.abs(dequant(self.dn[e], self.fmt))
-                total[t] += wt * (product_bound(ab, self.dn[e], self.fmt)[0] + (moved @ d.T)[0])
+                total[t] += wt * (product_bound(a64, self.dn[e], self.fmt)[0] + (moved @ d.T)[0])
         return total + 2.0 ** -22 * topk * np.abs(total)
 
 
