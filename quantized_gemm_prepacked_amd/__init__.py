@@ -173,8 +173,8 @@ def _ptr(x):
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without building a Stream object (0.3 us against 2.8)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -298,18 +298,24 @@ def hq_moe_combine(T, topk, E, N, topk_ids, y, out, stream=None):
 
 
 # ---- decode step ------------------------------------------------------------------------------
-def _buf(x, nbytes, what):
-    """Device address of a decode call's buffer. A tensor has to be contiguous, on the current device
-    and hold nbytes (None: not checked): what the C side cannot see, and would read past."""
-    if x is None or isinstance(x, int):
-        return x
-    if not x.is_contiguous():
-        raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} must be contiguous")
-    if nbytes is not None and x.nbytes < nbytes:
-        raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} holds {x.nbytes} bytes, {nbytes} are needed")
-    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
-        raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} must be on the current device")
-    return x.data_ptr()
+def _bufs(*wanted):
+    """Device addresses of a decode call's buffers, given as (tensor, bytes needed, name) each. A tensor has
+    to be contiguous, on the current device and as large as the call reads or writes: what the C side
+    cannot see, and would go past. Addresses (int) and None pass through."""
+    out, dev = [], -2
+    for x, nbytes, what in wanted:
+        if x is not None and x.__class__ is not int:
+            if dev == -2 and x.is_cuda:
+                dev = torch.cuda.current_device()
+            if not x.is_contiguous():
+                raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} must be contiguous")
+            if x.nbytes < nbytes:
+                raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} holds {x.nbytes} bytes, {nbytes} are needed")
+            if not x.is_cuda or x.get_device() != dev:
+                raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} must be on the current device")
+            x = x.data_ptr()
+        out.append(x)
+    return out
 
 
 def hq_decode_prepacked_bytes(desc, E, N, K) -> int:
@@ -327,16 +333,16 @@ def hq_decode_prepack_weights(desc, E, N, K, wq: np.ndarray, scales: np.ndarray,
 
 def hq_moe_route(score_fn, T, E, topk, logits, logits_fmt, bias, n_group, topk_group, group_top, renormalize, scale,
                  topk_ids, topk_weights, stream=None):
-    _check(_c["hq_moe_route"](score_fn, T, E, topk, _buf(logits, T * E * (2 if logits_fmt == HQ_LOGITS_BF16 else 4), "logits"),
-                              logits_fmt, _buf(bias, 4 * E, "bias"), n_group, topk_group, group_top, int(renormalize), scale,
-                              _buf(topk_ids, 4 * T * topk, "topk_ids"), _buf(topk_weights, 4 * T * topk, "topk_weights"),
-                              _stream(stream)))
+    l, b, ids, w = _bufs((logits, T * E * (2 if logits_fmt == HQ_LOGITS_BF16 else 4), "logits"), (bias, 4 * E, "bias"),
+                         (topk_ids, 4 * T * topk, "topk_ids"), (topk_weights, 4 * T * topk, "topk_weights"))
+    _check(_c["hq_moe_route"](score_fn, T, E, topk, l, logits_fmt, b, n_group, topk_group, group_top, int(renormalize), scale,
+                              ids, w, _stream(stream)))
 
 
 def hq_gemv(desc, op, M, N, K, x, w_packed, y, stream=None):
-    outs = N // 2 if op == HQ_GEMV_SILU_MUL else N
-    _check(_c["hq_gemv"](_d(desc), op, M, N, K, _buf(x, 2 * M * K, "x"), _buf(w_packed, None, "w_packed"),
-                         _buf(y, 2 * M * outs, "y"), _stream(stream)))
+    """The packed weights' size is the descriptor's (hq_decode_prepacked_bytes(desc, 1, N, K))."""
+    a, w, o = _bufs((x, 2 * M * K, "x"), (w_packed, 0, "w_packed"), (y, 2 * M * (N // 2 if op == HQ_GEMV_SILU_MUL else N), "y"))
+    _check(_c["hq_gemv"](_d(desc), op, M, N, K, a, w, o, _stream(stream)))
 
 
 def hq_moe_decode_workspace_bytes(desc, T, topk, E, H, I) -> int:
@@ -345,7 +351,7 @@ def hq_moe_decode_workspace_bytes(desc, T, topk, E, H, I) -> int:
 
 def hq_moe_decode(desc, T, topk, E, H, I, x, topk_ids, topk_weights, w_gate_up, w_down, out, ws=None, ws_bytes=0,
                   stream=None):
-    _check(_c["hq_moe_decode"](_d(desc), T, topk, E, H, I, _buf(x, 2 * T * H, "x"), _buf(topk_ids, 4 * T * topk, "topk_ids"),
-                               _buf(topk_weights, 4 * T * topk, "topk_weights"), _buf(w_gate_up, None, "w_gate_up"),
-                               _buf(w_down, None, "w_down"), _buf(out, 2 * T * H, "out"), _buf(ws, ws_bytes, "ws"), ws_bytes,
-                               _stream(stream)))
+    a, ids, w, gu, dn, o, s = _bufs((x, 2 * T * H, "x"), (topk_ids, 4 * T * topk, "topk_ids"),
+                                    (topk_weights, 4 * T * topk, "topk_weights"), (w_gate_up, 0, "w_gate_up"),
+                                    (w_down, 0, "w_down"), (out, 2 * T * H, "out"), (ws, ws_bytes, "ws"))
+    _check(_c["hq_moe_decode"](_d(desc), T, topk, E, H, I, a, ids, w, gu, dn, o, s, ws_bytes, _stream(stream)))

@@ -43,12 +43,13 @@ __global__ __launch_bounds__(NW * 64) void gemv_kernel(GemvParams p) {
   for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int n = p.W.units > wave ? (p.W.units - wave + NW - 1) / NW : 0;
   dec_stream<F, AM, NT, D>(
-      n, dec_rsrc(p.x + size_t(row0) * p.K, uint32_t(min(AM, p.M - row0)) * p.K * 2), smem + wave * dec_wave_lds<AM, D>(), lane, acc, [&](int, int t) __attribute__((always_inline)) { return tiles[t]; },
-      [&](int i) __attribute__((always_inline)) { return wave + i * NW; },
+      n, dec_rsrc(p.x + size_t(row0) * p.K, uint32_t(min(AM, p.M - row0)) * p.K * 2), smem + wave * dec_wave_lds<AM, D>(), lane, acc, [](int) __attribute__((always_inline)) {},
+      [&](int t) __attribute__((always_inline)) { return tiles[t]; },
+      [&](int i, int) __attribute__((always_inline)) { return wave + i * NW; },
       [&](int i, int r) __attribute__((always_inline)) {
         return uint32_t(min(r, p.M - 1 - row0)) * (p.K * 2) + uint32_t(wave + i * NW) * 256;
       },
-      [](int) __attribute__((always_inline)) {}, [](int) __attribute__((always_inline)) {});
+      [](int) __attribute__((always_inline)) {});
 
   float(*red)[NT][E][64] = reinterpret_cast<float(*)[NT][E][64]>(smem);
   __syncthreads();   // every wave is done with its activations

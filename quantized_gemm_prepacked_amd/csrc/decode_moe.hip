@@ -177,14 +177,14 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeParams p) {
     for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     dec_stream<F, AM, NT, D>(
         n, rows, smem + wave * dec_wave_lds<AM, D>(), lane, acc,
-        [&](int, int t) __attribute__((always_inline)) { return tiles[t]; },
-        [&](int i) __attribute__((always_inline)) { return wave + i * NW; },
+        [](int) __attribute__((always_inline)) {}, [&](int t) __attribute__((always_inline)) { return tiles[t]; },
+        [&](int i, int) __attribute__((always_inline)) { return wave + i * NW; },
         [&](int i, int r) __attribute__((always_inline)) {
           int t = tok[0];
           if constexpr (AM == 4) t = r == 0 ? tok[0] : r == 1 ? tok[1] : r == 2 ? tok[2] : tok[3];
           return uint32_t(t) * (p.K * 2) + uint32_t(wave + i * NW) * 256;
         },
-        [](int) __attribute__((always_inline)) {}, [](int) __attribute__((always_inline)) {});
+        [](int) __attribute__((always_inline)) {});
 
     float(*red)[NT][64] = reinterpret_cast<float(*)[NT][64]>(smem);
     __syncthreads();   // every wave is done with its activations
@@ -221,25 +221,14 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeParams p) {
   }
 }
 
-// Walks a wave's items (pass, unit) in order: at(i) for i = i0, i0, ..., rising by at most one a call.
-struct PassCursor {
-  int i, d, u, units;
-  __device__ __forceinline__ void at(int to) {
-    if (to > i) {
-      i = to;
-      if (++u == units) {
-        u = 0;
-        ++d;
-      }
-    }
-  }
-};
-
 // NT tiles of 16 outputs per workgroup; the items (pass, K unit) are cut into NW equal contiguous
-// ranges. AM = 2: one token, passes = its valid entries. AM = 8: passes of up to four tokens, sums per
+// ranges, one per wave. What a wave needs of an item -- its expert's address, its unit and pass, its
+// activation rows -- is worked out 64 items at a time, one per lane, and read back by lane: done item
+// by item on the scalar unit, which a CU's waves share, it took as long as the stream itself. AM = 2: one token, passes = its valid entries. AM = 8: passes of up to four tokens, sums per
 // token in LDS (one wave's, so the order is the passes').
 template <int F, int AM, int NT, int NW, int D>
 __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeParams p) {
+  constexpr int RS = AM == 8 ? kSlots : 1;   // act rows of an item
   extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int P = p.T * p.topk;
@@ -267,8 +256,8 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeParams p) {
   __syncthreads();
 
   const int out_tiles = p.N / 16, ot0 = blockIdx.x * NT, units = p.W.units;
-  const int64_t items = int64_t(count) * units;
-  const int q0 = int(items * wave / NW), n = int(items * (wave + 1) / NW) - q0;
+  const int items = count * units;
+  const int q0 = int(int64_t(items) * wave / NW), q1 = int(int64_t(items) * (wave + 1) / NW);
   f32x4 acc[NT];
   float total[NT];
 #pragma unroll
@@ -276,63 +265,59 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeParams p) {
     acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     total[t] = 0.f;
   }
-  const int d0 = q0 / units, u0 = q0 - d0 * units;
-  PassCursor load{0, d0, u0, units}, done{0, d0, u0, units};
-  PassCursor block{0, d0, u0, units};   // the first item of the block of rows being copied
-  auto expert = [&](int d) __attribute__((always_inline)) {
-    return p.W.w + size_t(__builtin_amdgcn_readfirstlane(passes[d].e)) * p.W.expert_stride;
-  };
-  int tile_d = -1;
-  const uint8_t* tile_w = nullptr;
-  dec_stream<F, AM, NT, D>(
-      n, dec_rsrc(p.x, uint32_t(P) * p.K * 4), rows_lds + wave * dec_wave_lds<AM, D>(), lane, acc,
-      [&](int i, int t) __attribute__((always_inline)) {
-        load.at(i);
-        if (load.d != tile_d) {
-          tile_d = load.d;
-          tile_w = expert(tile_d);
-        }
-        return dec_tile<F>(p.W, tile_w, min(ot0 + t, out_tiles - 1));
-      },
-      [&](int i) __attribute__((always_inline)) {
-        load.at(i);
-        return load.u;
-      },
-      [&](int i, int r) __attribute__((always_inline)) {
-        int d = block.d, u = block.u + (i - block.i);
+  const int tiles = min(NT, out_tiles - ot0);
+  const rsrc_t rows = dec_rsrc(p.x, uint32_t(P) * p.K * 4);
+  uint32_t* row_at = reinterpret_cast<uint32_t*>(sums + NW * NT * p.T * 16) + wave * (64 * RS);
+  for (int q = q0; q < q1; q += 64) {
+    const int n = min(64, q1 - q);
+    // lane i: item q + i
+    const int qi = min(q + lane, q1 - 1);
+    const int d = qi / units, u = qi - d * units;
+    const uint64_t w_at = reinterpret_cast<uint64_t>(p.W.w) + uint64_t(passes[d].e) * p.W.expert_stride;
+    const int w_lo = int(w_at), w_hi = int(w_at >> 32);
+    const bool last = u == units - 1 || qi == q1 - 1;   // of this wave's units of the pass
+    const int du = int(uint32_t(d) << 1 | uint32_t(last));
 #pragma unroll
-        for (int j = 1; j < D; ++j)
-          if (u >= units) {
-            u -= units;
-            ++d;
-          }
-        const int entry = passes[d].entry[AM == 8 ? r >> 1 : 0];
-        return uint32_t(entry * 2 + (r & 1)) * (p.K * 2) + uint32_t(u) * 256;
-      },
-      [&](int i) __attribute__((always_inline)) {
-        while (block.i < i) block.at(block.i + 1);
-      },
-      [&](int i) __attribute__((always_inline)) {
-        done.at(i);
-        if (done.u == units - 1 || i == n - 1) {
-          const Pass& s = passes[done.d];
-          const int g = AM == 8 ? lane >> 4 : 0;
-          const uint8_t* w = expert(done.d);
+    for (int g = 0; g < RS; ++g) row_at[lane * RS + g] = uint32_t(passes[d].entry[g]) * (p.K * 4) + uint32_t(u) * 256;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // written by this wave, read by this wave
+
+    DecTile<F> tile;
+    int at = 0;
+    dec_stream<F, AM, NT, D>(
+        n, rows, rows_lds + wave * dec_wave_lds<AM, D>(), lane, acc,
+        [&](int i) __attribute__((always_inline)) {
+          const uint64_t lo = uint32_t(__builtin_amdgcn_readlane(w_lo, i)), hi = uint32_t(__builtin_amdgcn_readlane(w_hi, i));
+          tile = dec_tile<F>(p.W, reinterpret_cast<const uint8_t*>(hi << 32 | lo), ot0, tiles);
+          at = __builtin_amdgcn_readlane(u, i);
+        },
+        [&](int) __attribute__((always_inline)) { return tile; },
+        // a tile past the last one lies outside the buffers
+        [&](int, int t) __attribute__((always_inline)) { return at + t * units; },
+        [&](int i, int r) __attribute__((always_inline)) { return row_at[i * RS + (AM == 8 ? r >> 1 : 0)] + (r & 1) * (p.K * 2); },
+        [&](int i) __attribute__((always_inline)) {
+          const int s = __builtin_amdgcn_readlane(du, i);
+          if (s & 1) {
+            const Pass& pass = passes[s >> 1];
+            const int g = AM == 8 ? lane >> 4 : 0;
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            float v = dec_value<F, AM>(acc[t], 0) * s.weight[g];
-            const int c = min(ot0 + t, out_tiles - 1) * 16 + (lane & 15);
-            if constexpr (DecTraits<F>::kW8) v *= reinterpret_cast<const float*>(w + p.W.scales_off)[c];
-            if constexpr (AM == 8) {
-              const int tok = s.token[g];
-              if (tok >= 0) sums[((wave * NT + t) * p.T + tok) * 16 + (lane & 15)] += v;
-            } else {
-              total[t] += v;
+            for (int t = 0; t < NT; ++t) {
+              float v = dec_value<F, AM>(acc[t], 0) * pass.weight[g];
+              if constexpr (DecTraits<F>::kW8) {
+                const int c = min(ot0 + t, out_tiles - 1) * 16 + (lane & 15);
+                const uint8_t* w = p.W.w + size_t(__builtin_amdgcn_readfirstlane(pass.e)) * p.W.expert_stride;
+                v *= reinterpret_cast<const float*>(w + p.W.scales_off)[c];
+              }
+              if constexpr (AM == 8) {
+                const int tok = pass.token[g];
+                if (tok >= 0) sums[((wave * NT + t) * p.T + tok) * 16 + (lane & 15)] += v;
+              } else {
+                total[t] += v;
+              }
+              acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
-            acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
           }
-        }
-      });
+        });
+  }
 
   if constexpr (AM == 2) {
     float(*red)[NT][16] = reinterpret_cast<float(*)[NT][16]>(sums);
@@ -376,9 +361,10 @@ hipError_t launch_up(const MoeParams& p, hipStream_t s) {
 template <int F, int AM, int NT, int NW, int D>
 hipError_t launch_down(const MoeParams& p, hipStream_t s) {
   const int P = p.T * p.topk;
+  constexpr int rows = NW * (dec_wave_lds<AM, D>() + 64 * (AM == 8 ? kSlots : 1) * 4);
   // at most 1024 passes: 64 KiB of the 160
-  static_assert(1024 * sizeof(Pass) + NW * dec_wave_lds<AM, D>() + NW * NT * (AM == 2 ? 1 : HQ_MOE_DECODE_MAX_TOKENS) * 64 <= 160 * 1024, "LDS");
-  const int lds = P * int(sizeof(Pass)) + NW * dec_wave_lds<AM, D>() + NW * NT * p.T * 64;
+  static_assert(1024 * sizeof(Pass) + rows + NW * NT * (AM == 2 ? 1 : HQ_MOE_DECODE_MAX_TOKENS) * 64 <= 160 * 1024, "LDS");
+  const int lds = P * int(sizeof(Pass)) + rows + NW * NT * p.T * 64;
   const int tiles = p.N / 16;
   return launch(moe_down_kernel<F, AM, NT, NW, D>, dim3(unsigned((tiles + NT - 1) / NT)), NW * 64, lds, s, p);
 }

@@ -24,6 +24,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device_ops.h"
 #include "layout.h"
 
@@ -90,19 +92,22 @@ __device__ __forceinline__ void dec_lds_copy(rsrc_t r, uint32_t at, uint8_t* lds
 constexpr uint32_t kDecOutside = 0x7FFFFFFFu;   // past every resource here (they stay below 2^31 bytes)
 constexpr int kNT = 2;                          // cache hint: streamed once
 
-// One tile's buffers: codes and scales (fine groups: scales and zeros), zeros.
+// One tile's buffers: codes and scales (fine groups: scales and zeros), zeros. Neighbouring tiles of
+// one expert may share them.
 template <int F>
 struct DecTile {
   rsrc_t codes, scales, zeros;
 };
 
+// Buffers over `tiles` tiles from tile nt on of the expert at w.
 template <int F>
-__device__ __forceinline__ DecTile<F> dec_tile(const DecW& W, const uint8_t* w, int64_t nt) {
+__device__ __forceinline__ DecTile<F> dec_tile(const DecW& W, const uint8_t* w, int nt, int tiles = 1) {
   using T = DecTraits<F>;
   DecTile<F> t;
-  t.codes = dec_rsrc(w + size_t(nt) * W.units * T::kUnit, uint32_t(W.units) * T::kUnit);
-  if constexpr (!T::kW8) t.scales = dec_rsrc(w + W.scales_off + size_t(nt) * W.units * T::kScaleStep, uint32_t(W.units) * T::kScaleStep);
-  if constexpr (F == DF_G128Z) t.zeros = dec_rsrc(w + W.zeros_off + size_t(nt) * W.units * 8, uint32_t(W.units) * 8);
+  const size_t at = size_t(nt) * W.units;
+  t.codes = dec_rsrc(w + at * T::kUnit, uint32_t(tiles) * W.units * T::kUnit);
+  if constexpr (!T::kW8) t.scales = dec_rsrc(w + W.scales_off + at * T::kScaleStep, uint32_t(tiles) * W.units * T::kScaleStep);
+  if constexpr (F == DF_G128Z) t.zeros = dec_rsrc(w + W.zeros_off + at * 8, uint32_t(tiles) * W.units * 8);
   return t;
 }
 
@@ -114,7 +119,7 @@ struct DecUnit {
   uint32_t z;
 };
 
-// Load unit u of a tile (live false: nothing is read).
+// Load unit u of a tile, counted from its buffers' start (live false: nothing is read).
 template <int F>
 __device__ __forceinline__ void dec_load(DecUnit<F>& v, const DecTile<F>& t, int u, bool live, int lane) {
   using T = DecTraits<F>;
@@ -213,43 +218,44 @@ __device__ __forceinline__ void dec_row_sums(const u32x4 (&af)[4], float (&rs)[D
   }
 }
 
-// LDS bytes of a wave's activations: two blocks of D units.
+// A block's activations, D units of AM rows, in whole copies of four 256-byte rows; a wave's LDS: two blocks.
 template <int AM, int D>
-constexpr int dec_wave_lds() { return 2 * D * AM * 256; }
+constexpr int dec_copies() { return (D * AM + 3) / 4; }
+template <int AM, int D>
+constexpr int dec_wave_lds() { return 2 * dec_copies<AM, D>() * 1024; }
 
 // The wave's loop over n items. An item is a unit of the wave's NT tiles:
-//   tile(i, t)  the DecTile of tile t of item i          (wave-uniform)
-//   unit(i)     its unit index                           (wave-uniform)
+//   item(i)     called before item i is loaded
+//   tile(t)     the DecTile of its tile t                      (wave-uniform)
+//   unit(i, t)  its unit, counted from that tile's buffers' start (wave-uniform)
 //   row(i, r)   byte offset in `rows` of LDS row r's first k of the item (any lane's r)
-//   block(i)    called before the rows of the block that starts at item i are asked for
 //   done(i)     called after item i's products were added
 // Items past the last are asked for with i clamped to n - 1.
-template <int F, int AM, int NT, int D, class Tile, class Unit, class Row, class Block, class Done>
-__device__ __forceinline__ void dec_stream(int n, rsrc_t rows, uint8_t* lds, int lane, f32x4 (&acc)[NT], Tile&& tile, Unit&& unit,
-                                           Row&& row, Block&& block, Done&& done) {
+template <int F, int AM, int NT, int D, class Item, class Tile, class Unit, class Row, class Done>
+__device__ __forceinline__ void dec_stream(int n, rsrc_t rows, uint8_t* lds, int lane, f32x4 (&acc)[NT], Item&& item, Tile&& tile,
+                                           Unit&& unit, Row&& row, Done&& done) {
   using T = DecTraits<F>;
-  constexpr int NA = D * AM / 4;               // 1 KiB activation copies per block
+  constexpr int NA = dec_copies<AM, D>();
   constexpr int PER = NT * T::kLoads;          // vector loads per item
-  static_assert(D * AM % 4 == 0, "whole copies");
   static_assert(D * PER + NA < 64, "vmcnt range");
   if (n <= 0) return;
 
   auto copy_rows = [&](int b) __attribute__((always_inline)) {
-    block(min(b * D, n - 1));
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
       const int R = 4 * a + (lane >> 4);       // LDS row of the block
       const int r = R % AM;
-      const int i = min(b * D + R / AM, n - 1);
+      const int i = min(b * D + min(R / AM, D - 1), n - 1);
       const int c = dec_k_chunk<F>((lane & 15) ^ dec_key<AM>(r));
-      dec_lds_copy(rows, uint32_t(row(i, r)) + 16 * c, lds + (b & 1) * (D * AM * 256) + 1024 * a);
+      dec_lds_copy(rows, uint32_t(row(i, r)) + 16 * c, lds + (b & 1) * (NA * 1024) + 1024 * a);
     }
   };
   DecUnit<F> ring[D][NT];
   auto load = [&](int j, int i) __attribute__((always_inline)) {
     const int ic = min(i, n - 1);
+    item(ic);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) dec_load<F>(ring[j][t], tile(ic, t), unit(ic), i < n, lane);
+    for (int t = 0; t < NT; ++t) dec_load<F>(ring[j][t], tile(t), unit(ic, t), i < n, lane);
     // Keep the issue order as written, before the loop as in it: the wait before a slot's first use has to
     // hold for both ways into the loop, and with another order before it that would be a wait for everything.
     asm volatile("" ::: "memory");
@@ -260,17 +266,21 @@ __device__ __forceinline__ void dec_stream(int n, rsrc_t rows, uint8_t* lds, int
   for (int j = 0; j < D; ++j) load(j, j);
   const int rr = dec_lds_row<AM>(lane);
   const int blocks = (n + D - 1) / D;
-  for (int b = 0; b < blocks; ++b) {
-    // every read of the other half has completed before its next contents are asked for
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    copy_rows(b + 1);
-    // this block's rows have landed: only the block's loads and the copies just issued may be open
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(D * PER + NA) : "memory");
-    const uint8_t* base = lds + (b & 1) * (D * AM * 256);
+  // One block of D items; MORE: ask for the next one's rows, and refill each slot as it is used up.
+  auto turn = [&](int b, auto more) __attribute__((always_inline)) {
+    constexpr bool MORE = decltype(more)::value;
+    if constexpr (MORE) {
+      // every read of the other half has completed before its next contents are asked for
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      copy_rows(b + 1);
+    }
+    // this block's rows have landed: only the block's loads and the copies just asked for may be open
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(D * PER + (MORE ? NA : 0)) : "memory");
+    const uint8_t* base = lds + (b & 1) * (NA * 1024);
 #pragma unroll
     for (int j = 0; j < D; ++j) {
       const int i = b * D + j;
-      if (i < n) {
+      if (MORE || i < n) {   // every turn but the last is a whole one
         u32x4 af[4];
 #pragma unroll
         for (int d = 0; d < 4; ++d)
@@ -281,9 +291,11 @@ __device__ __forceinline__ void dec_stream(int n, rsrc_t rows, uint8_t* lds, int
         for (int t = 0; t < NT; ++t) dec_mul<F, AM>(acc[t], af, rs, ring[j][t], lane);
         done(i);
       }
-      load(j, i + D);
+      if constexpr (MORE) load(j, i + D);
     }
-  }
+  };
+  for (int b = 0; b + 1 < blocks; ++b) turn(b, std::true_type{});
+  turn(blocks - 1, std::false_type{});
   // nothing of this wave may still be on its way into LDS when the caller uses it for something else
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 }
