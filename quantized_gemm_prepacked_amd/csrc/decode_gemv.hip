@@ -85,6 +85,7 @@ hipError_t launch_one(const GemvParams& p, hipStream_t s) {
   constexpr int red = NW * NT * dec_elems<AM>() * 256, rows = NW * dec_wave_lds<AM, D>();
   constexpr int lds = red > rows ? red : rows;
   static_assert(lds <= 160 * 1024, "LDS");
+  static_assert(!GATED || NT % 2 == 0, "gate and up tiles come in pairs: with none a workgroup, the grid below would divide by zero");
   auto kern = gemv_kernel<F, AM, NT, NW, D, GATED>;
   if (lds > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -98,9 +99,9 @@ hipError_t launch_one(const GemvParams& p, hipStream_t s) {
 
 template <int F, bool GATED>
 hipError_t launch_rows(const GemvParams& p, hipStream_t s) {
-  if (p.M == 1) return launch_one<F, 1, 2, 8, 4, GATED>(p, s);
-  if (p.M <= 4) return launch_one<F, 4, 2, 8, 4, GATED>(p, s);
-  return launch_one<F, 16, 2, 8, 2, GATED>(p, s);
+  if (p.M == 1) return launch_one<F, 1, 2, 8, 2, GATED>(p, s);
+  if (p.M <= 4) return launch_one<F, 4, 4, 8, 2, GATED>(p, s);
+  return launch_one<F, 16, 4, 8, 2, GATED>(p, s);
 }
 
 }  // namespace

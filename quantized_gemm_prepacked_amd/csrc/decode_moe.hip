@@ -25,16 +25,15 @@ namespace hq {
 
 namespace {
 
-constexpr int kSlots = 4;   // tokens of a pass
+constexpr int kSlots = 4;   // tokens of a pass, at most
 
 struct Pass {
-  int e;                // expert
-  int entry[kSlots];    // the routed entry (t * topk + j) whose act row the slot reads
-  int token[kSlots];    // -1: no token (the slot repeats slot 0's row and is dropped, whatever its weight)
-  float weight[kSlots]; // router weight (an expert that stands in a token's row twice: the sum)
-  int pad[3];
+  int e;                  // expert
+  float weight[kSlots];   // router weight of a slot's token (an expert that stands in its row twice: the sum)
+  int16_t entry[kSlots];  // the routed entry (t * topk + j) whose act row the slot reads
+  int8_t token[kSlots];   // -1: no token (the slot repeats another's row and is dropped)
 };
-static_assert(sizeof(Pass) == 64, "Pass");
+static_assert(sizeof(Pass) == 32 && HQ_MOE_DECODE_MAX_TOKENS * 64 <= 1 << 15, "Pass");
 
 struct MoeParams {
   DecW W;
@@ -46,6 +45,7 @@ struct MoeParams {
   int* n_passes;
   int T, topk, E;
   int N, K;                // weight rows and K of this launch
+  int slots;               // tokens of a pass of the down launch
 };
 
 __device__ __forceinline__ bool moe_valid(int e, int E) { return e >= 0 && e < E; }
@@ -69,7 +69,7 @@ __device__ void moe_write_passes(const MoeParams& p, int32_t* ids, int32_t* coun
           for (int j = 0; j < p.topk; ++j) here |= ids[t * p.topk + j] == e;
           tokens += here;
         }
-        passes = (tokens + kSlots - 1) / kSlots;
+        passes = (tokens + p.slots - 1) / p.slots;
       }
     }
     count[f] = passes;
@@ -91,19 +91,19 @@ __device__ void moe_write_passes(const MoeParams& p, int32_t* ids, int32_t* coun
           w += p.weights ? p.weights[t * p.topk + j] : 1.0f;
         }
       if (entry < 0) continue;
-      if (used == kSlots) {
+      if (used == p.slots) {
         ++s;
         used = 0;
       }
       if (used == 0) {
         s->e = e;
         for (int g = 1; g < kSlots; ++g) {
-          s->entry[g] = entry;
+          s->entry[g] = int16_t(entry);
           s->token[g] = -1;
         }
       }
-      s->entry[used] = entry;
-      s->token[used] = t;
+      s->entry[used] = int16_t(entry);
+      s->token[used] = int8_t(t);
       s->weight[used] = w;
       ++used;
     }
@@ -224,17 +224,18 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeParams p) {
 // NT tiles of 16 outputs per workgroup; the items (pass, K unit) are cut into NW equal contiguous
 // ranges, one per wave. What a wave needs of an item -- its expert's address, its unit and pass, its
 // activation rows -- is worked out 64 items at a time, one per lane, and read back by lane: done item
-// by item on the scalar unit, which a CU's waves share, it took as long as the stream itself. AM = 2: one token, passes = its valid entries. AM = 8: passes of up to four tokens, sums per
-// token in LDS (one wave's, so the order is the passes').
+// by item on the scalar unit, which a CU's waves share, it took as long as the stream itself. AM = 2:
+// one token, passes = its valid entries. AM = 6, 8: passes of up to two or four tokens, sums per token
+// in LDS (a wave's own, so their order is the passes').
 template <int F, int AM, int NT, int NW, int D>
 __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeParams p) {
-  constexpr int RS = AM == 8 ? kSlots : 1;   // act rows of an item
+  constexpr int RS = dec_rows<AM>() / 2;   // act rows (high and low) of an item
   extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int P = p.T * p.topk;
   Pass* passes = reinterpret_cast<Pass*>(smem);
   uint8_t* rows_lds = smem + P * sizeof(Pass);
-  float* sums = reinterpret_cast<float*>(rows_lds + NW * dec_wave_lds<AM, D>());   // AM = 8: [NW][NT][T][16]
+  float* sums = reinterpret_cast<float*>(rows_lds + NW * dec_wave_lds<AM, D>());   // [NW][NT][T][16]
   int count;
   if constexpr (AM == 2) {
     const int e = lane < P ? p.ids[lane] : -1;
@@ -244,13 +245,13 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeParams p) {
     if (wave == 0 && in) {
       Pass& s = passes[__popcll(mask & ((uint64_t(1) << lane) - 1))];
       s.e = e;
-      s.entry[0] = lane;
+      s.entry[0] = int16_t(lane);
       s.weight[0] = p.weights ? p.weights[lane] : 1.0f;
     }
   } else {
     count = __builtin_amdgcn_readfirstlane(*p.n_passes);
     const u32x4* from = reinterpret_cast<const u32x4*>(p.passes);
-    for (int q = threadIdx.x; q < count * 4; q += NW * 64) reinterpret_cast<u32x4*>(passes)[q] = from[q];
+    for (int q = threadIdx.x; q < count * 2; q += NW * 64) reinterpret_cast<u32x4*>(passes)[q] = from[q];
     for (int q = threadIdx.x; q < NW * NT * p.T * 16; q += NW * 64) sums[q] = 0.f;
   }
   __syncthreads();
@@ -293,12 +294,12 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeParams p) {
         [&](int) __attribute__((always_inline)) { return tile; },
         // a tile past the last one lies outside the buffers
         [&](int, int t) __attribute__((always_inline)) { return at + t * units; },
-        [&](int i, int r) __attribute__((always_inline)) { return row_at[i * RS + (AM == 8 ? r >> 1 : 0)] + (r & 1) * (p.K * 2); },
+        [&](int i, int r) __attribute__((always_inline)) { return row_at[i * RS + (r >> 1)] + (r & 1) * (p.K * 2); },
         [&](int i) __attribute__((always_inline)) {
           const int s = __builtin_amdgcn_readlane(du, i);
           if (s & 1) {
             const Pass& pass = passes[s >> 1];
-            const int g = AM == 8 ? lane >> 4 : 0;
+            const int g = AM == 2 ? 0 : (lane >> 4) & (RS - 1);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               float v = dec_value<F, AM>(acc[t], 0) * pass.weight[g];
@@ -307,9 +308,9 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeParams p) {
                 const uint8_t* w = p.W.w + size_t(__builtin_amdgcn_readfirstlane(pass.e)) * p.W.expert_stride;
                 v *= reinterpret_cast<const float*>(w + p.W.scales_off)[c];
               }
-              if constexpr (AM == 8) {
+              if constexpr (AM != 2) {
                 const int tok = pass.token[g];
-                if (tok >= 0) sums[((wave * NT + t) * p.T + tok) * 16 + (lane & 15)] += v;
+                if (tok >= 0 && (lane >> 4) < RS) sums[((wave * NT + t) * p.T + tok) * 16 + (lane & 15)] += v;
               } else {
                 total[t] += v;
               }
@@ -361,8 +362,8 @@ hipError_t launch_up(const MoeParams& p, hipStream_t s) {
 template <int F, int AM, int NT, int NW, int D>
 hipError_t launch_down(const MoeParams& p, hipStream_t s) {
   const int P = p.T * p.topk;
-  constexpr int rows = NW * (dec_wave_lds<AM, D>() + 64 * (AM == 8 ? kSlots : 1) * 4);
-  // at most 1024 passes: 64 KiB of the 160
+  constexpr int rows = NW * (dec_wave_lds<AM, D>() + 64 * (dec_rows<AM>() / 2) * 4);
+  // at most 1024 passes: 32 KiB of the 160
   static_assert(1024 * sizeof(Pass) + rows + NW * NT * (AM == 2 ? 1 : HQ_MOE_DECODE_MAX_TOKENS) * 64 <= 160 * 1024, "LDS");
   const int lds = P * int(sizeof(Pass)) + rows + NW * NT * p.T * 64;
   const int tiles = p.N / 16;
@@ -381,6 +382,7 @@ MoeWs moe_ws(int64_t T, int32_t topk, int64_t I) {
   return w;
 }
 
+constexpr int SLOTS = 2;
 template <int F>
 hipError_t moe_fmt(const MoeDecodeCall& m, hipStream_t s) {
   const MoeWs ws = moe_ws(m.T, m.topk, m.I);
@@ -388,16 +390,16 @@ hipError_t moe_fmt(const MoeDecodeCall& m, hipStream_t s) {
   uint16_t* act = reinterpret_cast<uint16_t*>(base);
   MoeParams up{dec_weights(m.c, m.w_gate_up, 2 * m.I, m.H), static_cast<const uint16_t*>(m.x), m.topk_ids, m.topk_weights, act,
                reinterpret_cast<Pass*>(base + ws.passes), reinterpret_cast<int*>(base + ws.count), m.T, m.topk, m.E,
-               int(2 * m.I), int(m.H)};
+               int(2 * m.I), int(m.H), SLOTS};
   MoeParams down = up;
   down.W = dec_weights(m.c, m.w_down, m.H, m.I);
   down.x = act;
   down.y = static_cast<uint16_t*>(m.out);
   down.N = int(m.H);
   down.K = int(m.I);
-  hipError_t e = m.T == 1 ? launch_up<F, 1, 1, 8, 4>(up, s) : launch_up<F, 4, 1, 8, 4>(up, s);
+  hipError_t e = m.T == 1 ? launch_up<F, 1, 1, 8, 2>(up, s) : launch_up<F, 4, 2, 4, 2>(up, s);
   if (e != hipSuccess) return e;
-  return m.T == 1 ? launch_down<F, 2, 1, 8, 4>(down, s) : launch_down<F, 8, 1, 8, 2>(down, s);
+  return m.T == 1 ? (m.H >= 6144 ? launch_down<F, 2, 2, 16, 2>(down, s) : launch_down<F, 2, 1, 16, 3>(down, s)) : SLOTS == 2 ? launch_down<F, 6, 1, 16, 3>(down, s) : launch_down<F, 8, 1, 8, 2>(down, s);
 }
 
 }  // namespace

@@ -14,12 +14,13 @@
 //   AM = 1   one row (repeated; lane group 0's element 0 counts)
 //   AM = 2   one row as a high and a low bf16 (MFMA rows 0 and 1: elements 0 and 1, added)
 //   AM = 4   four rows at MFMA rows 0, 4, 8, 12: row g is element 0 of lane group g
-//   AM = 8   four rows, each high (row 4 g) and low (row 4 g + 1)
+//   AM = 6   two rows, each high (row 4 g) and low (row 4 g + 1), g = 0, 1
+//   AM = 8   four rows, likewise
 //   AM = 16  sixteen rows, all four elements
 // so that for few rows the per-group scaling on the vector ALU (with the dequantization the larger
 // part of the arithmetic) touches one element instead of four. The other MFMA rows repeat live
 // ones and are dropped: rows do not mix in a matrix product.
-// The activations reach LDS by direct copies, a block of D units at a time, two blocks deep.
+// An item's activation rows reach LDS by direct copies, asked for with its weights.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -63,18 +64,22 @@ __device__ __forceinline__ constexpr int dec_k_chunk(int at) {
   return DecTraits<F>::kFine ? ((at & 3) << 2) | (at >> 2) : at;
 }
 
+// LDS rows of a unit.
+template <int AM>
+constexpr int dec_rows() { return AM == 6 ? 4 : AM; }
+
 // Row r's chunk at position p stands in slot p ^ key: with 256-byte rows every row starts in the same
 // LDS bank, and unrotated the lanes of one read would all meet there.
 template <int AM>
 __device__ __forceinline__ int dec_key(int r) {
-  return AM == 16 ? (((r & 7) << 1) | ((r >> 3) & 1)) : AM >= 8 ? (r >> 1) : r;
+  return AM == 16 ? (((r & 7) << 1) | ((r >> 3) & 1)) : AM == 8 ? (r >> 1) : r;
 }
 
 // The LDS row that lane l feeds to the MFMA (its row l & 15).
 template <int AM>
 __device__ __forceinline__ int dec_lds_row(int lane) {
   const int r = lane & 15;
-  return AM == 1 ? 0 : AM == 2 ? (r & 1) : AM == 4 ? (r >> 2) : AM == 8 ? ((r >> 2) * 2 + (r & 1)) : r;
+  return AM == 1 ? 0 : AM == 2 ? (r & 1) : AM == 4 ? (r >> 2) : AM == 6 ? (((r >> 2) & 1) * 2 + (r & 1)) : AM == 8 ? ((r >> 2) * 2 + (r & 1)) : r;
 }
 
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
@@ -152,7 +157,7 @@ template <int AM>
 constexpr int dec_elems() { return AM == 16 ? 4 : 1; }
 template <int AM>
 __device__ __forceinline__ float dec_elem(const f32x4& d, int i) {
-  return AM == 2 || AM == 8 ? d[0] + d[1] : d[i];
+  return AM == 2 || AM == 6 || AM == 8 ? d[0] + d[1] : d[i];
 }
 
 // acc += the unit's product with the A operand af; rs: the row sums of its groups (INT4).
@@ -218,11 +223,11 @@ __device__ __forceinline__ void dec_row_sums(const u32x4 (&af)[4], float (&rs)[D
   }
 }
 
-// A block's activations, D units of AM rows, in whole copies of four 256-byte rows; a wave's LDS: two blocks.
+// Copies of an item's activation rows (four 256-byte rows each), and a wave's LDS: D items' rows.
+template <int AM>
+constexpr int dec_copies() { return (dec_rows<AM>() + 3) / 4; }
 template <int AM, int D>
-constexpr int dec_copies() { return (D * AM + 3) / 4; }
-template <int AM, int D>
-constexpr int dec_wave_lds() { return 2 * dec_copies<AM, D>() * 1024; }
+constexpr int dec_wave_lds() { return D * dec_copies<AM>() * 1024; }
 
 // The wave's loop over n items. An item is a unit of the wave's NT tiles:
 //   item(i)     called before item i is loaded
@@ -235,63 +240,59 @@ template <int F, int AM, int NT, int D, class Item, class Tile, class Unit, clas
 __device__ __forceinline__ void dec_stream(int n, rsrc_t rows, uint8_t* lds, int lane, f32x4 (&acc)[NT], Item&& item, Tile&& tile,
                                            Unit&& unit, Row&& row, Done&& done) {
   using T = DecTraits<F>;
-  constexpr int NA = dec_copies<AM, D>();
+  constexpr int ROWS = dec_rows<AM>();
+  constexpr int NA = dec_copies<AM>();
   constexpr int PER = NT * T::kLoads;          // vector loads per item
-  static_assert(D * PER + NA < 64, "vmcnt range");
+  static_assert(D * (PER + NA) < 64, "vmcnt range");
   if (n <= 0) return;
 
-  auto copy_rows = [&](int b) __attribute__((always_inline)) {
-#pragma unroll
-    for (int a = 0; a < NA; ++a) {
-      const int R = 4 * a + (lane >> 4);       // LDS row of the block
-      const int r = R % AM;
-      const int i = min(b * D + min(R / AM, D - 1), n - 1);
-      const int c = dec_k_chunk<F>((lane & 15) ^ dec_key<AM>(r));
-      dec_lds_copy(rows, uint32_t(row(i, r)) + 16 * c, lds + (b & 1) * (NA * 1024) + 1024 * a);
-    }
-  };
+  // Ask for item i, into slot j: its rows, then its tiles' units.
   DecUnit<F> ring[D][NT];
   auto load = [&](int j, int i) __attribute__((always_inline)) {
     const int ic = min(i, n - 1);
     item(ic);
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+      const int r = (4 * a + (lane >> 4)) % ROWS;   // fewer than four rows: again
+      const int c = dec_k_chunk<F>((lane & 15) ^ dec_key<AM>(r));
+      dec_lds_copy(rows, uint32_t(row(ic, r)) + 16 * c, lds + (j * NA + a) * 1024);
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) dec_load<F>(ring[j][t], tile(t), unit(ic, t), i < n, lane);
     // Keep the issue order as written, before the loop as in it: the wait before a slot's first use has to
     // hold for both ways into the loop, and with another order before it that would be a wait for everything.
     asm volatile("" ::: "memory");
   };
-
-  copy_rows(0);
 #pragma unroll
   for (int j = 0; j < D; ++j) load(j, j);
   const int rr = dec_lds_row<AM>(lane);
   const int blocks = (n + D - 1) / D;
-  // One block of D items; MORE: ask for the next one's rows, and refill each slot as it is used up.
+  // D items from b * D on; MORE: refill each slot as it is used up.
   auto turn = [&](int b, auto more) __attribute__((always_inline)) {
     constexpr bool MORE = decltype(more)::value;
-    if constexpr (MORE) {
-      // every read of the other half has completed before its next contents are asked for
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      copy_rows(b + 1);
-    }
-    // this block's rows have landed: only the block's loads and the copies just asked for may be open
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(D * PER + (MORE ? NA : 0)) : "memory");
-    const uint8_t* base = lds + (b & 1) * (NA * 1024);
 #pragma unroll
     for (int j = 0; j < D; ++j) {
       const int i = b * D + j;
+      // the item's rows have landed: only its own loads and the items asked for after it may be open
+      const int after = MORE ? D - 1 : D - 1 - j;
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(PER + after * (PER + NA)) : "memory");
       if (MORE || i < n) {   // every turn but the last is a whole one
+        const uint8_t* base = lds + j * NA * 1024 + rr * 256;
         u32x4 af[4];
 #pragma unroll
         for (int d = 0; d < 4; ++d)
-          af[d] = *reinterpret_cast<const u32x4*>(base + (j * AM + rr) * 256 + 16 * ((4 * (lane >> 4) + d) ^ dec_key<AM>(rr)));
+          af[d] = *reinterpret_cast<const u32x4*>(base + 16 * ((4 * (lane >> 4) + d) ^ dec_key<AM>(rr)));
         float rs[T::kGroups][dec_elems<AM>()];
         dec_row_sums<F, AM>(af, rs);
 #pragma unroll
         for (int t = 0; t < NT; ++t) dec_mul<F, AM>(acc[t], af, rs, ring[j][t], lane);
         done(i);
       }
-      if constexpr (MORE) load(j, i + D);
+      if constexpr (MORE) {
+        // every read of the slot's rows has completed before its next contents are asked for
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        load(j, i + D);
+      }
     }
   };
   for (int b = 0; b + 1 < blocks; ++b) turn(b, std::true_type{});
