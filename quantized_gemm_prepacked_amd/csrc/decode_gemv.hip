@@ -97,11 +97,31 @@ hipError_t launch_one(const GemvParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Tiles per workgroup (NT), waves and ring depth by what fills the 256 CUs, one WNA16 group-128 layer a
+// launch, weights from HBM, us (NT x waves x D):
+//   few output tiles: one a workgroup, so every CU has one, and a deep ring (M = 1: 4096 x 14336 8.0 as
+//   1x8x4, 11.5 as 2x8x2, 15.2 as 4x8x2; 2048 x 8192 4.7, 6.2, 9.3); with two K units a wave or less a
+//   ring of two (2048 x 2048: 2.9, 3.2 as 1x8x4)
+//   many: two or four tiles share the activations' reads and row sums (M = 1: 14336 x 4096 7.5 as 2x8x2,
+//   8.5 as 1x8x4; M = 16: 28672 x 8192 26 as 4x8x2, 31 as 2x8x2, 48 as 1x8x3)
+//   gated: pairs of a gate and an up tile; more waves where K is long and pairs are few (M = 1: 1024
+//   outputs x 8192 6.0 as 2x16x2, 6.4 as 2x8x2)
 template <int F, bool GATED>
 hipError_t launch_rows(const GemvParams& p, hipStream_t s) {
-  if (p.M == 1) return launch_one<F, 1, 2, 8, 2, GATED>(p, s);
-  if (p.M <= 4) return launch_one<F, 4, 4, 8, 2, GATED>(p, s);
-  return launch_one<F, 16, 4, 8, 2, GATED>(p, s);
+  const int tiles = p.N / 16 / (GATED ? 2 : 1);
+  if constexpr (GATED) {
+    if (p.M == 1) return tiles < 256 && p.W.units >= 64 ? launch_one<F, 1, 2, 16, 2, true>(p, s) : launch_one<F, 1, 2, 8, 2, true>(p, s);
+    if (p.M <= 4) return launch_one<F, 4, 2, 8, 2, true>(p, s);
+    return tiles < 448 ? launch_one<F, 16, 2, 8, 2, true>(p, s) : launch_one<F, 16, 4, 8, 2, true>(p, s);
+  } else {
+    if (p.M == 1) {
+      if (tiles >= 512) return launch_one<F, 1, 2, 8, 2, false>(p, s);
+      return p.W.units <= 16 ? launch_one<F, 1, 1, 8, 2, false>(p, s) : launch_one<F, 1, 1, 8, 4, false>(p, s);
+    }
+    if (p.M <= 4) return tiles < 512 ? launch_one<F, 4, 1, 8, 3, false>(p, s) : launch_one<F, 4, 2, 8, 2, false>(p, s);
+    if (tiles < 512) return launch_one<F, 16, 1, 8, 3, false>(p, s);
+    return tiles < 896 ? launch_one<F, 16, 2, 8, 2, false>(p, s) : launch_one<F, 16, 4, 8, 2, false>(p, s);
+  }
 }
 
 }  // namespace

@@ -382,7 +382,6 @@ MoeWs moe_ws(int64_t T, int32_t topk, int64_t I) {
   return w;
 }
 
-constexpr int SLOTS = 2;
 template <int F>
 hipError_t moe_fmt(const MoeDecodeCall& m, hipStream_t s) {
   const MoeWs ws = moe_ws(m.T, m.topk, m.I);
@@ -390,7 +389,7 @@ hipError_t moe_fmt(const MoeDecodeCall& m, hipStream_t s) {
   uint16_t* act = reinterpret_cast<uint16_t*>(base);
   MoeParams up{dec_weights(m.c, m.w_gate_up, 2 * m.I, m.H), static_cast<const uint16_t*>(m.x), m.topk_ids, m.topk_weights, act,
                reinterpret_cast<Pass*>(base + ws.passes), reinterpret_cast<int*>(base + ws.count), m.T, m.topk, m.E,
-               int(2 * m.I), int(m.H), SLOTS};
+               int(2 * m.I), int(m.H), m.T * m.topk > 2 * m.E ? 4 : 2};
   MoeParams down = up;
   down.W = dec_weights(m.c, m.w_down, m.H, m.I);
   down.x = act;
@@ -399,7 +398,9 @@ hipError_t moe_fmt(const MoeDecodeCall& m, hipStream_t s) {
   down.K = int(m.I);
   hipError_t e = m.T == 1 ? launch_up<F, 1, 1, 8, 2>(up, s) : launch_up<F, 4, 2, 4, 2>(up, s);
   if (e != hipSuccess) return e;
-  return m.T == 1 ? (m.H >= 6144 ? launch_down<F, 2, 2, 16, 2>(down, s) : launch_down<F, 2, 1, 16, 3>(down, s)) : SLOTS == 2 ? launch_down<F, 6, 1, 16, 3>(down, s) : launch_down<F, 8, 1, 8, 2>(down, s);
+  if (m.T == 1) return launch_down<F, 2, 1, 16, 3>(down, s);
+  if (up.slots == 4) return launch_down<F, 8, 1, 16, 2>(down, s);
+  return m.H >= 6144 ? launch_down<F, 6, 2, 16, 2>(down, s) : launch_down<F, 6, 1, 16, 3>(down, s);
 }
 
 }  // namespace
