@@ -4,11 +4,16 @@
 // Per token: scores s = softmax(l) or sigmoid(l) over E experts, selection values v = s + bias,
 // optionally only the best groups of experts kept, the k largest v in order (ties to the lowest
 // id), weights from the scores s. One wave per token; the row's E <= 512 values live in registers,
-// ceil(E / 64) per lane (expert i * 64 + lane, so the load is coalesced).
+// VPL = ceil(E / 64) neighbours per lane, so that among equal values the lowest lane, and in it the
+// lowest place, is the lowest id.
 //
-// Selection decides between neighbours, so it never compares rounded values: without a bias the
-// order of s is the order of the logits themselves (both scores are strictly increasing), with a
-// bias (or groups) s and v are held in 64 bits.
+// Selection decides between neighbours, so it never compares rounded values. Without bias and groups
+// the order of s is the order of the logits themselves (both scores are strictly increasing): the keys are
+// their 32 bits, and scores are worked out for the chosen ones only. Otherwise s and v are held in 64 bits.
+//
+// Bound by latency: one wave's chain of k wave-wide maxima, each six data-parallel moves inside the
+// vector unit and one lane read (through LDS shuffles of 64-bit values and ids the same selection took
+// twice as long).
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -22,165 +27,247 @@ namespace {
 
 constexpr int kWaves = 4;   // tokens per workgroup
 
-// The largest (v, lowest id) of the wave; every lane gets it.
-__device__ __forceinline__ void wave_best(double& v, int& id) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) {
-    const double ov = __shfl_xor(v, o);
-    const int oi = __shfl_xor(id, o);
-    if (ov > v || (ov == v && oi < id)) {
-      v = ov;
-      id = oi;
-    }
-  }
+// A lane's value moved within the wave (data-parallel primitive); lanes without a source get 0.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, ROWS, 0xF, false));
 }
 
+// Steps of a wave-wide fold into lane 63: shifts by 1, 2, 4, 8 inside rows of 16, then lane 15 of a row to
+// the next one, then lane 31 to the upper half.
+#define HQ_WAVE_FOLD(STEP) \
+  STEP(0x111, 0xF) STEP(0x112, 0xF) STEP(0x114, 0xF) STEP(0x118, 0xF) STEP(0x142, 0xA) STEP(0x143, 0xC)
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#define HQ_STEP(C, R) v = max(v, dpp<C, R>(v));
+  HQ_WAVE_FOLD(HQ_STEP)
+#undef HQ_STEP
+  return uint32_t(__builtin_amdgcn_readlane(int(v), 63));
+}
+
+__device__ __forceinline__ double make_f64(uint32_t hi, uint32_t lo) {
+  return __longlong_as_double((long long)(uint64_t(hi) << 32 | lo));
+}
+__device__ __forceinline__ uint32_t hi32(double v) { return uint32_t(uint64_t(__double_as_longlong(v)) >> 32); }
+__device__ __forceinline__ uint32_t lo32(double v) { return uint32_t(uint64_t(__double_as_longlong(v))); }
+
+__device__ __forceinline__ double lane_f64(double v, int lane) {
+  return make_f64(uint32_t(__builtin_amdgcn_readlane(int(hi32(v)), lane)), uint32_t(__builtin_amdgcn_readlane(int(lo32(v)), lane)));
+}
+
+// Sum over the wave, in a fixed order.
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+#define HQ_STEP(C, R) v += make_f64(dpp<C, R>(hi32(v)), dpp<C, R>(lo32(v)));
+  HQ_WAVE_FOLD(HQ_STEP)
+#undef HQ_STEP
+  return lane_f64(v, 63);
 }
 
-template <int VPL, bool BF16>
+// Unsigned keys in the order of the values; 0 is below every key. Zeros must not be negative.
+__device__ __forceinline__ uint32_t key_f32(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float f32_of_key(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ uint64_t key_f64(double f) {
+  const uint64_t u = uint64_t(__double_as_longlong(f));
+  return u ^ (uint64_t(int64_t(u) >> 63) | 0x8000000000000000ull);
+}
+
+// The largest value of the wave and the lowest lane that holds it.
+__device__ __forceinline__ int best_lane(uint32_t key, uint32_t& best) {
+  best = wave_max(key);
+  return __builtin_ctzll(__ballot(key == best));
+}
+__device__ __forceinline__ int best_lane(uint64_t key, uint64_t& best) {
+  const uint32_t hi = wave_max(uint32_t(key >> 32));
+  const bool top = uint32_t(key >> 32) == hi;
+  const uint32_t lo = wave_max(top ? uint32_t(key) : 0u);
+  best = uint64_t(hi) << 32 | lo;
+  return __builtin_ctzll(__ballot(key == best));
+}
+
+// exp(l - top), 1 where both are infinite.
+__device__ __forceinline__ double exp_below(float l, float top) { return l == top ? 1.0 : exp(double(l) - double(top)); }
+__device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-double(l))); }
+
+// PLAIN: no bias and no groups.
+template <int VPL, bool BF16, bool PLAIN>
 __global__ __launch_bounds__(kWaves * 64) void moe_route_kernel(RouteCall c) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = int64_t(blockIdx.x) * kWaves + (threadIdx.x >> 6);
-  if (t >= c.T) return;
-  const double ninf = -__builtin_huge_val();
+  const int wave = threadIdx.x >> 6;
+  const int64_t t = int64_t(blockIdx.x) * kWaves + wave;
+  const bool live = t < c.T;   // the workgroup's last waves may have no token; they take part in no barrier
+  if (!live) return;
+  const float ninf = -__builtin_huge_valf();
+  const double ninf64 = -__builtin_huge_val();
 
-  // logits; NaN counts as -infinity, the value of a switched-off expert
-  double l[VPL];
+  // logits; NaN counts as -infinity, the value of a switched-off expert; -0 as +0
+  float l[VPL];
+  uint32_t key[VPL];   // 0: switched off
+  uint32_t most = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const int e = 64 * i + lane;
-    float f = -__builtin_huge_valf();
+    const int e = lane * VPL + i;
+    float f = ninf;
     if (e < c.E) {
       const size_t at = size_t(t) * c.E + e;
       f = BF16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(c.logits)[at]) : static_cast<const float*>(c.logits)[at];
-      if (f != f) f = -__builtin_huge_valf();
+      f = f != f ? ninf : f + 0.0f;
     }
     l[i] = f;
+    key[i] = f == ninf ? 0u : key_f32(f);
+    most = max(most, key[i]);
   }
+  const bool sigmoid = c.score_fn == HQ_SCORE_SIGMOID;
 
-  double s[VPL], v[VPL];
-  if (c.score_fn == HQ_SCORE_SIGMOID) {
+  int my_id = -1;      // lane k: the k-th choice
+  double my_s = 0.0;   // and its score
+  if constexpr (PLAIN) {
+    uint32_t my_key = 0, first = 0;
+    for (int k = 0; k < c.topk; ++k) {
+      uint32_t m = key[0], best;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) s[i] = 1.0 / (1.0 + exp(-l[i]));
+      for (int i = 1; i < VPL; ++i) m = max(m, key[i]);
+      const int from = best_lane(m, best);
+      if (best == 0) break;
+      if (k == 0) first = best;
+      int place = VPL - 1;
+#pragma unroll
+      for (int i = VPL - 2; i >= 0; --i) place = key[i] == best ? i : place;
+      const int at = __builtin_amdgcn_readlane(place, from);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = lane == from && i == at ? 0u : key[i];
+      if (lane == k) {
+        my_id = from * VPL + at;
+        my_key = best;
+      }
+    }
+    if (my_id >= 0) {
+      const float mine = f32_of_key(my_key);
+      my_s = sigmoid ? sigmoid64(mine) : exp_below(mine, f32_of_key(first));
+    }
+    if (!sigmoid && !c.renormalize) {   // renormalised, the sum over all experts cancels
+      const float top = f32_of_key(first);
+      double sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) sum += l[i] == ninf ? 0.0 : exp_below(l[i], top);
+      sum = wave_sum(sum);
+      my_s = sum > 0.0 ? my_s / sum : 0.0;
+    }
   } else {
-    double top = l[0];
+    __shared__ double group_v[kWaves][64 * VPL];
+    double s[VPL], v[VPL];
+    if (sigmoid) {
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) top = fmax(top, l[i]);
+      for (int i = 0; i < VPL; ++i) s[i] = l[i] == ninf ? 0.0 : sigmoid64(l[i]);
+    } else {
+      const float top = f32_of_key(wave_max(most));
+      double sum = 0.0;
 #pragma unroll
-    for (int o = 32; o; o >>= 1) top = fmax(top, __shfl_xor(top, o));
-    double sum = 0.0;
+      for (int i = 0; i < VPL; ++i) {
+        s[i] = l[i] == ninf ? 0.0 : exp_below(l[i], top);
+        sum += s[i];
+      }
+      sum = wave_sum(sum);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) s[i] = sum > 0.0 ? s[i] / sum : 0.0;
+    }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      // equal to the maximum: 1 (also where both are infinite)
-      s[i] = l[i] == ninf ? 0.0 : l[i] == top ? 1.0 : exp(l[i] - top);
-      sum += s[i];
+      const int e = lane * VPL + i;
+      float b = 0.0f;
+      if (c.bias && e < c.E) {
+        b = c.bias[e];
+        if (b != b) b = ninf;
+      }
+      v[i] = l[i] == ninf ? ninf64 : s[i] + double(b) + 0.0;
     }
-    sum = wave_sum(sum);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) s[i] = sum > 0.0 ? s[i] / sum : 0.0;
-  }
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = 64 * i + lane;
-    double b = 0.0;
-    if (c.bias && e < c.E) {
-      b = c.bias[e];
-      if (b != b) b = ninf;
-    }
-    v[i] = l[i] == ninf ? ninf : s[i] + b;
-  }
 
-  // groups: keep the experts of the best ones
-  const int per = c.E / c.n_group;
-  uint64_t kept = ~uint64_t(0);
-  if (c.n_group > 1) {
-    double mine = ninf;   // lane g < n_group: the value of group g
-    for (int g = 0; g < c.n_group; ++g) {
-      double sum = 0.0;
-      int first = -1;
-      bool any = false;
-      for (int r = 0; r < c.group_top; ++r) {
-        double bv = ninf;
-        int bi = 1 << 30;
+    // groups: keep the experts of the best ones
+    uint64_t kept = ~uint64_t(0);
+    const int per = c.E / c.n_group;
+    if (c.n_group > 1) {
+      // lane g: the sum of the largest group_top values of group g, from the wave's own LDS (each lane
+      // starts at another place, so that equal strides do not meet in one bank)
+      double* mine = group_v[wave];
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          const int e = 64 * i + lane;
-          if (e < c.E && e / per == g && e != first && v[i] > bv) {
-            bv = v[i];
-            bi = e;
-          }
+      for (int i = 0; i < VPL; ++i) mine[lane * VPL + i] = v[i];
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // written and read by this wave alone
+      double a = ninf64, b = ninf64;   // the largest two
+      if (lane < c.n_group) {
+        int j = lane % per;
+        for (int n = 0; n < per; ++n) {
+          const double x = mine[lane * per + j];
+          b = fmax(b, fmin(a, x));
+          a = fmax(a, x);
+          j = j + 1 == per ? 0 : j + 1;
         }
-        wave_best(bv, bi);
-        if (bv != ninf) {
-          sum += bv;
-          any = true;
-        }
-        first = bi;
       }
-      if (lane == g && any) mine = sum;
+      const double value = a == ninf64 ? ninf64 : (c.group_top == 2 && b != ninf64 ? a + b : a) + 0.0;
+      // kept: fewer than topk_group groups are better (ties: the lower one is)
+      int better = 0;
+      for (int g = 0; g < c.n_group; ++g) {
+        const double other = lane_f64(value, g);
+        better += other > value || (other == value && g < lane);
+      }
+      kept = __ballot(lane < c.n_group && better < c.topk_group);
     }
-    kept = 0;
-    for (int r = 0; r < c.topk_group; ++r) {
-      double bv = mine;
-      int bi = lane < c.n_group && !((kept >> lane) & 1) ? lane : 1 << 30;
-      if (bi == 1 << 30) bv = ninf;
-      wave_best(bv, bi);
-      if (bi < 64) kept |= uint64_t(1) << bi;
-    }
-  }
-  double by[VPL];
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = 64 * i + lane;
-    const bool in = e < c.E && ((kept >> (c.n_group > 1 ? e / per : 0)) & 1) && v[i] != ninf;
-    by[i] = !in ? ninf : c.bias ? v[i] : l[i];
-  }
 
-  // the k largest, one at a time; lane k keeps the k-th
-  int my_id = -1;
-  double my_s = 0.0, sum = 0.0;
-  for (int k = 0; k < c.topk; ++k) {
-    double bv = by[0];
-    int bi = bv == ninf ? 1 << 30 : lane;
+    // the keys are the values' (bias) or still the logits' (groups alone)
+    uint64_t by[VPL];
 #pragma unroll
-    for (int i = 1; i < VPL; ++i)
-      if (by[i] > bv) {
-        bv = by[i];
-        bi = 64 * i + lane;
-      }
-    wave_best(bv, bi);
-    if (bv == ninf) break;
-    double sv = 0.0;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (bi == 64 * i + lane) {
-        sv = s[i];
-        by[i] = ninf;
-      }
-    sv = __shfl(sv, bi & 63);
-    sum += sv;
-    if (lane == k) {
-      my_id = bi;
-      my_s = sv;
+    for (int i = 0; i < VPL; ++i) {
+      const int e = lane * VPL + i;
+      const bool in = e < c.E && v[i] != ninf64 && ((kept >> (c.n_group > 1 ? e / per : 0)) & 1);
+      by[i] = !in ? 0u : c.bias ? key_f64(v[i]) : uint64_t(key[i]);
     }
+    for (int k = 0; k < c.topk; ++k) {
+      uint64_t m = by[0], best;
+#pragma unroll
+      for (int i = 1; i < VPL; ++i) m = by[i] > m ? by[i] : m;
+      const int from = best_lane(m, best);
+      if (best == 0) break;
+      int place = VPL - 1;
+      double sv = s[VPL - 1];
+#pragma unroll
+      for (int i = VPL - 2; i >= 0; --i) {
+        place = by[i] == best ? i : place;
+        sv = by[i] == best ? s[i] : sv;
+      }
+      const int at = __builtin_amdgcn_readlane(place, from);
+      sv = lane_f64(sv, from);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) by[i] = lane == from && i == at ? 0u : by[i];
+      if (lane == k) {
+        my_id = from * VPL + at;
+        my_s = sv;
+      }
+    }
+  }
+  if (c.renormalize) {
+    const double sum = wave_sum(my_s);   // lanes without a choice hold 0
+    my_s = sum > 0.0 ? my_s / sum : 0.0;
   }
   if (lane < c.topk) {
-    if (c.renormalize) my_s = sum > 0.0 ? my_s / sum : 0.0;
     c.topk_ids[t * c.topk + lane] = my_id;
-    c.topk_weights[t * c.topk + lane] = float(my_s * c.scale);
+    c.topk_weights[t * c.topk + lane] = float(my_s * double(c.scale));
   }
 }
 
 template <int VPL>
 void launch(const RouteCall& c, dim3 grid, hipStream_t s) {
-  if (c.bf16)
-    hipLaunchKernelGGL((moe_route_kernel<VPL, true>), grid, dim3(kWaves * 64), 0, s, c);
-  else
-    hipLaunchKernelGGL((moe_route_kernel<VPL, false>), grid, dim3(kWaves * 64), 0, s, c);
+  const bool plain = !c.bias && c.n_group == 1;
+  const dim3 block(kWaves * 64);
+  if (c.bf16) {
+    if (plain) hipLaunchKernelGGL((moe_route_kernel<VPL, true, true>), grid, block, 0, s, c);
+    else hipLaunchKernelGGL((moe_route_kernel<VPL, true, false>), grid, block, 0, s, c);
+  } else {
+    if (plain) hipLaunchKernelGGL((moe_route_kernel<VPL, false, true>), grid, block, 0, s, c);
+    else hipLaunchKernelGGL((moe_route_kernel<VPL, false, false>), grid, block, 0, s, c);
+  }
 }
 
 }  // namespace
