@@ -97,14 +97,30 @@ hipError_t launch_one(const GemvParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Tiles per workgroup (NT), waves and ring depth by what fills the 256 CUs, one WNA16 group-128 layer a
-// launch, weights from HBM, us (NT x waves x D):
-//   few output tiles: one a workgroup, so every CU has one, and a deep ring (M = 1: 4096 x 14336 8.0 as
+// Tile groups (of lo .. hi tiles) per workgroup: what leaves the fullest CU the fewest tiles when the
+// workgroups are dealt over the 256 CUs, ties to the more (or fewer) tiles.
+int tiles_per_workgroup(int tiles, int lo, int hi, bool ties_to_more) {
+  int best = lo, cost = 1 << 30;
+  for (int nt = lo; nt <= hi; ++nt) {
+    const int c = ((tiles + nt - 1) / nt + 255) / 256 * nt;
+    if (c < cost || (c == cost && ties_to_more)) {
+      best = nt;
+      cost = c;
+    }
+  }
+  return best;
+}
+
+// Tiles per workgroup (NT), waves and ring depth, measured on one WNA16 group-128 layer a launch, weights
+// from HBM, us (NT x waves x D):
+//   up to 256 output tiles: one a workgroup, so every CU has one, and a deep ring (M = 1: 4096 x 14336 8.0 as
 //   1x8x4, 11.5 as 2x8x2, 15.2 as 4x8x2; 2048 x 8192 4.7, 6.2, 9.3); with two K units a wave or less a
 //   ring of two (2048 x 2048: 2.9, 3.2 as 1x8x4)
-//   many: two or four tiles share the activations' reads and row sums (M = 1: 14336 x 4096 7.5 as 2x8x2,
-//   8.5 as 1x8x4; M = 16: 28672 x 8192 26 as 4x8x2, 31 as 2x8x2, 48 as 1x8x3)
-//   gated: pairs of a gate and an up tile; more waves where K is long and pairs are few (M = 1: 1024
+//   more: two to four tiles share the activations' reads and row sums (M = 1: 14336 x 4096 7.5 as 2x8x2,
+//   8.5 as 1x8x4; M = 16: 28672 x 8192 26 as 4x8x2, 31 as 2x8x2, 48 as 1x8x3), as many as fill the CUs
+//   evenly (M = 16: 8192 x 8192 11.0 as 2x8x2, 13.7 as 4x8x2; one tile more, 8208 x 8192, 15.4 as 2x8x2,
+//   12.5 as 3x8x2, 13.9 as 4x8x2)
+//   gated: pairs of a gate and an up tile; more waves where K is long and pairs are few (M = 1: 2048 / 2
 //   outputs x 8192 6.0 as 2x16x2, 6.4 as 2x8x2)
 template <int F, bool GATED>
 hipError_t launch_rows(const GemvParams& p, hipStream_t s) {
@@ -112,15 +128,22 @@ hipError_t launch_rows(const GemvParams& p, hipStream_t s) {
   if constexpr (GATED) {
     if (p.M == 1) return tiles < 256 && p.W.units >= 64 ? launch_one<F, 1, 2, 16, 2, true>(p, s) : launch_one<F, 1, 2, 8, 2, true>(p, s);
     if (p.M <= 4) return launch_one<F, 4, 2, 8, 2, true>(p, s);
-    return tiles < 448 ? launch_one<F, 16, 2, 8, 2, true>(p, s) : launch_one<F, 16, 4, 8, 2, true>(p, s);
+    return tiles_per_workgroup(tiles, 1, 2, true) == 1 ? launch_one<F, 16, 2, 8, 2, true>(p, s) : launch_one<F, 16, 4, 8, 2, true>(p, s);
   } else {
     if (p.M == 1) {
-      if (tiles >= 512) return launch_one<F, 1, 2, 8, 2, false>(p, s);
-      return p.W.units <= 16 ? launch_one<F, 1, 1, 8, 2, false>(p, s) : launch_one<F, 1, 1, 8, 4, false>(p, s);
+      if (tiles <= 256) return p.W.units <= 16 ? launch_one<F, 1, 1, 8, 2, false>(p, s) : launch_one<F, 1, 1, 8, 4, false>(p, s);
+      return tiles_per_workgroup(tiles, 2, 3, false) == 2 ? launch_one<F, 1, 2, 8, 2, false>(p, s) : launch_one<F, 1, 3, 8, 2, false>(p, s);
     }
-    if (p.M <= 4) return tiles < 512 ? launch_one<F, 4, 1, 8, 3, false>(p, s) : launch_one<F, 4, 2, 8, 2, false>(p, s);
-    if (tiles < 512) return launch_one<F, 16, 1, 8, 3, false>(p, s);
-    return tiles < 896 ? launch_one<F, 16, 2, 8, 2, false>(p, s) : launch_one<F, 16, 4, 8, 2, false>(p, s);
+    if (p.M <= 4) {
+      if (tiles <= 256) return launch_one<F, 4, 1, 8, 3, false>(p, s);
+      return tiles_per_workgroup(tiles, 2, 3, false) == 2 ? launch_one<F, 4, 2, 8, 2, false>(p, s) : launch_one<F, 4, 3, 8, 2, false>(p, s);
+    }
+    if (tiles <= 256) return launch_one<F, 16, 1, 8, 3, false>(p, s);
+    switch (tiles_per_workgroup(tiles, 2, 4, true)) {
+      case 2: return launch_one<F, 16, 2, 8, 2, false>(p, s);
+      case 3: return launch_one<F, 16, 3, 8, 2, false>(p, s);
+      default: return launch_one<F, 16, 4, 8, 2, false>(p, s);
+    }
   }
 }
 

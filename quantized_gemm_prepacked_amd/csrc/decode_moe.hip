@@ -398,7 +398,7 @@ hipError_t moe_fmt(const MoeDecodeCall& m, hipStream_t s) {
   down.K = int(m.I);
   hipError_t e = m.T == 1 ? launch_up<F, 1, 1, 8, 2>(up, s) : launch_up<F, 4, 2, 4, 2>(up, s);
   if (e != hipSuccess) return e;
-  if (m.T == 1) return launch_down<F, 2, 1, 16, 3>(down, s);
+  if (m.T == 1) return m.H >= 6144 ? launch_down<F, 2, 2, 16, 2>(down, s) : launch_down<F, 2, 1, 16, 3>(down, s);
   if (up.slots == 4) return launch_down<F, 8, 1, 16, 2>(down, s);
   return m.H >= 6144 ? launch_down<F, 6, 2, 16, 2>(down, s) : launch_down<F, 6, 1, 16, 3>(down, s);
 }
