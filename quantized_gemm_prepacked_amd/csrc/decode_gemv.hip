@@ -49,7 +49,7 @@ __global__ __launch_bounds__(NW * 64) void gemv_kernel(GemvParams p) {
       [&](int i, int r) __attribute__((always_inline)) {
         return uint32_t(min(r, p.M - 1 - row0)) * (p.K * 2) + uint32_t(wave + i * NW) * 256;
       },
-      [](int) __attribute__((always_inline)) {});
+      [](int, const DecUnit<F>(&)[NT]) __attribute__((always_inline)) {});
 
   float(*red)[NT][E][64] = reinterpret_cast<float(*)[NT][E][64]>(smem);
   __syncthreads();   // every wave is done with its activations

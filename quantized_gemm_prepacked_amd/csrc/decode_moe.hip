@@ -46,72 +46,72 @@ struct MoeParams {
   int T, topk, E;
   int N, K;                // weight rows and K of this launch
   int slots;               // tokens of a pass of the down launch
+  int tiles, splits;       // down: workgroups along the outputs, and along the items
+  float* partial;          // splits > 1: [tiles][splits][the workgroup's sums]
+  uint32_t* arrived;       // splits > 1: [tiles], zeroed by the up launch
 };
 
 __device__ __forceinline__ bool moe_valid(int e, int E) { return e >= 0 && e < E; }
 
-// The list of passes (T > 1), by one workgroup: experts in the order of their first entry.
-__device__ void moe_write_passes(const MoeParams& p, int32_t* ids, int32_t* count) {
-  const int P = p.T * p.topk;
-  for (int f = threadIdx.x; f < P; f += blockDim.x) ids[f] = p.ids[f];
+// The list of passes (T > 1), by one workgroup of NW waves: experts in order, an expert's tokens in order,
+// p.slots to a pass. lds: moe_pass_lds(P, E) bytes.
+inline constexpr int moe_pass_lds(int P, int E) { return (P + 2 * E + 16) * 4; }
+
+template <int NW>
+__device__ void moe_write_passes(const MoeParams& p, uint8_t* lds) {
+  const int P = p.T * p.topk, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int32_t* ids = reinterpret_cast<int32_t*>(lds);
+  uint32_t* mask = reinterpret_cast<uint32_t*>(ids + P);   // bit t: token t is routed to the expert
+  int32_t* base = reinterpret_cast<int32_t*>(mask + p.E);  // the expert's first pass
+  int32_t* wave_sum = base + p.E;
+  for (int e = tid; e < p.E; e += NW * 64) mask[e] = 0;
+  for (int f = tid; f < P; f += NW * 64) ids[f] = p.ids[f];
   __syncthreads();
-  // first entry of an expert: the number of its tokens' passes; elsewhere 0
-  for (int f = threadIdx.x; f < P; f += blockDim.x) {
-    const int e = ids[f];
-    int passes = 0;
-    if (moe_valid(e, p.E)) {
-      bool first = true;
-      for (int q = 0; q < f; ++q) first &= ids[q] != e;
-      if (first) {
-        int tokens = 0;
-        for (int t = f / p.topk; t < p.T; ++t) {
-          bool here = false;
-          for (int j = 0; j < p.topk; ++j) here |= ids[t * p.topk + j] == e;
-          tokens += here;
-        }
-        passes = (tokens + p.slots - 1) / p.slots;
-      }
-    }
-    count[f] = passes;
-  }
+  for (int f = tid; f < P; f += NW * 64)
+    if (moe_valid(ids[f], p.E)) atomicOr(&mask[ids[f]], 1u << (f / p.topk));
   __syncthreads();
-  for (int f = threadIdx.x; f < P; f += blockDim.x) {
-    if (count[f] == 0) continue;
-    int at = 0;
-    for (int q = 0; q < f; ++q) at += count[q];
-    const int e = ids[f];
-    int used = 0;
-    Pass* s = p.passes + at;
-    for (int t = f / p.topk; t < p.T; ++t) {
-      int entry = -1;
-      float w = 0.f;
-      for (int j = 0; j < p.topk; ++j)
-        if (ids[t * p.topk + j] == e) {
-          if (entry < 0) entry = t * p.topk + j;
-          w += p.weights ? p.weights[t * p.topk + j] : 1.0f;
-        }
-      if (entry < 0) continue;
-      if (used == p.slots) {
-        ++s;
-        used = 0;
-      }
-      if (used == 0) {
-        s->e = e;
-        for (int g = 1; g < kSlots; ++g) {
-          s->entry[g] = int16_t(entry);
-          s->token[g] = -1;
-        }
-      }
-      s->entry[used] = int16_t(entry);
-      s->token[used] = int8_t(t);
-      s->weight[used] = w;
-      ++used;
-    }
+  // exclusive prefix sum of the experts' passes, neighbouring experts per thread
+  const int each = (p.E + NW * 64 - 1) / (NW * 64), e0 = tid * each;
+  int mine = 0;
+  for (int e = e0; e < min(e0 + each, p.E); ++e) mine += (__popc(mask[e]) + p.slots - 1) / p.slots;
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(upto, o);
+    if (lane >= o) upto += v;
   }
-  if (threadIdx.x == 0) {
-    int total = 0;
-    for (int q = 0; q < P; ++q) total += count[q];
-    *p.n_passes = total;
+  if (lane == 63) wave_sum[wave] = upto;
+  __syncthreads();
+  int at = upto - mine;
+  for (int w = 0; w < wave; ++w) at += wave_sum[w];
+  for (int e = e0; e < min(e0 + each, p.E); ++e) {
+    base[e] = at;
+    at += (__popc(mask[e]) + p.slots - 1) / p.slots;
+  }
+  if (tid == NW * 64 - 1) *p.n_passes = at;
+  __syncthreads();
+  // each routed entry fills its token's slot; an expert's later entries in the same row only add their weight
+  for (int f = tid; f < P; f += NW * 64) {
+    const int e = ids[f], t = f / p.topk, row = t * p.topk;
+    if (!moe_valid(e, p.E)) continue;
+    bool again = false;
+    for (int q = row; q < f; ++q) again |= ids[q] == e;
+    if (again) continue;
+    float w = 0.f;
+    for (int q = f; q < row + p.topk; ++q)
+      if (ids[q] == e) w += p.weights ? p.weights[q] : 1.0f;
+    const uint32_t m = mask[e];
+    const int r = __popc(m & ((1u << t) - 1)), g = r % p.slots;
+    Pass* s = p.passes + base[e] + r / p.slots;
+    if (g == 0) s->e = e;
+    s->entry[g] = int16_t(f);
+    s->token[g] = int8_t(t);
+    s->weight[g] = w;
+    if (r == __popc(m) - 1)   // the last token: the slots behind it repeat it
+      for (int d = g + 1; d < p.slots; ++d) {
+        s->entry[d] = int16_t(f);
+        s->token[d] = -1;
+      }
   }
 }
 
@@ -123,21 +123,32 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int I = p.N / 2;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && p.splits > 1)
+    for (int q = threadIdx.x; q < p.tiles; q += NW * 64) p.arrived[q] = 0;
   int f = blockIdx.y, e, slots = 1;
   uint32_t tokens = 0;   // bit t: token t is routed to e
   int entry = 0;         // AM = 4: lane t's first entry routed to e
   if constexpr (AM == 4) {
     if (f == 0) {
-      if (blockIdx.x == 0) moe_write_passes(p, reinterpret_cast<int32_t*>(smem), reinterpret_cast<int32_t*>(smem) + p.T * p.topk);
+      if (blockIdx.x == 0) moe_write_passes<NW>(p, smem);
       return;
     }
     --f;
     e = p.ids[f];
     if (!moe_valid(e, p.E)) return;
     entry = -1;
-    if (lane < p.T)
-      for (int j = p.topk - 1; j >= 0; --j)
-        if (p.ids[lane * p.topk + j] == e) entry = lane * p.topk + j;
+    {
+      const int32_t* row = p.ids + min(lane, p.T - 1) * p.topk;
+      for (int j = 0; j < p.topk; j += 8) {   // eight loads at a time
+        int32_t id[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) id[q] = row[min(j + q, p.topk - 1)];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (id[q] == e && entry < 0) entry = min(j + q, p.topk - 1);
+      }
+      entry = entry >= 0 && lane < p.T ? lane * p.topk + entry : -1;
+    }
     tokens = uint32_t(__ballot(entry >= 0));
     if (__builtin_amdgcn_readlane(entry, __builtin_ctz(tokens)) != f) return;
     slots = __builtin_popcount(tokens);
@@ -184,7 +195,7 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeParams p) {
           if constexpr (AM == 4) t = r == 0 ? tok[0] : r == 1 ? tok[1] : r == 2 ? tok[2] : tok[3];
           return uint32_t(t) * (p.K * 2) + uint32_t(wave + i * NW) * 256;
         },
-        [](int) __attribute__((always_inline)) {});
+        [](int, const DecUnit<F>(&)[NT]) __attribute__((always_inline)) {});
 
     float(*red)[NT][64] = reinterpret_cast<float(*)[NT][64]>(smem);
     __syncthreads();   // every wave is done with its activations
@@ -221,8 +232,9 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeParams p) {
   }
 }
 
-// NT tiles of 16 outputs per workgroup; the items (pass, K unit) are cut into NW equal contiguous
-// ranges, one per wave. What a wave needs of an item -- its expert's address, its unit and pass, its
+// NT tiles of 16 outputs per workgroup; the items (pass, K unit) are cut into splits * NW equal contiguous
+// ranges, one per wave of the splits workgroups (blockIdx.y) of a tile. With more than one, each leaves its
+// sums in the workspace and the one that arrives last adds them, in split order. What a wave needs of an item -- its expert's address, its unit and pass, its
 // activation rows -- is worked out 64 items at a time, one per lane, and read back by lane: done item
 // by item on the scalar unit, which a CU's waves share, it took as long as the stream itself. AM = 2:
 // one token, passes = its valid entries. AM = 6, 8: passes of up to two or four tokens, sums per token
@@ -258,7 +270,8 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeParams p) {
 
   const int out_tiles = p.N / 16, ot0 = blockIdx.x * NT, units = p.W.units;
   const int items = count * units;
-  const int q0 = int(int64_t(items) * wave / NW), q1 = int(int64_t(items) * (wave + 1) / NW);
+  const int part = blockIdx.y * NW + wave, parts = p.splits * NW;
+  const int q0 = int(int64_t(items) * part / parts), q1 = int(int64_t(items) * (part + 1) / parts);
   f32x4 acc[NT];
   float total[NT];
 #pragma unroll
@@ -284,18 +297,18 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeParams p) {
 
     DecTile<F> tile;
     int at = 0;
-    dec_stream<F, AM, NT, D>(
+    dec_stream<F, AM, NT, D, true>(
         n, rows, rows_lds + wave * dec_wave_lds<AM, D>(), lane, acc,
         [&](int i) __attribute__((always_inline)) {
           const uint64_t lo = uint32_t(__builtin_amdgcn_readlane(w_lo, i)), hi = uint32_t(__builtin_amdgcn_readlane(w_hi, i));
-          tile = dec_tile<F>(p.W, reinterpret_cast<const uint8_t*>(hi << 32 | lo), ot0, tiles);
+          tile = dec_tile<F, true>(p.W, reinterpret_cast<const uint8_t*>(hi << 32 | lo), ot0, tiles);
           at = __builtin_amdgcn_readlane(u, i);
         },
         [&](int) __attribute__((always_inline)) { return tile; },
         // a tile past the last one lies outside the buffers
         [&](int, int t) __attribute__((always_inline)) { return at + t * units; },
         [&](int i, int r) __attribute__((always_inline)) { return row_at[i * RS + (r >> 1)] + (r & 1) * (p.K * 2); },
-        [&](int i) __attribute__((always_inline)) {
+        [&](int i, const DecUnit<F>(&unit)[NT]) __attribute__((always_inline)) {
           const int s = __builtin_amdgcn_readlane(du, i);
           if (s & 1) {
             const Pass& pass = passes[s >> 1];
@@ -303,11 +316,7 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeParams p) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               float v = dec_value<F, AM>(acc[t], 0) * pass.weight[g];
-              if constexpr (DecTraits<F>::kW8) {
-                const int c = min(ot0 + t, out_tiles - 1) * 16 + (lane & 15);
-                const uint8_t* w = p.W.w + size_t(__builtin_amdgcn_readfirstlane(pass.e)) * p.W.expert_stride;
-                v *= reinterpret_cast<const float*>(w + p.W.scales_off)[c];
-              }
+              if constexpr (DecTraits<F>::kW8) v *= __uint_as_float(unit[t].s[0]);
               if constexpr (AM != 2) {
                 const int tok = pass.token[g];
                 if (tok >= 0 && (lane >> 4) < RS) sums[((wave * NT + t) * p.T + tok) * 16 + (lane & 15)] += v;
@@ -328,13 +337,35 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeParams p) {
     }
   }
   __syncthreads();
-  const int T = AM == 2 ? 1 : p.T;
-  for (int q = threadIdx.x; q < NT * T * 16; q += NW * 64) {
+  const int T = AM == 2 ? 1 : p.T, values = NT * T * 16;
+  float* partial = p.partial + size_t(blockIdx.x) * p.splits * values;
+  for (int q = threadIdx.x; q < values; q += NW * 64) {
     const int c = q & 15, tok = (q >> 4) % T, t = (q >> 4) / T;
-    if (ot0 + t >= out_tiles) continue;
     float v = 0.f;
 #pragma unroll
     for (int k = 0; k < NW; ++k) v += sums[((k * NT + t) * T + tok) * 16 + c];
+    if (p.splits > 1)
+      // device scope: written through to where every CU's loads see it
+      __hip_atomic_store(partial + size_t(blockIdx.y) * values + q, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    else if (ot0 + t < out_tiles)
+      p.y[size_t(tok) * p.N + (ot0 + t) * 16 + c] = f32_to_bf16_rne(v);
+  }
+  if (p.splits == 1) return;
+  // every store above has completed before the workgroup counts as arrived; the last one's loads are of
+  // device scope as well
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  int* last = reinterpret_cast<int*>(smem);
+  if (threadIdx.x == 0)
+    *last = __hip_atomic_fetch_add(p.arrived + blockIdx.x, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == uint32_t(p.splits);
+  __syncthreads();
+  if (!*last) return;
+  for (int q = threadIdx.x; q < values; q += NW * 64) {
+    const int c = q & 15, tok = (q >> 4) % T, t = (q >> 4) / T;
+    if (ot0 + t >= out_tiles) continue;
+    float v = 0.f;
+    for (int k = 0; k < p.splits; ++k)
+      v += __hip_atomic_load(partial + size_t(k) * values + q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     p.y[size_t(tok) * p.N + (ot0 + t) * 16 + c] = f32_to_bf16_rne(v);
   }
 }
@@ -353,7 +384,7 @@ template <int F, int AM, int PAIRS, int NW, int D>
 hipError_t launch_up(const MoeParams& p, hipStream_t s) {
   const int P = p.T * p.topk;
   constexpr int red = NW * 2 * PAIRS * 256, rows = NW * dec_wave_lds<AM, D>();
-  const int lds = std::max(std::max(red, rows), AM == 4 ? P * 8 : 0);
+  const int lds = std::max(std::max(red, rows), AM == 4 ? moe_pass_lds(P, p.E) : 0);
   const int tiles = p.N / 32;
   return launch(moe_up_kernel<F, AM, PAIRS, NW, D>, dim3(unsigned((tiles + PAIRS - 1) / PAIRS), unsigned(P + (AM == 4 ? 1 : 0))),
                 NW * 64, lds, s, p);
@@ -366,47 +397,80 @@ hipError_t launch_down(const MoeParams& p, hipStream_t s) {
   // at most 1024 passes: 32 KiB of the 160
   static_assert(1024 * sizeof(Pass) + rows + NW * NT * (AM == 2 ? 1 : HQ_MOE_DECODE_MAX_TOKENS) * 64 <= 160 * 1024, "LDS");
   const int lds = P * int(sizeof(Pass)) + rows + NW * NT * p.T * 64;
-  const int tiles = p.N / 16;
-  return launch(moe_down_kernel<F, AM, NT, NW, D>, dim3(unsigned((tiles + NT - 1) / NT)), NW * 64, lds, s, p);
+  return launch(moe_down_kernel<F, AM, NT, NW, D>, dim3(unsigned(p.tiles), unsigned(p.splits)), NW * 64, lds, s, p);
 }
 
-// Workspace: the activations (high and low rows of every routed entry), the passes, their number.
-struct MoeWs {
-  size_t passes, count, total;
+// The down launch: tokens of a pass, tiles of a workgroup, workgroups along the outputs and the items.
+struct DownPlan {
+  int slots, nt, tiles, splits;
 };
-MoeWs moe_ws(int64_t T, int32_t topk, int64_t I) {
+DownPlan down_plan(int64_t T, int32_t topk, int32_t E, int64_t H, int64_t I) {
+  DownPlan d;
+  d.slots = T * topk > 2 * E ? 4 : 2;
+  d.nt = H >= 6144 && (T == 1 || d.slots == 2) ? 2 : 1;
+  d.tiles = int((H / 16 + d.nt - 1) / d.nt);
+  // workgroups for every CU, as long as a wave keeps two K units or more
+  const int64_t units = std::min<int64_t>(T * topk, E) * (I / 128) / 16;
+  d.splits = int(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(256 / d.tiles, units / 2), 16)));
+  return d;
+}
+
+// Workspace: the activations (high and low rows of every routed entry), the passes, their number, the
+// splits' sums and arrival counts.
+struct MoeWs {
+  size_t passes, count, partial, arrived, total;
+};
+MoeWs moe_ws(const DownPlan& d, int64_t T, int32_t topk, int64_t I) {
   MoeWs w;
   w.passes = align256(size_t(T) * topk * I * 4);
   w.count = w.passes + align256(size_t(T) * topk * sizeof(Pass));
-  w.total = w.count + 256;
+  w.partial = w.count + 256;
+  w.arrived = w.partial + (d.splits > 1 ? align256(size_t(d.tiles) * d.splits * d.nt * T * 64) : 0);
+  w.total = w.arrived + (d.splits > 1 ? align256(size_t(d.tiles) * 4) : 0);
   return w;
 }
 
 template <int F>
 hipError_t moe_fmt(const MoeDecodeCall& m, hipStream_t s) {
-  const MoeWs ws = moe_ws(m.T, m.topk, m.I);
+  const DownPlan d = down_plan(m.T, m.topk, m.E, m.H, m.I);
+  const MoeWs ws = moe_ws(d, m.T, m.topk, m.I);
   uint8_t* base = static_cast<uint8_t*>(m.ws);
   uint16_t* act = reinterpret_cast<uint16_t*>(base);
-  MoeParams up{dec_weights(m.c, m.w_gate_up, 2 * m.I, m.H), static_cast<const uint16_t*>(m.x), m.topk_ids, m.topk_weights, act,
-               reinterpret_cast<Pass*>(base + ws.passes), reinterpret_cast<int*>(base + ws.count), m.T, m.topk, m.E,
-               int(2 * m.I), int(m.H), m.T * m.topk > 2 * m.E ? 4 : 2};
+  MoeParams up{};
+  up.W = dec_weights(m.c, m.w_gate_up, 2 * m.I, m.H);
+  up.x = static_cast<const uint16_t*>(m.x);
+  up.ids = m.topk_ids;
+  up.weights = m.topk_weights;
+  up.y = act;
+  up.passes = reinterpret_cast<Pass*>(base + ws.passes);
+  up.n_passes = reinterpret_cast<int*>(base + ws.count);
+  up.T = m.T;
+  up.topk = m.topk;
+  up.E = m.E;
+  up.N = int(2 * m.I);
+  up.K = int(m.H);
+  up.slots = d.slots;
+  up.tiles = d.tiles;
+  up.splits = d.splits;
+  up.partial = reinterpret_cast<float*>(base + ws.partial);
+  up.arrived = reinterpret_cast<uint32_t*>(base + ws.arrived);
   MoeParams down = up;
   down.W = dec_weights(m.c, m.w_down, m.H, m.I);
   down.x = act;
   down.y = static_cast<uint16_t*>(m.out);
   down.N = int(m.H);
   down.K = int(m.I);
-  hipError_t e = m.T == 1 ? launch_up<F, 1, 1, 8, 2>(up, s) : launch_up<F, 4, 2, 4, 2>(up, s);
+  const hipError_t e = m.T == 1 ? launch_up<F, 1, 1, 8, 2>(up, s) : launch_up<F, 4, 2, 4, 2>(up, s);
   if (e != hipSuccess) return e;
-  if (m.T == 1) return m.H >= 6144 ? launch_down<F, 2, 2, 16, 2>(down, s) : launch_down<F, 2, 1, 16, 3>(down, s);
-  if (up.slots == 4) return launch_down<F, 8, 1, 16, 2>(down, s);
-  return m.H >= 6144 ? launch_down<F, 6, 2, 16, 2>(down, s) : launch_down<F, 6, 1, 16, 3>(down, s);
+  if (m.T == 1) return d.nt == 2 ? launch_down<F, 2, 2, 16, 2>(down, s) : launch_down<F, 2, 1, 16, 3>(down, s);
+  if (d.slots == 4) return launch_down<F, 8, 1, 16, 2>(down, s);
+  return d.nt == 2 ? launch_down<F, 6, 2, 16, 2>(down, s) : launch_down<F, 6, 1, 16, 3>(down, s);
 }
 
 }  // namespace
 
-size_t moe_decode_ws_bytes(const Combo&, int64_t T, int32_t topk, int32_t, int64_t, int64_t I) {
-  return moe_ws(T, topk, I).total;
+size_t moe_decode_ws_bytes(const Combo&, int64_t T, int32_t topk, int32_t E, int64_t H, int64_t I) {
+  return moe_ws(down_plan(T, topk, E, H, I), T, topk, I).total;
 }
 
 hipError_t launch_moe_decode(const MoeDecodeCall& m, hipStream_t s) {

@@ -47,7 +47,9 @@ struct DecTraits {
   static constexpr int kUnit = kUnitBytes * kWLoads;   // code bytes of 16 channels x 128 k
   // bytes from one unit's scales to the next's
   static constexpr int kScaleStep = F == DF_MXFP4 ? 64 : kFine ? fine_meta_bytes(kG, kAsym) : 32;
-  static constexpr int kLoads = kWLoads + (kW8 ? 0 : 1) + (kAsym ? 1 : 0);   // vector loads per unit and tile
+  // vector loads per unit and tile; with CHAN, 8-bit weights' channel scales are among them
+  template <bool CHAN>
+  static constexpr int kLoads = kWLoads + (kW8 && !CHAN ? 0 : 1) + (kAsym ? 1 : 0);
 };
 
 // A layer's packed weights (one expert's, at w + e * expert_stride).
@@ -104,14 +106,15 @@ struct DecTile {
   rsrc_t codes, scales, zeros;
 };
 
-// Buffers over `tiles` tiles from tile nt on of the expert at w.
-template <int F>
+// Buffers over `tiles` tiles from tile nt on of the expert at w. CHAN: 8-bit weights' channel scales too.
+template <int F, bool CHAN = false>
 __device__ __forceinline__ DecTile<F> dec_tile(const DecW& W, const uint8_t* w, int nt, int tiles = 1) {
   using T = DecTraits<F>;
   DecTile<F> t;
   const size_t at = size_t(nt) * W.units;
   t.codes = dec_rsrc(w + at * T::kUnit, uint32_t(tiles) * W.units * T::kUnit);
   if constexpr (!T::kW8) t.scales = dec_rsrc(w + W.scales_off + at * T::kScaleStep, uint32_t(tiles) * W.units * T::kScaleStep);
+  else if constexpr (CHAN) t.scales = dec_rsrc(w + W.scales_off + size_t(nt) * 64, uint32_t(tiles) * 64);
   if constexpr (F == DF_G128Z) t.zeros = dec_rsrc(w + W.zeros_off + at * 8, uint32_t(tiles) * W.units * 8);
   return t;
 }
@@ -124,9 +127,10 @@ struct DecUnit {
   uint32_t z;
 };
 
-// Load unit u of a tile, counted from its buffers' start (live false: nothing is read).
-template <int F>
-__device__ __forceinline__ void dec_load(DecUnit<F>& v, const DecTile<F>& t, int u, bool live, int lane) {
+// Load unit u of a tile, counted from its buffers' start (live false: nothing is read). CHAN: 8-bit
+// weights' channel scales from the buffer's tile nt.
+template <int F, bool CHAN>
+__device__ __forceinline__ void dec_load(DecUnit<F>& v, const DecTile<F>& t, int u, int nt, bool live, int lane) {
   using T = DecTraits<F>;
   const uint32_t at = live ? uint32_t(u) * T::kUnit : kDecOutside - 16 * 64;
 #pragma unroll
@@ -149,6 +153,8 @@ __device__ __forceinline__ void dec_load(DecUnit<F>& v, const DecTile<F>& t, int
       v.z = __builtin_amdgcn_raw_buffer_load_b8(t.scales, int(ms + fine_scale_bytes(64) + n), 0, 0);
     else if constexpr (F == DF_G32Z)
       v.z = __builtin_amdgcn_raw_buffer_load_b16(t.scales, int(ms + fine_scale_bytes(32) + 2 * n), 0, 0);
+  } else if constexpr (CHAN) {
+    v.s[0] = __builtin_amdgcn_raw_buffer_load_b32(t.scales, int(live ? 64 * nt + 4 * (lane & 15) : kDecOutside - 4096), 0, 0);
   }
 }
 
@@ -234,15 +240,15 @@ constexpr int dec_wave_lds() { return D * dec_copies<AM>() * 1024; }
 //   tile(t)     the DecTile of its tile t                      (wave-uniform)
 //   unit(i, t)  its unit, counted from that tile's buffers' start (wave-uniform)
 //   row(i, r)   byte offset in `rows` of LDS row r's first k of the item (any lane's r)
-//   done(i)     called after item i's products were added
+//   done(i, units)  called after item i's products were added, with its units as loaded
 // Items past the last are asked for with i clamped to n - 1.
-template <int F, int AM, int NT, int D, class Item, class Tile, class Unit, class Row, class Done>
+template <int F, int AM, int NT, int D, bool CHAN = false, class Item, class Tile, class Unit, class Row, class Done>
 __device__ __forceinline__ void dec_stream(int n, rsrc_t rows, uint8_t* lds, int lane, f32x4 (&acc)[NT], Item&& item, Tile&& tile,
                                            Unit&& unit, Row&& row, Done&& done) {
   using T = DecTraits<F>;
   constexpr int ROWS = dec_rows<AM>();
   constexpr int NA = dec_copies<AM>();
-  constexpr int PER = NT * T::kLoads;          // vector loads per item
+  constexpr int PER = NT * T::template kLoads<CHAN>;   // vector loads per item
   static_assert(D * (PER + NA) < 64, "vmcnt range");
   if (n <= 0) return;
 
@@ -258,7 +264,7 @@ __device__ __forceinline__ void dec_stream(int n, rsrc_t rows, uint8_t* lds, int
       dec_lds_copy(rows, uint32_t(row(ic, r)) + 16 * c, lds + (j * NA + a) * 1024);
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) dec_load<F>(ring[j][t], tile(t), unit(ic, t), i < n, lane);
+    for (int t = 0; t < NT; ++t) dec_load<F, CHAN>(ring[j][t], tile(t), unit(ic, t), t, i < n, lane);
     // Keep the issue order as written, before the loop as in it: the wait before a slot's first use has to
     // hold for both ways into the loop, and with another order before it that would be a wait for everything.
     asm volatile("" ::: "memory");
@@ -286,7 +292,7 @@ __device__ __forceinline__ void dec_stream(int n, rsrc_t rows, uint8_t* lds, int
         dec_row_sums<F, AM>(af, rs);
 #pragma unroll
         for (int t = 0; t < NT; ++t) dec_mul<F, AM>(acc[t], af, rs, ring[j][t], lane);
-        done(i);
+        done(i, ring[j]);
       }
       if constexpr (MORE) {
         // every read of the slot's rows has completed before its next contents are asked for

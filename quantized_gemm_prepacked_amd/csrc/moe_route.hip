@@ -186,42 +186,51 @@ __global__ __launch_bounds__(kWaves * 64) void moe_route_kernel(RouteCall c) {
       v[i] = l[i] == ninf ? ninf64 : s[i] + double(b) + 0.0;
     }
 
-    // groups: keep the experts of the best ones
+    // groups: keep the experts of the best ones. LPG neighbouring lanes share a group (a power of two of
+    // them), going through its values in the wave's own LDS, then fold their largest two.
     uint64_t kept = ~uint64_t(0);
     const int per = c.E / c.n_group;
+    int lpg = 64;
     if (c.n_group > 1) {
-      // lane g: the sum of the largest group_top values of group g, from the wave's own LDS (each lane
-      // starts at another place, so that equal strides do not meet in one bank)
+      while (lpg * c.n_group > 64) lpg >>= 1;
       double* mine = group_v[wave];
 #pragma unroll
       for (int i = 0; i < VPL; ++i) mine[lane * VPL + i] = v[i];
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // written and read by this wave alone
+      const int g = lane / lpg;
       double a = ninf64, b = ninf64;   // the largest two
-      if (lane < c.n_group) {
-        int j = lane % per;
-        for (int n = 0; n < per; ++n) {
-          const double x = mine[lane * per + j];
+      if (g < c.n_group)
+        for (int j = lane % lpg; j < per; j += lpg) {
+          const double x = mine[g * per + j];
           b = fmax(b, fmin(a, x));
           a = fmax(a, x);
-          j = j + 1 == per ? 0 : j + 1;
         }
+      for (int o = 1; o < lpg; o <<= 1) {
+        const double oa = __shfl_xor(a, o), ob = __shfl_xor(b, o);
+        b = fmax(fmin(a, oa), fmax(b, ob));
+        a = fmax(a, oa);
       }
       const double value = a == ninf64 ? ninf64 : (c.group_top == 2 && b != ninf64 ? a + b : a) + 0.0;
       // kept: fewer than topk_group groups are better (ties: the lower one is)
       int better = 0;
-      for (int g = 0; g < c.n_group; ++g) {
-        const double other = lane_f64(value, g);
-        better += other > value || (other == value && g < lane);
+      for (int q = 0; q < c.n_group; ++q) {
+        const double other = lane_f64(value, q * lpg);
+        better += other > value || (other == value && q < g);
       }
-      kept = __ballot(lane < c.n_group && better < c.topk_group);
+      kept = __ballot(g < c.n_group && better < c.topk_group);   // bit lpg * g: group g
     }
 
     // the keys are the values' (bias) or still the logits' (groups alone)
     uint64_t by[VPL];
+    int group = lane * VPL / per, in_group = lane * VPL - group * per;   // of the lane's next expert
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = lane * VPL + i;
-      const bool in = e < c.E && v[i] != ninf64 && ((kept >> (c.n_group > 1 ? e / per : 0)) & 1);
+      const bool in = e < c.E && v[i] != ninf64 && ((kept >> (c.n_group > 1 ? group * lpg : 0)) & 1);
+      if (++in_group == per) {
+        in_group = 0;
+        ++group;
+      }
       by[i] = !in ? 0u : c.bias ? key_f64(v[i]) : uint64_t(key[i]);
     }
     for (int k = 0; k < c.topk; ++k) {

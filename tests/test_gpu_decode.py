@@ -278,7 +278,9 @@ def _ids(g, T, topk, E):
 
 @pytest.mark.parametrize("fmt", list(FORMATS))
 @pytest.mark.parametrize("T,topk,E,H,I", [(1, 1, 1, 128, 128), (1, 8, 16, 256, 384), (2, 2, 3, 384, 128), (3, 6, 8, 1152, 256),
-                                          (4, 4, 9, 256, 640), (5, 3, 4, 128, 256), (11, 2, 32, 256, 128), (16, 8, 8, 384, 256)])
+                                          (4, 4, 9, 256, 640), (5, 3, 4, 128, 256), (11, 2, 32, 256, 128), (16, 8, 8, 384, 256),
+                                          # the down products' items split over several workgroups
+                                          (1, 8, 16, 128, 1024), (4, 8, 20, 256, 512), (16, 4, 40, 128, 640), (16, 6, 6, 256, 896)])
 def test_moe_decode(fmt, T, topk, E, H, I):
     g = np.random.default_rng(2000 + T + H + I)
     L = Layer(2100 + T, fmt, E, H, I)
@@ -335,7 +337,7 @@ def test_moe_decode_tokens_do_not_mix(fmt, T):
 
 def test_moe_decode_is_repeatable_and_in_place():
     g = np.random.default_rng(2400)
-    L = Layer(2401, "int4_g128", 12, 512, 384)
+    L = Layer(2401, "int4_g128", 12, 512, 1408)
     for T in (1, 4, 16):
         x = synth.normal_bf16(g, (T, 512))
         ids, w = _ids(g, T, 4, 12), g.random((T, 4)).astype(np.float32)
@@ -395,7 +397,7 @@ def test_moe_decode_agrees_with_the_five_calls():
 def test_other_stream_and_graph():
     """On a stream of its own, and captured: replayed with new inputs, eager work between the replays."""
     g = np.random.default_rng(2700)
-    E, H, I, T, topk = 16, 256, 256, 3, 4
+    E, H, I, T, topk = 16, 256, 768, 3, 4      # the down launch splits its items
     L = Layer(2701, "uint4_g32", E, H, I)
     sh = random_weights(g, "uint4_g32", 2 * I, H)
     sh_dev = to_dev(prepack_host(L.desc, sh, 2 * I, H))
@@ -468,18 +470,18 @@ def test_decode_step():
 def test_two_streams_at_once():
     """Two calls in flight with a workspace each."""
     g = np.random.default_rng(2900)
-    L = Layer(2901, "int4_g128", 16, 512, 512)
+    L = Layer(2901, "int4_g128", 16, 512, 768)
     calls = []
     for k in range(2):
         x, ids, w = synth.normal_bf16(g, (4, 512)), _ids(g, 4, 4, 16), g.random((4, 4)).astype(np.float32)
-        n = hq.hq_moe_decode_workspace_bytes(L.desc, 4, 4, 16, 512, 512)
+        n = hq.hq_moe_decode_workspace_bytes(L.desc, 4, 4, 16, 512, 768)
         calls.append(dict(want=L.run(x, ids, w), x=to_dev(x.view(np.int16)), ids=to_dev(ids), w=to_dev(w), n=n,
                           ws=torch.empty(n, dtype=torch.uint8, device=DEV), out=torch.empty((4, 512), dtype=torch.int16, device=DEV),
                           stream=torch.cuda.Stream()))
     torch.cuda.synchronize()
     for _ in range(20):
         for c in calls:
-            hq.hq_moe_decode(L.desc, 4, 4, 16, 512, 512, c["x"], c["ids"], c["w"], L.gu_dev, L.dn_dev, c["out"], c["ws"], c["n"], c["stream"])
+            hq.hq_moe_decode(L.desc, 4, 4, 16, 512, 768, c["x"], c["ids"], c["w"], L.gu_dev, L.dn_dev, c["out"], c["ws"], c["n"], c["stream"])
     torch.cuda.synchronize()
     for c in calls:
         assert np.array_equal(_bits(c["out"]), c["want"])
