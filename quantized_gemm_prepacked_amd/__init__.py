@@ -318,6 +318,18 @@ def _bufs(*wanted):
     return out
 
 
+_packed_sizes = {}
+
+
+def _packed_bytes(desc, E, N, K):
+    """hq_decode_prepacked_bytes, worked out once per description and size."""
+    key = (bytes(desc), E, N, K)
+    n = _packed_sizes.get(key)
+    if n is None:
+        n = _packed_sizes[key] = hq_decode_prepacked_bytes(desc, E, N, K)
+    return n
+
+
 def hq_decode_prepacked_bytes(desc, E, N, K) -> int:
     return _c["hq_decode_prepacked_bytes"](_d(desc), E, N, K)
 
@@ -340,8 +352,7 @@ def hq_moe_route(score_fn, T, E, topk, logits, logits_fmt, bias, n_group, topk_g
 
 
 def hq_gemv(desc, op, M, N, K, x, w_packed, y, stream=None):
-    """The packed weights' size is the descriptor's (hq_decode_prepacked_bytes(desc, 1, N, K))."""
-    a, w, o = _bufs((x, 2 * M * K, "x"), (w_packed, 0, "w_packed"), (y, 2 * M * (N // 2 if op == HQ_GEMV_SILU_MUL else N), "y"))
+    a, w, o = _bufs((x, 2 * M * K, "x"), (w_packed, _packed_bytes(desc, 1, N, K), "w_packed"), (y, 2 * M * (N // 2 if op == HQ_GEMV_SILU_MUL else N), "y"))
     _check(_c["hq_gemv"](_d(desc), op, M, N, K, a, w, o, _stream(stream)))
 
 
@@ -352,6 +363,6 @@ def hq_moe_decode_workspace_bytes(desc, T, topk, E, H, I) -> int:
 def hq_moe_decode(desc, T, topk, E, H, I, x, topk_ids, topk_weights, w_gate_up, w_down, out, ws=None, ws_bytes=0,
                   stream=None):
     a, ids, w, gu, dn, o, s = _bufs((x, 2 * T * H, "x"), (topk_ids, 4 * T * topk, "topk_ids"),
-                                    (topk_weights, 4 * T * topk, "topk_weights"), (w_gate_up, 0, "w_gate_up"),
-                                    (w_down, 0, "w_down"), (out, 2 * T * H, "out"), (ws, ws_bytes, "ws"))
+                                    (topk_weights, 4 * T * topk, "topk_weights"), (w_gate_up, _packed_bytes(desc, E, 2 * I, H), "w_gate_up"),
+                                    (w_down, _packed_bytes(desc, E, H, I), "w_down"), (out, 2 * T * H, "out"), (ws, ws_bytes, "ws"))
     _check(_c["hq_moe_decode"](_d(desc), T, topk, E, H, I, a, ids, w, gu, dn, o, s, ws_bytes, _stream(stream)))

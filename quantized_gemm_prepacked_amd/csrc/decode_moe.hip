@@ -409,9 +409,11 @@ DownPlan down_plan(int64_t T, int32_t topk, int32_t E, int64_t H, int64_t I) {
   d.slots = T * topk > 2 * E ? 4 : 2;
   d.nt = H >= 6144 && (T == 1 || d.slots == 2) ? 2 : 1;
   d.tiles = int((H / 16 + d.nt - 1) / d.nt);
-  // workgroups for every CU, as long as a wave keeps two K units or more
+  // Few output tiles leave CUs idle: then several workgroups share a tile's items, as long as a wave keeps
+  // four units of distinct experts' weights (T = 16 top-8 of 128, 2048 x 768: 51 us as two, 57 as one; T = 4
+  // top-2 of 16, 2048 x 1024: 12.9 as two, with two units a wave, 12.2 as one).
   const int64_t units = std::min<int64_t>(T * topk, E) * (I / 128) / 16;
-  d.splits = int(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(256 / d.tiles, units / 2), 16)));
+  d.splits = int(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(256 / d.tiles, units / 4), 16)));
   return d;
 }
 

@@ -160,6 +160,22 @@ def test_gemv(fmt, M, N, K):
         check_float(got, ref, "gated", rounding_floor=True)
 
 
+@pytest.mark.parametrize("M,N,K,gated", [(1, 8208, 128, False), (4, 8208, 256, False), (16, 8208, 128, False),   # three tiles a workgroup
+                                         (16, 12304, 128, False), (9, 8224, 128, True),                      # four
+                                         (1, 64, 8192, True), (1, 4096, 2176, False), (1, 32, 16384, False)])
+@pytest.mark.parametrize("fmt", ["uint4_g128", "int4_g64", "uint4_g32", "mxfp4", "int8"])
+def test_gemv_workgroup_shapes(fmt, M, N, K, gated):
+    """Sizes that take the other tile counts, waves and ring depths."""
+    g = np.random.default_rng(1050 + N)
+    w = random_weights(g, fmt, N, K)
+    x = synth.normal_bf16(g, (M, K))
+    say(f"[gemv shapes] {fmt} M={M} N={N} K={K} gated={gated}")
+    got = _gemv(FORMATS[fmt][0], gated, x, to_dev(prepack_host(FORMATS[fmt][0], w, N, K)), N, K)
+    ref = oracle.ref_gemv(x, dequant(w, fmt), gated)
+    _check(got, ref, _gated_bound(x, w, fmt, N) if gated else product_bound(x, w, fmt), "shapes")
+    check_float(got, ref, "shapes", rounding_floor=True)
+
+
 def test_gemv_large():
     """The sizes a model has: a wide projection, sampled against the oracle."""
     g = np.random.default_rng(1100)
@@ -357,6 +373,53 @@ def test_moe_decode_large_sampled():
         ids, w = _ids(g, T, topk, 4), g.random((T, topk)).astype(np.float32)
         say(f"[moe decode large] T={T}")
         check_float(L.run(x, ids, w), L.ref(x, ids, w), f"T={T}")
+
+
+@pytest.mark.parametrize("fmt", ["uint4_g64", "mxfp4", "fp8"])
+@pytest.mark.parametrize("T,topk,E,H,I", [(16, 64, 64, 128, 128),      # the longest routing: 1024 entries, passes of four
+                                          (16, 32, 512, 128, 128),     # 512 experts, passes of two
+                                          (1, 64, 200, 256, 128),
+                                          (1, 2, 3, 6272, 128), (3, 2, 8, 6272, 256)])   # two output tiles a workgroup
+def test_moe_decode_workgroup_shapes(fmt, T, topk, E, H, I):
+    g = np.random.default_rng(2550 + T + topk)
+    L = Layer(2551, fmt, E, H, I)
+    x, ids = synth.normal_bf16(g, (T, H)), _ids(g, T, topk, E)
+    w = (g.random((T, topk)) / topk).astype(np.float32)
+    say(f"[moe decode shapes] {fmt} T={T} topk={topk} E={E} H={H} I={I}")
+    got, ref = L.run(x, ids, w), L.ref(x, ids, w)
+    _check(got, ref, L.bound(x, ids, w), "layer")
+    check_float(got, ref, "layer", rounding_floor=True)
+
+
+def test_moe_decode_long_lists():
+    """More than 64 (pass, K unit) items to a wave of the down launch."""
+    g = np.random.default_rng(2560)
+    T, topk, E, H, I = 16, 8, 8, 2176, 4352
+    L = Layer(2561, "int4_g128", E, H, I)
+    x, ids, w = synth.normal_bf16(g, (T, H)), _ids(g, T, topk, E), g.random((T, topk)).astype(np.float32)
+    check_float(L.run(x, ids, w), L.ref(x, ids, w), "long lists")
+
+
+def test_moe_decode_experts_past_4_gib():
+    """Expert offsets past 2^32 bytes: only the first and the last expert of 160 hold weights."""
+    E, H, I, fmt = 160, 7168, 2048, "int8"
+    desc, last = FORMATS[fmt][0], E - 1
+    L = Layer(2570, fmt, 2, H, I)
+    gu = torch.empty(hq.hq_decode_prepacked_bytes(desc, E, 2 * I, H), dtype=torch.uint8, device=DEV)
+    dn = torch.empty(hq.hq_decode_prepacked_bytes(desc, E, H, I), dtype=torch.uint8, device=DEV)
+    assert gu.numel() > 2 ** 32
+    for whole, two in ((gu, L.gu_dev), (dn, L.dn_dev)):
+        n = two.numel() // 2
+        assert whole.numel() == E * n
+        whole[:n], whole[last * n:] = two[:n], two[n:]
+    g = np.random.default_rng(2571)
+    for T in (1, 3):
+        x, w = synth.normal_bf16(g, (T, H)), g.random((T, 2)).astype(np.float32)
+        ids = np.array([[last, 0], [0, -1], [last, last]], np.int32)[:T]
+        ref = L.ref(x, np.where(ids == last, 1, ids), w)
+        L2 = Layer.__new__(Layer)
+        L2.fmt, L2.desc, L2.E, L2.H, L2.I, L2.gu_dev, L2.dn_dev = fmt, desc, E, H, I, gu, dn
+        check_float(L2.run(x, ids, w), ref, f"past 4 GiB T={T}")
 
 
 def test_moe_decode_agrees_with_the_five_calls():
