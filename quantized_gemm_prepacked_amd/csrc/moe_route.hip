@@ -13,7 +13,8 @@
 //
 // Bound by latency: one wave's chain of k wave-wide maxima, each six data-parallel moves inside the
 // vector unit and one lane read (through LDS shuffles of 64-bit values and ids the same selection took
-// twice as long).
+// twice as long). A lane's values are sorted once, so that a maximum looks at its first only and the
+// winner moves up by one; of 64-bit keys the low halves are compared only where the high halves tie.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -83,13 +84,93 @@ __device__ __forceinline__ int best_lane(uint32_t key, uint32_t& best) {
 }
 __device__ __forceinline__ int best_lane(uint64_t key, uint64_t& best) {
   const uint32_t hi = wave_max(uint32_t(key >> 32));
-  const bool top = uint32_t(key >> 32) == hi;
-  const uint32_t lo = wave_max(top ? uint32_t(key) : 0u);
+  const uint64_t top = __ballot(uint32_t(key >> 32) == hi);
+  int lane = __builtin_ctzll(top);
+  uint32_t lo;
+  if ((top & (top - 1)) == 0) {
+    lo = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(key)), lane));
+  } else {
+    lo = wave_max(uint32_t(key >> 32) == hi ? uint32_t(key) : 0u);
+    lane = __builtin_ctzll(__ballot(key == (uint64_t(hi) << 32 | lo)));
+  }
   best = uint64_t(hi) << 32 | lo;
-  return __builtin_ctzll(__ballot(key == best));
+  return lane;
 }
 
-// exp(l - top), 1 where both are infinite.
+// A lane's keys in falling order with their places, equal ones in the order of their places (only
+// neighbours are exchanged, and only where the later is larger).
+template <int VPL, class K>
+__device__ __forceinline__ void sort_keys(K (&key)[VPL], int (&place)[VPL]) {
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) place[i] = i;
+#pragma unroll
+  for (int n = VPL - 1; n > 0; --n)
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const bool swap = key[i + 1] > key[i];
+      const K a = key[i], b = key[i + 1];
+      const int pa = place[i], pb = place[i + 1];
+      key[i] = swap ? b : a;
+      key[i + 1] = swap ? a : b;
+      place[i] = swap ? pb : pa;
+      place[i + 1] = swap ? pa : pb;
+    }
+}
+
+// A lane's keys as one sorted list, or (eight of them, for which sorting costs more than it saves) two of
+// the lower and the upper places.
+template <int VPL, class K>
+struct LaneKeys {
+  static constexpr int kLists = VPL > 4 ? 2 : 1, kLen = VPL / kLists;
+  K key[kLists][kLen];
+  int place[kLists][kLen];
+  __device__ __forceinline__ explicit LaneKeys(const K (&from)[VPL]) {
+#pragma unroll
+    for (int h = 0; h < kLists; ++h) {
+#pragma unroll
+      for (int i = 0; i < kLen; ++i) key[h][i] = from[h * kLen + i];
+      sort_keys<kLen, K>(key[h], place[h]);
+    }
+  }
+  __device__ __forceinline__ bool upper() const { return kLists == 2 && key[kLists - 1][0] > key[0][0]; }
+  __device__ __forceinline__ K head() const { return upper() ? key[kLists - 1][0] : key[0][0]; }
+  __device__ __forceinline__ int head_place() const { return upper() ? place[kLists - 1][0] + kLen : place[0][0]; }
+  __device__ __forceinline__ void drop(bool yes) {
+    const bool up = upper();
+#pragma unroll
+    for (int h = 0; h < kLists; ++h) {
+      const bool mine = yes && up == (h == 1);
+#pragma unroll
+      for (int i = 0; i + 1 < kLen; ++i) {
+        key[h][i] = mine ? key[h][i + 1] : key[h][i];
+        place[h][i] = mine ? place[h][i + 1] : place[h][i];
+      }
+      key[h][kLen - 1] = mine ? K(0) : key[h][kLen - 1];
+    }
+  }
+};
+
+// The topk largest keys of the wave in order, keys of 0 left out: lane k gets the k-th one's id, -1 where
+// there is none. first: the largest.
+template <int VPL, class K>
+__device__ __forceinline__ int choose(const K (&key)[VPL], int topk, int lane, K& first) {
+  LaneKeys<VPL, K> keys(key);
+  int id = -1;
+  first = 0;
+  for (int k = 0; k < topk; ++k) {
+    K best;
+    const int from = best_lane(keys.head(), best);
+    if (best == 0) break;
+    if (k == 0) first = best;
+    const int at = __builtin_amdgcn_readlane(keys.head_place(), from);
+    if (lane == k) id = from * VPL + at;
+    keys.drop(lane == from);
+  }
+  return id;
+}
+
+// exp(l - top), 1 where both are +infinity, 0 at l = -infinity. (With nothing but switched-off logits top is
+// NaN and so is every value: the sums are then not above 0, which gives weights of 0.)
 __device__ __forceinline__ double exp_below(float l, float top) { return l == top ? 1.0 : exp(double(l) - double(top)); }
 __device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-double(l))); }
 
@@ -104,56 +185,47 @@ __global__ __launch_bounds__(kWaves * 64) void moe_route_kernel(RouteCall c) {
   const float ninf = -__builtin_huge_valf();
   const double ninf64 = -__builtin_huge_val();
 
-  // logits; NaN counts as -infinity, the value of a switched-off expert; -0 as +0
+  // logits; NaN counts as -infinity, the value of a switched-off expert; -0 as +0. Every lane loads (the
+  // last expert again past the end), so that the loads stand together and are waited for once.
   float l[VPL];
   uint32_t key[VPL];   // 0: switched off
   uint32_t most = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const int e = lane * VPL + i;
-    float f = ninf;
-    if (e < c.E) {
-      const size_t at = size_t(t) * c.E + e;
-      f = BF16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(c.logits)[at]) : static_cast<const float*>(c.logits)[at];
-      f = f != f ? ninf : f + 0.0f;
-    }
-    l[i] = f;
-    key[i] = f == ninf ? 0u : key_f32(f);
+    const size_t at = size_t(t) * c.E + min(lane * VPL + i, c.E - 1);
+    l[i] = BF16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(c.logits)[at]) : static_cast<const float*>(c.logits)[at];
+  }
+  float bias[VPL];
+  if constexpr (!PLAIN) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) bias[i] = c.bias ? c.bias[min(lane * VPL + i, c.E - 1)] : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    l[i] = lane * VPL + i >= c.E || l[i] != l[i] ? ninf : l[i] + 0.0f;
+    key[i] = l[i] == ninf ? 0u : key_f32(l[i]);
     most = max(most, key[i]);
   }
   const bool sigmoid = c.score_fn == HQ_SCORE_SIGMOID;
 
-  int my_id = -1;      // lane k: the k-th choice
+  int my_id;           // lane k: the k-th choice, -1: none
   double my_s = 0.0;   // and its score
   if constexpr (PLAIN) {
-    uint32_t my_key = 0, first = 0;
-    for (int k = 0; k < c.topk; ++k) {
-      uint32_t m = key[0], best;
+    uint32_t first;
+    my_id = choose<VPL>(key, c.topk, lane, first);
+    // the chosen logits, from the lanes that hold them
+    float mine = 0.f;
 #pragma unroll
-      for (int i = 1; i < VPL; ++i) m = max(m, key[i]);
-      const int from = best_lane(m, best);
-      if (best == 0) break;
-      if (k == 0) first = best;
-      int place = VPL - 1;
-#pragma unroll
-      for (int i = VPL - 2; i >= 0; --i) place = key[i] == best ? i : place;
-      const int at = __builtin_amdgcn_readlane(place, from);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = lane == from && i == at ? 0u : key[i];
-      if (lane == k) {
-        my_id = from * VPL + at;
-        my_key = best;
-      }
+    for (int i = 0; i < VPL; ++i) {
+      const float x = __shfl(l[i], max(my_id, 0) / VPL);
+      mine = my_id % VPL == i ? x : mine;
     }
-    if (my_id >= 0) {
-      const float mine = f32_of_key(my_key);
-      my_s = sigmoid ? sigmoid64(mine) : exp_below(mine, f32_of_key(first));
-    }
+    if (my_id >= 0) my_s = sigmoid ? sigmoid64(mine) : exp_below(mine, f32_of_key(first));
     if (!sigmoid && !c.renormalize) {   // renormalised, the sum over all experts cancels
       const float top = f32_of_key(first);
       double sum = 0.0;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) sum += l[i] == ninf ? 0.0 : exp_below(l[i], top);
+      for (int i = 0; i < VPL; ++i) sum += exp_below(l[i], top);
       sum = wave_sum(sum);
       my_s = sum > 0.0 ? my_s / sum : 0.0;
     }
@@ -162,13 +234,13 @@ __global__ __launch_bounds__(kWaves * 64) void moe_route_kernel(RouteCall c) {
     double s[VPL], v[VPL];
     if (sigmoid) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) s[i] = l[i] == ninf ? 0.0 : sigmoid64(l[i]);
+      for (int i = 0; i < VPL; ++i) s[i] = sigmoid64(l[i]);   // 0 at -infinity
     } else {
       const float top = f32_of_key(wave_max(most));
       double sum = 0.0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        s[i] = l[i] == ninf ? 0.0 : exp_below(l[i], top);
+        s[i] = exp_below(l[i], top);
         sum += s[i];
       }
       sum = wave_sum(sum);
@@ -177,12 +249,7 @@ __global__ __launch_bounds__(kWaves * 64) void moe_route_kernel(RouteCall c) {
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int e = lane * VPL + i;
-      float b = 0.0f;
-      if (c.bias && e < c.E) {
-        b = c.bias[e];
-        if (b != b) b = ninf;
-      }
+      const float b = bias[i] != bias[i] ? ninf : bias[i];
       v[i] = l[i] == ninf ? ninf64 : s[i] + double(b) + 0.0;
     }
 
@@ -233,27 +300,12 @@ __global__ __launch_bounds__(kWaves * 64) void moe_route_kernel(RouteCall c) {
       }
       by[i] = !in ? 0u : c.bias ? key_f64(v[i]) : uint64_t(key[i]);
     }
-    for (int k = 0; k < c.topk; ++k) {
-      uint64_t m = by[0], best;
+    uint64_t first;
+    my_id = choose<VPL>(by, c.topk, lane, first);
 #pragma unroll
-      for (int i = 1; i < VPL; ++i) m = by[i] > m ? by[i] : m;
-      const int from = best_lane(m, best);
-      if (best == 0) break;
-      int place = VPL - 1;
-      double sv = s[VPL - 1];
-#pragma unroll
-      for (int i = VPL - 2; i >= 0; --i) {
-        place = by[i] == best ? i : place;
-        sv = by[i] == best ? s[i] : sv;
-      }
-      const int at = __builtin_amdgcn_readlane(place, from);
-      sv = lane_f64(sv, from);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) by[i] = lane == from && i == at ? 0u : by[i];
-      if (lane == k) {
-        my_id = from * VPL + at;
-        my_s = sv;
-      }
+    for (int i = 0; i < VPL; ++i) {
+      const double x = __shfl(s[i], max(my_id, 0) / VPL);
+      if (my_id >= 0 && my_id % VPL == i) my_s = x;
     }
   }
   if (c.renormalize) {
