@@ -134,21 +134,23 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeParams p) {
       return;
     }
     --f;
-    e = p.ids[f];
-    if (!moe_valid(e, p.E)) return;
+    // lane t looks through token t's ids, eight loads at a time; the first eight are asked for together with
+    // the entry's own
+    const int32_t* row = p.ids + min(lane, p.T - 1) * p.topk;
+    int32_t id[8];
     entry = -1;
-    {
-      const int32_t* row = p.ids + min(lane, p.T - 1) * p.topk;
-      for (int j = 0; j < p.topk; j += 8) {   // eight loads at a time
-        int32_t id[8];
+    for (int j = 0; j < p.topk; j += 8) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) id[q] = row[min(j + q, p.topk - 1)];
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (id[q] == e && entry < 0) entry = min(j + q, p.topk - 1);
+      for (int q = 0; q < 8; ++q) id[q] = row[min(j + q, p.topk - 1)];
+      if (j == 0) {
+        e = p.ids[f];
+        if (!moe_valid(e, p.E)) return;
       }
-      entry = entry >= 0 && lane < p.T ? lane * p.topk + entry : -1;
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (id[q] == e && entry < 0) entry = min(j + q, p.topk - 1);
     }
+    entry = entry >= 0 && lane < p.T ? lane * p.topk + entry : -1;
     tokens = uint32_t(__ballot(entry >= 0));
     if (__builtin_amdgcn_readlane(entry, __builtin_ctz(tokens)) != f) return;
     slots = __builtin_popcount(tokens);
@@ -261,9 +263,10 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeParams p) {
       s.weight[0] = p.weights ? p.weights[lane] : 1.0f;
     }
   } else {
-    count = __builtin_amdgcn_readfirstlane(*p.n_passes);
+    // all P places, not the count's, so that the two loads do not wait for each other
     const u32x4* from = reinterpret_cast<const u32x4*>(p.passes);
-    for (int q = threadIdx.x; q < count * 2; q += NW * 64) reinterpret_cast<u32x4*>(passes)[q] = from[q];
+    for (int q = threadIdx.x; q < P * 2; q += NW * 64) reinterpret_cast<u32x4*>(passes)[q] = from[q];
+    count = __builtin_amdgcn_readfirstlane(*p.n_passes);
     for (int q = threadIdx.x; q < NW * NT * p.T * 16; q += NW * 64) sums[q] = 0.f;
   }
   __syncthreads();
