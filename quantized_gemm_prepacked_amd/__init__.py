@@ -298,24 +298,22 @@ def hq_moe_combine(T, topk, E, N, topk_ids, y, out, stream=None):
 
 
 # ---- decode step ------------------------------------------------------------------------------
-def _bufs(*wanted):
-    """Device addresses of a decode call's buffers, given as (tensor, bytes needed, name) each. A tensor has
-    to be contiguous, on the current device and as large as the call reads or writes: what the C side
-    cannot see, and would go past. Addresses (int) and None pass through."""
-    out, dev = [], -2
-    for x, nbytes, what in wanted:
-        if x is not None and x.__class__ is not int:
-            if dev == -2 and x.is_cuda:
-                dev = torch.cuda.current_device()
-            if not x.is_contiguous():
-                raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} must be contiguous")
-            if x.nbytes < nbytes:
-                raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} holds {x.nbytes} bytes, {nbytes} are needed")
-            if not x.is_cuda or x.get_device() != dev:
-                raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} must be on the current device")
-            x = x.data_ptr()
-        out.append(x)
-    return out
+def _here():
+    """The current device, -2 where there is none yet."""
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+
+
+def _at(x, nbytes, dev, what):
+    """Device address of a decode call's buffer. A tensor has to be contiguous, on the current device and as
+    large as the call reads or writes: what the C side cannot see, and would go past. Addresses (int) and
+    None pass through."""
+    if x is None or x.__class__ is int:
+        return x
+    if x.nbytes < nbytes or not x.is_contiguous() or x.get_device() != dev:
+        why = (f"holds {x.nbytes} bytes, {nbytes} are needed" if x.nbytes < nbytes else
+               "must be contiguous" if not x.is_contiguous() else "must be on the current device")
+        raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} {why}")
+    return x.data_ptr()
 
 
 _packed_sizes = {}
@@ -345,15 +343,18 @@ def hq_decode_prepack_weights(desc, E, N, K, wq: np.ndarray, scales: np.ndarray,
 
 def hq_moe_route(score_fn, T, E, topk, logits, logits_fmt, bias, n_group, topk_group, group_top, renormalize, scale,
                  topk_ids, topk_weights, stream=None):
-    l, b, ids, w = _bufs((logits, T * E * (2 if logits_fmt == HQ_LOGITS_BF16 else 4), "logits"), (bias, 4 * E, "bias"),
-                         (topk_ids, 4 * T * topk, "topk_ids"), (topk_weights, 4 * T * topk, "topk_weights"))
-    _check(_c["hq_moe_route"](score_fn, T, E, topk, l, logits_fmt, b, n_group, topk_group, group_top, int(renormalize), scale,
-                              ids, w, _stream(stream)))
+    dev = _here()
+    _check(_c["hq_moe_route"](score_fn, T, E, topk, _at(logits, T * E * (2 if logits_fmt == HQ_LOGITS_BF16 else 4), dev, "logits"),
+                              logits_fmt, _at(bias, 4 * E, dev, "bias"), n_group, topk_group, group_top, int(renormalize), scale,
+                              _at(topk_ids, 4 * T * topk, dev, "topk_ids"), _at(topk_weights, 4 * T * topk, dev, "topk_weights"),
+                              _stream(stream)))
 
 
 def hq_gemv(desc, op, M, N, K, x, w_packed, y, stream=None):
-    a, w, o = _bufs((x, 2 * M * K, "x"), (w_packed, _packed_bytes(desc, 1, N, K), "w_packed"), (y, 2 * M * (N // 2 if op == HQ_GEMV_SILU_MUL else N), "y"))
-    _check(_c["hq_gemv"](_d(desc), op, M, N, K, a, w, o, _stream(stream)))
+    dev = _here()
+    _check(_c["hq_gemv"](_d(desc), op, M, N, K, _at(x, 2 * M * K, dev, "x"),
+                         _at(w_packed, _packed_bytes(desc, 1, N, K), dev, "w_packed"),
+                         _at(y, 2 * M * (N // 2 if op == HQ_GEMV_SILU_MUL else N), dev, "y"), _stream(stream)))
 
 
 def hq_moe_decode_workspace_bytes(desc, T, topk, E, H, I) -> int:
@@ -362,7 +363,9 @@ def hq_moe_decode_workspace_bytes(desc, T, topk, E, H, I) -> int:
 
 def hq_moe_decode(desc, T, topk, E, H, I, x, topk_ids, topk_weights, w_gate_up, w_down, out, ws=None, ws_bytes=0,
                   stream=None):
-    a, ids, w, gu, dn, o, s = _bufs((x, 2 * T * H, "x"), (topk_ids, 4 * T * topk, "topk_ids"),
-                                    (topk_weights, 4 * T * topk, "topk_weights"), (w_gate_up, _packed_bytes(desc, E, 2 * I, H), "w_gate_up"),
-                                    (w_down, _packed_bytes(desc, E, H, I), "w_down"), (out, 2 * T * H, "out"), (ws, ws_bytes, "ws"))
-    _check(_c["hq_moe_decode"](_d(desc), T, topk, E, H, I, a, ids, w, gu, dn, o, s, ws_bytes, _stream(stream)))
+    dev = _here()
+    _check(_c["hq_moe_decode"](_d(desc), T, topk, E, H, I, _at(x, 2 * T * H, dev, "x"), _at(topk_ids, 4 * T * topk, dev, "topk_ids"),
+                               _at(topk_weights, 4 * T * topk, dev, "topk_weights"),
+                               _at(w_gate_up, _packed_bytes(desc, E, 2 * I, H), dev, "w_gate_up"),
+                               _at(w_down, _packed_bytes(desc, E, H, I), dev, "w_down"), _at(out, 2 * T * H, dev, "out"),
+                               _at(ws, ws_bytes, dev, "ws"), ws_bytes, _stream(stream)))

@@ -3,16 +3,21 @@
 //   up     act[t, j] = silu(Wg x[t]) * (Wu x[t]) for every routed entry (t, j)
 //   down   out[t] = sum_j weight[t, j] * Wd act[t, j]
 //
-// Both stream expert weights through decode_ops.h. With few tokens an expert is hit by one or a few of
-// them, so an expert's weights are read once for up to four of its tokens (a pass); more tokens on
-// one expert take further passes, whose weights come from the caches.
-// One token: a pass is a routed entry; ids outside [0, E) are left out. More: the up launch's first
-// workgroups find an expert's tokens themselves (one lane per token looks through its own row of
-// ids), and one extra workgroup writes the list of all passes that the down launch goes through.
+// Both stream expert weights through decode_ops.h, and reading them is what bounds them: at T = 1, 8 of
+// 32 experts of 7168 x 2048 INT4, up reads 121 MB at 6.1 TB/s and down 61 MB at 4.7 (a 2 GiB copy moves 4.9
+// TB/s on this card); at T = 16, 41 experts of 4096 x 1536 in groups of 32, 5.2 and 4.7 TB/s with the vector
+// ALU half busy. Below some 20 MB the two launches' own time (about 4 us each) is most of it.
+// With few tokens an expert is hit by one or a few of them, so its weights are read once for up to four
+// of its tokens (a pass; in the down launch two, unless experts are shared widely); further tokens take
+// further passes, whose weights come from the caches.
+// One token: a pass is a routed entry; ids outside [0, E) are left out. More: the up launch's workgroups
+// find an expert's tokens themselves (one lane per token looks through its own row of ids), and one extra
+// workgroup writes the list of all passes that the down launch goes through.
 //
 // act stays between the launches as a high and a low bf16 (16 significant bits): the down product's A
 // operand has unused MFMA rows, so the low half costs no matrix instruction, and the activations'
-// rounding to 8 bits would otherwise be as large as the output's own.
+// rounding to 8 bits would otherwise be as large as the output's own (relative L2 against 64 bits 2.3e-3
+// with it, 1.6e-3 without: the output's rounding alone).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -236,11 +241,13 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeParams p) {
 
 // NT tiles of 16 outputs per workgroup; the items (pass, K unit) are cut into splits * NW equal contiguous
 // ranges, one per wave of the splits workgroups (blockIdx.y) of a tile. With more than one, each leaves its
-// sums in the workspace and the one that arrives last adds them, in split order. What a wave needs of an item -- its expert's address, its unit and pass, its
-// activation rows -- is worked out 64 items at a time, one per lane, and read back by lane: done item
-// by item on the scalar unit, which a CU's waves share, it took as long as the stream itself. AM = 2:
-// one token, passes = its valid entries. AM = 6, 8: passes of up to two or four tokens, sums per token
-// in LDS (a wave's own, so their order is the passes').
+// sums in the workspace and the one that arrives last adds them, in split order.
+// What a wave needs of an item -- its expert's address, its unit and pass, its activation rows -- is worked
+// out 64 items at a time, one per lane, and read back by lane: done item by item on the scalar unit, which
+// a CU's waves share, it took as long as the stream itself (T = 1, 7168 x 2048: 18.7 us against 17.8, and
+// 2048 x 768: 6.5 against 5.3, tile shapes alike).
+// AM = 2: one token, passes = its valid entries. AM = 6, 8: passes of up to two or four tokens, sums per
+// token in LDS (a wave's own, so their order is the passes').
 template <int F, int AM, int NT, int NW, int D>
 __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeParams p) {
   constexpr int RS = dec_rows<AM>() / 2;   // act rows (high and low) of an item
@@ -435,6 +442,15 @@ MoeWs moe_ws(const DownPlan& d, int64_t T, int32_t topk, int64_t I) {
   return w;
 }
 
+// Tile shapes (tiles or pairs x waves x ring depth), us at the sizes of decode's benchmark cases:
+//   up    T = 1: 1x8x2 20.4 at 7168 x 2048 and 5.5 at 2048 x 768 (1x8x4 21.7 / 5.8, 1x16x1 23.5 / 5.2);
+//         T > 1: 2x4x2 20.4 at T = 3, 4096 x 1408 and 53 at T = 16, 4096 x 1536 (1x8x4 25.9 / 91: with eight
+//         waves a wave has three or four units, and dead slots of the ring are a third of its loads)
+//   down  T = 1: 2x16x2 13.4 at 7168 x 2048 but 6.9 at 2048 x 768, where half the CUs have no tile; 1x16x3
+//         16.7 and 5.0 -- so two tiles a workgroup from H = 6144 on, where there are 192 workgroups
+//         T > 1: 1x16x3 12.4 and 33 (2x16x2 16.3 / 48.6); with H = 7168 2x16x2 (T = 16 top-8 of 64: 253
+//         against 269 for both launches); passes of four tokens where an expert has over two on average (T = 16
+//         top-2 of 8, 4096 x 14336: 194 against 219 with passes of two)
 template <int F>
 hipError_t moe_fmt(const MoeDecodeCall& m, hipStream_t s) {
   const DownPlan d = down_plan(m.T, m.topk, m.E, m.H, m.I);

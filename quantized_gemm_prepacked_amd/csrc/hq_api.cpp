@@ -551,6 +551,7 @@ hq_status hq_decode_prepack_weights(const hq_quant_desc* desc, int64_t E, int64_
   if (c.asym != (zeros != nullptr))
     return fail(HQ_ERR_INVALID_ARGUMENT, c.asym ? "zeros must be non-NULL for UINT4_ASYM" : "zeros must be NULL without zero-points");
   const size_t need = hq::decode_prepacked_bytes(c, E, N, K);
+  if (need == 0) return fail(HQ_ERR_UNSUPPORTED, "E=%lld N=%lld K=%lld: more bytes than a size_t counts", (long long)E, (long long)N, (long long)K);
   if (out_bytes < need) return fail(HQ_ERR_WORKSPACE, "out_bytes %zu < required %zu", out_bytes, need);
   hq::decode_prepack(c, E, N, K, wq, scales, zeros, out);
   return ok();

@@ -253,8 +253,9 @@ void pack_fine(const PackedLayout& L, int G, const uint8_t* wq, const uint16_t* 
 }  // namespace
 
 size_t decode_prepacked_bytes(const Combo& c, int64_t E, int64_t N, int64_t K) {
-  if (!c.fine_group) return prepacked_bytes(c, E, N, K);
-  return make_fine_layout(c.fine_group, c.asym, N, K).expert_stride * size_t(E);
+  const size_t stride = (c.fine_group ? make_fine_layout(c.fine_group, c.asym, N, K) : make_layout(c.fam, c.asym, N, K)).expert_stride;
+  size_t bytes;
+  return __builtin_mul_overflow(stride, size_t(E), &bytes) ? 0 : bytes;
 }
 
 void decode_prepack(const Combo& c, int64_t E, int64_t N, int64_t K, const void* wq, const void* scales,

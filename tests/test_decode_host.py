@@ -156,6 +156,15 @@ def test_descriptions():
     assert _status(hq.hq_gemm, hq.DESC_W4A16_ASYM_G32, 4, 256, 512, 16, None, 16, 16, stream=0) == UNS
 
 
+def test_prepack_size_overflow():
+    """More bytes than a size_t counts: no size, and nothing is written."""
+    huge = (65536, 1 << 30, 1 << 30)
+    for desc, *_ in FORMATS.values():
+        assert hq.hq_decode_prepacked_bytes(desc, *huge) == 0
+        z = np.zeros(1, np.uint8) if desc.has_zero_point else None
+        assert _status(hq.hq_decode_prepack_weights, desc, *huge, np.zeros(1, np.uint8), np.zeros(1, np.uint16), z, np.zeros(1, np.uint8)) == UNS
+
+
 def test_prepack_refusals():
     g = np.random.default_rng(6)
     w = random_weights(g, "uint4_g32", 32, 256)

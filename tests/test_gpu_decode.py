@@ -457,10 +457,11 @@ def test_moe_decode_agrees_with_the_five_calls():
 
 
 # ---- streams, graphs, the step as a whole -----------------------------------------------------
-def test_other_stream_and_graph():
+@pytest.mark.parametrize("T", [3, 16])
+def test_other_stream_and_graph(T):
     """On a stream of its own, and captured: replayed with new inputs, eager work between the replays."""
     g = np.random.default_rng(2700)
-    E, H, I, T, topk = 16, 256, 768, 3, 4      # the down launch splits its items
+    E, H, I, topk = 16, 256, 768, 4      # the down launch splits its items
     L = Layer(2701, "uint4_g32", E, H, I)
     sh = random_weights(g, "uint4_g32", 2 * I, H)
     sh_dev = to_dev(prepack_host(L.desc, sh, 2 * I, H))
