@@ -303,14 +303,16 @@ def _here():
     return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
 
 
-def _at(x, nbytes, dev, what):
-    """Device address of a decode call's buffer. A tensor has to be contiguous, on the current device and as
+def _at(x, count, size, dev, what):
+    """Device address of a decode call's buffer of `count` elements of `size` bytes (size 0: of any type,
+    count bytes). A tensor has to be contiguous, on the current device, of elements of that size and as
     large as the call reads or writes: what the C side cannot see, and would go past. Addresses (int) and
     None pass through."""
     if x is None or x.__class__ is int:
         return x
-    if x.nbytes < nbytes or not x.is_contiguous() or x.get_device() != dev:
-        why = (f"holds {x.nbytes} bytes, {nbytes} are needed" if x.nbytes < nbytes else
+    if x.nbytes < count * (size or 1) or (size and x.element_size() != size) or not x.is_contiguous() or x.get_device() != dev:
+        why = (f"has elements of {x.element_size()} bytes, not {size}" if size and x.element_size() != size else
+               f"holds {x.nbytes} bytes, {count * (size or 1)} are needed" if x.nbytes < count * (size or 1) else
                "must be contiguous" if not x.is_contiguous() else "must be on the current device")
         raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} {why}")
     return x.data_ptr()
@@ -343,18 +345,17 @@ def hq_decode_prepack_weights(desc, E, N, K, wq: np.ndarray, scales: np.ndarray,
 
 def hq_moe_route(score_fn, T, E, topk, logits, logits_fmt, bias, n_group, topk_group, group_top, renormalize, scale,
                  topk_ids, topk_weights, stream=None):
-    dev = _here()
-    _check(_c["hq_moe_route"](score_fn, T, E, topk, _at(logits, T * E * (2 if logits_fmt == HQ_LOGITS_BF16 else 4), dev, "logits"),
-                              logits_fmt, _at(bias, 4 * E, dev, "bias"), n_group, topk_group, group_top, int(renormalize), scale,
-                              _at(topk_ids, 4 * T * topk, dev, "topk_ids"), _at(topk_weights, 4 * T * topk, dev, "topk_weights"),
-                              _stream(stream)))
+    dev, n = _here(), T * topk
+    _check(_c["hq_moe_route"](score_fn, T, E, topk, _at(logits, T * E, 2 if logits_fmt == HQ_LOGITS_BF16 else 4, dev, "logits"),
+                              logits_fmt, _at(bias, E, 4, dev, "bias"), n_group, topk_group, group_top, int(renormalize), scale,
+                              _at(topk_ids, n, 4, dev, "topk_ids"), _at(topk_weights, n, 4, dev, "topk_weights"), _stream(stream)))
 
 
 def hq_gemv(desc, op, M, N, K, x, w_packed, y, stream=None):
     dev = _here()
-    _check(_c["hq_gemv"](_d(desc), op, M, N, K, _at(x, 2 * M * K, dev, "x"),
-                         _at(w_packed, _packed_bytes(desc, 1, N, K), dev, "w_packed"),
-                         _at(y, 2 * M * (N // 2 if op == HQ_GEMV_SILU_MUL else N), dev, "y"), _stream(stream)))
+    _check(_c["hq_gemv"](_d(desc), op, M, N, K, _at(x, M * K, 2, dev, "x"),
+                         _at(w_packed, _packed_bytes(desc, 1, N, K), 0, dev, "w_packed"),
+                         _at(y, M * (N // 2 if op == HQ_GEMV_SILU_MUL else N), 2, dev, "y"), _stream(stream)))
 
 
 def hq_moe_decode_workspace_bytes(desc, T, topk, E, H, I) -> int:
@@ -363,9 +364,9 @@ def hq_moe_decode_workspace_bytes(desc, T, topk, E, H, I) -> int:
 
 def hq_moe_decode(desc, T, topk, E, H, I, x, topk_ids, topk_weights, w_gate_up, w_down, out, ws=None, ws_bytes=0,
                   stream=None):
-    dev = _here()
-    _check(_c["hq_moe_decode"](_d(desc), T, topk, E, H, I, _at(x, 2 * T * H, dev, "x"), _at(topk_ids, 4 * T * topk, dev, "topk_ids"),
-                               _at(topk_weights, 4 * T * topk, dev, "topk_weights"),
-                               _at(w_gate_up, _packed_bytes(desc, E, 2 * I, H), dev, "w_gate_up"),
-                               _at(w_down, _packed_bytes(desc, E, H, I), dev, "w_down"), _at(out, 2 * T * H, dev, "out"),
-                               _at(ws, ws_bytes, dev, "ws"), ws_bytes, _stream(stream)))
+    dev, n = _here(), T * topk
+    _check(_c["hq_moe_decode"](_d(desc), T, topk, E, H, I, _at(x, T * H, 2, dev, "x"), _at(topk_ids, n, 4, dev, "topk_ids"),
+                               _at(topk_weights, n, 4, dev, "topk_weights"),
+                               _at(w_gate_up, _packed_bytes(desc, E, 2 * I, H), 0, dev, "w_gate_up"),
+                               _at(w_down, _packed_bytes(desc, E, H, I), 0, dev, "w_down"), _at(out, T * H, 2, dev, "out"),
+                               _at(ws, ws_bytes, 0, dev, "ws"), ws_bytes, _stream(stream)))

@@ -227,6 +227,10 @@ def test_buffers_are_checked():
     assert _status(hq.hq_gemv, G32, 0, 4, 256, 512, x.T, 16, 16, stream=0) == INV                     # not contiguous
     assert _status(hq.hq_gemv, G32, 0, 5, 256, 512, x, 16, 16, stream=0) == INV                       # four rows, five asked
     assert _status(hq.hq_moe_route, 0, 4, 512, 8, x, 0, None, 1, 1, 2, True, 1.0, 16, 16, stream=0) == INV   # bf16 held, fp32 asked
+    with pytest.raises(hq.HQError, match="topk_ids has elements of 8 bytes"):                         # torch's own index type
+        hq.hq_moe_decode(G32, 1, 8, 16, 256, 512, 16, torch.zeros(8, dtype=torch.int64), None, 16, 16, 16, 16, 1 << 20, stream=0)
+    with pytest.raises(hq.HQError, match="x has elements of 4 bytes"):
+        hq.hq_gemv(G32, 0, 4, 256, 512, x.float(), 16, 16, stream=0)
     w = torch.zeros(hq.hq_decode_prepacked_bytes(G32, 1, 256, 512) - 1, dtype=torch.uint8)
     with pytest.raises(hq.HQError, match="w_packed holds"):
         hq.hq_gemv(G32, 0, 4, 256, 512, 16, w, 16, stream=0)
