@@ -475,6 +475,9 @@ typedef enum {
  * layer's weights of N rows (E = 1), y bf16 [M, N] (or [M, N/2], see op). fp32 accumulation, one
  * rounding at the end (silu(g) * u never passes through bf16). Made for M of 1 to 16; more rows run
  * in blocks of 16 that each read the weights again. M <= 65536, N and K <= 2^24, M * N < 2^31.
+ * NaN or infinity in a row of x reaches that row of y only; INT4 products are formed from codes offset by
+ * 128 with the row's sum taken off, so there an infinity gives NaN (and a group's sums of activations
+ * above 2^113 may overflow where the exact ones would not).
  * x, w_packed and y 16-byte aligned; y must not overlap x. M == 0 is a no-op. No workspace.
  * ------------------------------------------------------------------------------------------- */
 hq_status hq_gemv(const hq_quant_desc* desc, int32_t op, int64_t M, int64_t N, int64_t K, const void* x,
@@ -488,7 +491,8 @@ hq_status hq_gemv(const hq_quant_desc* desc, int32_t op, int64_t M, int64_t N, i
  * act is kept to 16 significant bits (a high and a low bf16), out is rounded once; the five calls round
  * gate_up, act and each expert's output to bf16 on the way.
  * Entries whose id is outside [0, E) contribute nothing; a token with none left gets zeros. The same
- * expert may stand in a token's row more than once.
+ * expert may stand in a token's row more than once. NaN and infinity in x or topk_weights reach their own
+ * token's row of out only, as in hq_gemv.
  *   x             bf16 [T, H], out bf16 [T, H] (out may be x)
  *   topk_ids      int32 [T, topk], topk_weights fp32 [T, topk] or NULL (all 1)
  *   w_gate_up     E experts of 2I rows (I gate rows, then I up rows) by H, prepacked with desc
