@@ -110,6 +110,19 @@ def test_route_ties_take_the_lowest_id():
     assert ids.tolist() == [[0, 1, 2, 3], [5, 70, 299, 0]]
 
 
+@pytest.mark.parametrize("bias,n_group,topk_group", [(False, 1, 1), (True, 1, 1), (False, 4, 2)])
+def test_route_sigmoid_far_below_zero(bias, n_group, topk_group):
+    """Rows of nothing but logits whose exp(-l) binary64 does not hold, though it holds their sigmoids: the
+    weights are the scores' shares all the same. (At -720 a subnormal score has 35 bits left, so the check's
+    2^-24 of a weight stands.)"""
+    g = np.random.default_rng(450)
+    l = g.uniform(-720, -650, (6, 40)).astype(np.float32)
+    l[:3] = g.uniform(-720, -711, (3, 40))
+    l[5, 1:] = -np.inf
+    l[5, 0] = -715.0
+    _check_route(l, np.zeros(40, np.float32) if bias else None, "sigmoid", 5, False, n_group=n_group, topk_group=topk_group)
+
+
 def test_route_many_rows():
     g = np.random.default_rng(400)
     l = route_case(g, 5000, 128, True)
