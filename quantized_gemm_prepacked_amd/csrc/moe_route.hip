@@ -174,12 +174,11 @@ __device__ __forceinline__ int choose(const K (&key)[VPL], int topk, int lane, K
 // exp(l - top), 1 where both are +infinity, 0 at l = -infinity. (With nothing but switched-off logits top is
 // NaN and so is every value: the sums are then not above 0, which gives weights of 0.)
 __device__ __forceinline__ double exp_below(float l, float top) { return l == top ? 1.0 : exp(double(l) - double(top)); }
-// Below -700, where exp(-l) nears the end of binary64's range (709.78), the sigmoid is exp(l) to the last bit:
-// a row of nothing but such logits still has weights, down to exp's own end near -745.
+// From exp(-|l|), which cannot overflow: 1 / (1 + exp(-l)) would be 0 below -709.78, although the sigmoid is a
+// number of binary64 down to -745, and a row of nothing but such logits still has weights.
 __device__ __forceinline__ double sigmoid64(float l) {
-  const bool far = l < -700.0f;
-  const double e = exp(far ? double(l) : -double(l));
-  return far ? e : 1.0 / (1.0 + e);
+  const double e = exp(-fabs(double(l)));
+  return (l < 0.0f ? e : 1.0) / (1.0 + e);
 }
 
 // PLAIN: no bias and no groups.
