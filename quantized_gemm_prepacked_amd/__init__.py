@@ -303,16 +303,30 @@ def _here():
     return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
 
 
-def _at(x, count, size, dev, what):
-    """Device address of a decode call's buffer of `count` elements of `size` bytes (size 0: of any type,
-    count bytes). A tensor has to be contiguous, on the current device, of elements of that size and as
-    large as the call reads or writes: what the C side cannot see, and would go past. Addresses (int) and
-    None pass through."""
+# Element types of a decode call's buffers: size in bytes, then the tensor types that hold such values (the
+# first names them; bf16 also as its raw bits). _BYTES: packed weights and workspaces, of any type.
+_BF16 = (2, (torch.bfloat16, torch.int16, torch.uint16))
+_FP32 = (4, (torch.float32,))
+_INT32 = (4, (torch.int32,))
+_BYTES = (1, None)
+
+
+def _at(x, count, kind, dev, what):
+    """Device address of a decode call's buffer of `count` elements of a kind. A tensor has to hold that type,
+    be contiguous, on the current device and as large as the call reads or writes: what the C side cannot
+    see, and would misread or go past. Addresses (int), None and other objects with a data_ptr() pass
+    through unchecked."""
     if x is None or x.__class__ is int:
         return x
-    if x.nbytes < count * (size or 1) or (size and x.element_size() != size) or not x.is_contiguous() or x.get_device() != dev:
-        why = (f"has elements of {x.element_size()} bytes, not {size}" if size and x.element_size() != size else
-               f"holds {x.nbytes} bytes, {count * (size or 1)} are needed" if x.nbytes < count * (size or 1) else
+    if not isinstance(x, torch.Tensor):
+        if isinstance(x, np.ndarray):
+            raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} is a host array")
+        return _ptr(x)
+    size, types = kind
+    if (types and x.dtype not in types) or x.nbytes < count * size or not x.is_contiguous() or x.get_device() != dev:
+        why = (f"has elements of {x.element_size()} bytes, not {size}" if types and x.element_size() != size else
+               f"holds {x.dtype}, not {types[0]}" if types and x.dtype not in types else
+               f"holds {x.nbytes} bytes, {count * size} are needed" if x.nbytes < count * size else
                "must be contiguous" if not x.is_contiguous() else "must be on the current device")
         raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} {why}")
     return x.data_ptr()
@@ -346,16 +360,16 @@ def hq_decode_prepack_weights(desc, E, N, K, wq: np.ndarray, scales: np.ndarray,
 def hq_moe_route(score_fn, T, E, topk, logits, logits_fmt, bias, n_group, topk_group, group_top, renormalize, scale,
                  topk_ids, topk_weights, stream=None):
     dev, n = _here(), T * topk
-    _check(_c["hq_moe_route"](score_fn, T, E, topk, _at(logits, T * E, 2 if logits_fmt == HQ_LOGITS_BF16 else 4, dev, "logits"),
-                              logits_fmt, _at(bias, E, 4, dev, "bias"), n_group, topk_group, group_top, int(renormalize), scale,
-                              _at(topk_ids, n, 4, dev, "topk_ids"), _at(topk_weights, n, 4, dev, "topk_weights"), _stream(stream)))
+    _check(_c["hq_moe_route"](score_fn, T, E, topk, _at(logits, T * E, _BF16 if logits_fmt == HQ_LOGITS_BF16 else _FP32, dev, "logits"),
+                              logits_fmt, _at(bias, E, _FP32, dev, "bias"), n_group, topk_group, group_top, int(renormalize), scale,
+                              _at(topk_ids, n, _INT32, dev, "topk_ids"), _at(topk_weights, n, _FP32, dev, "topk_weights"), _stream(stream)))
 
 
 def hq_gemv(desc, op, M, N, K, x, w_packed, y, stream=None):
     dev = _here()
-    _check(_c["hq_gemv"](_d(desc), op, M, N, K, _at(x, M * K, 2, dev, "x"),
-                         _at(w_packed, _packed_bytes(desc, 1, N, K), 0, dev, "w_packed"),
-                         _at(y, M * (N // 2 if op == HQ_GEMV_SILU_MUL else N), 2, dev, "y"), _stream(stream)))
+    _check(_c["hq_gemv"](_d(desc), op, M, N, K, _at(x, M * K, _BF16, dev, "x"),
+                         _at(w_packed, _packed_bytes(desc, 1, N, K), _BYTES, dev, "w_packed"),
+                         _at(y, M * (N // 2 if op == HQ_GEMV_SILU_MUL else N), _BF16, dev, "y"), _stream(stream)))
 
 
 def hq_moe_decode_workspace_bytes(desc, T, topk, E, H, I) -> int:
@@ -365,8 +379,8 @@ def hq_moe_decode_workspace_bytes(desc, T, topk, E, H, I) -> int:
 def hq_moe_decode(desc, T, topk, E, H, I, x, topk_ids, topk_weights, w_gate_up, w_down, out, ws=None, ws_bytes=0,
                   stream=None):
     dev, n = _here(), T * topk
-    _check(_c["hq_moe_decode"](_d(desc), T, topk, E, H, I, _at(x, T * H, 2, dev, "x"), _at(topk_ids, n, 4, dev, "topk_ids"),
-                               _at(topk_weights, n, 4, dev, "topk_weights"),
-                               _at(w_gate_up, _packed_bytes(desc, E, 2 * I, H), 0, dev, "w_gate_up"),
-                               _at(w_down, _packed_bytes(desc, E, H, I), 0, dev, "w_down"), _at(out, T * H, 2, dev, "out"),
-                               _at(ws, ws_bytes, 0, dev, "ws"), ws_bytes, _stream(stream)))
+    _check(_c["hq_moe_decode"](_d(desc), T, topk, E, H, I, _at(x, T * H, _BF16, dev, "x"), _at(topk_ids, n, _INT32, dev, "topk_ids"),
+                               _at(topk_weights, n, _FP32, dev, "topk_weights"),
+                               _at(w_gate_up, _packed_bytes(desc, E, 2 * I, H), _BYTES, dev, "w_gate_up"),
+                               _at(w_down, _packed_bytes(desc, E, H, I), _BYTES, dev, "w_down"), _at(out, T * H, _BF16, dev, "out"),
+                               _at(ws, ws_bytes, _BYTES, dev, "ws"), ws_bytes, _stream(stream)))

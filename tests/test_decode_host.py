@@ -238,3 +238,38 @@ def test_buffers_are_checked():
         hq.hq_moe_decode(G32, 1, 8, 16, 256, 512, 16, 16, None, 16, w, 16, 16, 1 << 20, stream=0)
     ws = torch.zeros(8, dtype=torch.uint8)
     assert _status(hq.hq_moe_decode, G32, 1, 8, 16, 256, 512, 16, 16, None, 16, 16, 16, ws, 1 << 20, stream=0) == INV
+
+
+def test_types_of_the_same_size_are_refused():
+    """fp16 for bf16 and int32 for fp32 have the right size and the wrong values."""
+    h, i = torch.zeros((4, 512), dtype=torch.float16), torch.zeros((4, 512), dtype=torch.int32)
+    for call, what in ((lambda: hq.hq_gemv(G32, 0, 4, 256, 512, h, 16, 16, stream=0), "x"),
+                       (lambda: hq.hq_gemv(G32, 0, 4, 256, 512, 16, 16, h, stream=0), "y"),
+                       (lambda: hq.hq_moe_route(0, 4, 512, 8, h, hq.HQ_LOGITS_BF16, None, 1, 1, 2, True, 1.0, 16, 16, stream=0), "logits"),
+                       (lambda: hq.hq_moe_route(0, 4, 512, 8, i, hq.HQ_LOGITS_FP32, None, 1, 1, 2, True, 1.0, 16, 16, stream=0), "logits"),
+                       (lambda: hq.hq_moe_route(0, 4, 512, 8, 16, 0, i, 1, 1, 2, True, 1.0, 16, 16, stream=0), "bias"),
+                       (lambda: hq.hq_moe_route(0, 4, 512, 8, 16, 0, None, 1, 1, 2, True, 1.0, i.float(), 16, stream=0), "topk_ids"),
+                       (lambda: hq.hq_moe_route(0, 4, 512, 8, 16, 0, None, 1, 1, 2, True, 1.0, 16, i, stream=0), "topk_weights"),
+                       (lambda: hq.hq_moe_decode(G32, 1, 8, 16, 256, 512, h, 16, None, 16, 16, 16, 16, 1 << 20, stream=0), "x"),
+                       (lambda: hq.hq_moe_decode(G32, 1, 8, 16, 256, 512, 16, i.float(), None, 16, 16, 16, 16, 1 << 20, stream=0), "topk_ids"),
+                       (lambda: hq.hq_moe_decode(G32, 1, 8, 16, 256, 512, 16, 16, i, 16, 16, 16, 16, 1 << 20, stream=0), "topk_weights"),
+                       (lambda: hq.hq_moe_decode(G32, 1, 8, 16, 256, 512, 16, 16, None, 16, 16, h, 16, 1 << 20, stream=0), "out")):
+        with pytest.raises(hq.HQError, match=rf"{what} holds torch\.\w+, not torch\.") as ei:
+            call()
+        assert ei.value.status == INV
+    # a host array is no device buffer, whatever it holds
+    with pytest.raises(hq.HQError, match="x is a host array"):
+        hq.hq_gemv(G32, 0, 4, 256, 512, np.zeros((4, 512), np.uint16), 16, 16, stream=0)
+
+
+def test_raw_bits_and_addresses_pass():
+    """bf16 as its raw bits, addresses, and anything with a data_ptr()."""
+    class Buffer:
+        def data_ptr(self):
+            return 16
+    for x in (torch.zeros((4, 512), dtype=torch.int16), torch.zeros((4, 512), dtype=torch.uint16), torch.zeros((4, 512), dtype=torch.bfloat16)):
+        with pytest.raises(hq.HQError, match="x must be on the current device"):   # the last check: every other one passed
+            hq.hq_gemv(G32, 0, 4, 256, 512, x, 16, 16, stream=0)
+    for x in (16, Buffer()):
+        assert _status(hq.hq_gemv, G32, 2, 4, 256, 512, x, x, x, stream=0) == INV   # reaches the C side: unknown op
+        assert "unknown op" in hq.hq_last_error()
