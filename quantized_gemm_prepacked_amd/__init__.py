@@ -348,12 +348,39 @@ def hq_decode_prepacked_bytes(desc, E, N, K) -> int:
     return _c["hq_decode_prepacked_bytes"](_d(desc), E, N, K)
 
 
+#: numpy types of one scale; bf16 ones as raw bits
+_SCALE_TYPES = {HQ_SCALE_BF16: (2, "iuV"), HQ_SCALE_FP32: (4, "f"), HQ_SCALE_E8M0: (1, "iu")}
+
+
+def _host_array(a, count, size, kinds, what):
+    """A prepack's input, contiguous. The C side takes an address alone: fewer values than the sizes ask for would
+    be read past their end, values of another type misread."""
+    a = np.ascontiguousarray(a)
+    why = (f"holds {a.dtype}, {size}-byte values are needed" if a.itemsize != size or a.dtype.kind not in kinds else
+           f"holds {a.size} values, {count} are needed" if a.size < count else None)
+    if why:
+        raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} {why}")
+    return a
+
+
 def hq_decode_prepack_weights(desc, E, N, K, wq: np.ndarray, scales: np.ndarray, zeros, out: np.ndarray):
-    """Host prepack for the decode calls into ``out`` (uint8, hq_decode_prepacked_bytes bytes)."""
-    arrs = [np.ascontiguousarray(a) for a in (wq, scales)]
-    z = None if zeros is None else np.ascontiguousarray(zeros)
-    _check(_c["hq_decode_prepack_weights"](_d(desc), E, N, K, _ptr(arrs[0]), _ptr(arrs[1]), _ptr(z), _ptr(out),
-                                           out.nbytes))
+    """Host prepack for the decode calls into ``out`` (uint8, hq_decode_prepacked_bytes bytes). bf16 scales come
+    as raw bits (uint16 or int16)."""
+    if wq is not None and scales is not None and out is not None and hq_decode_prepacked_bytes(desc, E, N, K):
+        w8 = desc.weight_fmt in (HQ_W_INT8_SYM, HQ_W_FP8_E4M3)
+        groups = E * N * (K // desc.group_size if desc.group_size else 1)
+        wq = _host_array(wq, E * N * (K if w8 else K // 2), 1, "iuV", "wq")
+        scales = _host_array(scales, groups, *_SCALE_TYPES[desc.scale_dtype], "scales")
+        if zeros is not None and desc.has_zero_point:
+            zeros = _host_array(zeros, groups, 1, "iu", "zeros")
+        if isinstance(out, np.ndarray):
+            whole, writable = out.flags.forc, out.flags.writeable
+        else:
+            whole, writable = out.is_contiguous() and out.device.type == "cpu", True
+        if not whole or not writable:
+            raise HQError(HQ_ERR_INVALID_ARGUMENT, "out must be contiguous, writable and on the host")
+    arrs = [None if a is None else np.ascontiguousarray(a) for a in (wq, scales, zeros)]
+    _check(_c["hq_decode_prepack_weights"](_d(desc), E, N, K, *map(_ptr, arrs), _ptr(out), 0 if out is None else out.nbytes))
     return out
 
 

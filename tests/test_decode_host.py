@@ -273,3 +273,50 @@ def test_raw_bits_and_addresses_pass():
     for x in (16, Buffer()):
         assert _status(hq.hq_gemv, G32, 2, 4, 256, 512, x, x, x, stream=0) == INV   # reaches the C side: unknown op
         assert "unknown op" in hq.hq_last_error()
+
+
+@pytest.mark.parametrize("fmt", list(FORMATS))
+def test_prepack_checks_its_arrays(fmt):
+    """Arrays shorter than the sizes say would be read past their end, and scales of another type misread."""
+    desc = FORMATS[fmt][0]
+    E, N, K = 2, 32, 256
+    g = np.random.default_rng(7)
+    w = [random_weights(g, fmt, N, K) for _ in range(E)]
+    wq, sc = (np.stack([e[k] for e in w]) for k in ("wq", "scales"))
+    z = None if w[0]["zeros"] is None else np.stack([e["zeros"] for e in w])
+    out = np.zeros(hq.hq_decode_prepacked_bytes(desc, E, N, K), np.uint8)
+    pack = lambda wq=wq, sc=sc, z=z, out=out: hq.hq_decode_prepack_weights(desc, E, N, K, wq, sc, z, out)  # noqa: E731
+    want = pack().copy()
+    bad = {"wq": [dict(wq=wq[:1]), dict(wq=wq.ravel()[:-1]), dict(wq=wq.astype(np.int32))],
+           "scales": [dict(sc=sc[:1]), dict(sc=sc.ravel()[:-1]), dict(sc=sc.astype(np.float64)), dict(sc=sc.astype(np.float16))],
+           "zeros": [] if z is None else [dict(z=z[:1]), dict(z=z.ravel()[:-1]), dict(z=z.astype(np.int64))]}
+    if sc.dtype != np.float32:
+        bad["scales"].append(dict(sc=sc.astype(np.float32)))
+    for what, calls in bad.items():
+        for call in calls:
+            with pytest.raises(hq.HQError, match=f"^hq status 1: {what} ") as ei:
+                pack(**call)
+            assert ei.value.status == INV
+    # any memory order, a larger array, and tensors on the host: as before
+    assert np.array_equal(pack(wq=np.asfortranarray(wq), out=np.zeros_like(out)), want)
+    assert np.array_equal(pack(wq=np.concatenate([wq, wq]), sc=np.concatenate([sc, sc]), out=np.zeros_like(out)), want)
+    t = torch.zeros(out.size, dtype=torch.uint8)
+    pack(wq=torch.from_numpy(wq), out=t)
+    assert np.array_equal(t.numpy(), want)
+
+
+def test_prepack_writes_only_into_whole_arrays():
+    """A strided view counts its own bytes, but the call would write through its start over what lies between;
+    a read-only array is somebody's constant."""
+    g = np.random.default_rng(8)
+    w = random_weights(g, "int4_g32", 32, 256)
+    n = hq.hq_decode_prepacked_bytes(G32, 1, 32, 256)
+    whole = np.zeros(2 * n, np.uint8)
+    frozen = np.zeros(n, np.uint8)
+    frozen.flags.writeable = False
+    for out in (whole[::2], frozen, torch.zeros(2 * n, dtype=torch.uint8)[::2]):
+        with pytest.raises(hq.HQError, match="^hq status 1: out ") as ei:
+            hq.hq_decode_prepack_weights(G32, 1, 32, 256, w["wq"], w["scales"], None, out)
+        assert ei.value.status == INV
+    assert not whole.any() and not frozen.any()
+    assert hq.hq_decode_prepack_weights(G32, 1, 32, 256, w["wq"], w["scales"], None, whole[:n]).any()
