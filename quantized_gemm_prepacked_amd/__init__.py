@@ -332,6 +332,13 @@ def _at(x, count, kind, dev, what):
     return x.data_ptr()
 
 
+def _stream_at(stream, dev):
+    """The stream's handle; a stream object has to belong to the current device, as the buffers do."""
+    if stream is not None and getattr(stream, "device_index", dev) != dev:
+        raise HQError(HQ_ERR_INVALID_ARGUMENT, "stream must be on the current device")
+    return _stream(stream)
+
+
 _packed_sizes = {}
 
 
@@ -389,14 +396,14 @@ def hq_moe_route(score_fn, T, E, topk, logits, logits_fmt, bias, n_group, topk_g
     dev, n = _here(), T * topk
     _check(_c["hq_moe_route"](score_fn, T, E, topk, _at(logits, T * E, _BF16 if logits_fmt == HQ_LOGITS_BF16 else _FP32, dev, "logits"),
                               logits_fmt, _at(bias, E, _FP32, dev, "bias"), n_group, topk_group, group_top, int(renormalize), scale,
-                              _at(topk_ids, n, _INT32, dev, "topk_ids"), _at(topk_weights, n, _FP32, dev, "topk_weights"), _stream(stream)))
+                              _at(topk_ids, n, _INT32, dev, "topk_ids"), _at(topk_weights, n, _FP32, dev, "topk_weights"), _stream_at(stream, dev)))
 
 
 def hq_gemv(desc, op, M, N, K, x, w_packed, y, stream=None):
     dev = _here()
     _check(_c["hq_gemv"](_d(desc), op, M, N, K, _at(x, M * K, _BF16, dev, "x"),
                          _at(w_packed, _packed_bytes(desc, 1, N, K), _BYTES, dev, "w_packed"),
-                         _at(y, M * (N // 2 if op == HQ_GEMV_SILU_MUL else N), _BF16, dev, "y"), _stream(stream)))
+                         _at(y, M * (N // 2 if op == HQ_GEMV_SILU_MUL else N), _BF16, dev, "y"), _stream_at(stream, dev)))
 
 
 def hq_moe_decode_workspace_bytes(desc, T, topk, E, H, I) -> int:
@@ -410,4 +417,4 @@ def hq_moe_decode(desc, T, topk, E, H, I, x, topk_ids, topk_weights, w_gate_up, 
                                _at(topk_weights, n, _FP32, dev, "topk_weights"),
                                _at(w_gate_up, _packed_bytes(desc, E, 2 * I, H), _BYTES, dev, "w_gate_up"),
                                _at(w_down, _packed_bytes(desc, E, H, I), _BYTES, dev, "w_down"), _at(out, T * H, _BF16, dev, "out"),
-                               _at(ws, ws_bytes, _BYTES, dev, "ws"), ws_bytes, _stream(stream)))
+                               _at(ws, ws_bytes, _BYTES, dev, "ws"), ws_bytes, _stream_at(stream, dev)))

@@ -320,3 +320,15 @@ def test_prepack_writes_only_into_whole_arrays():
         assert ei.value.status == INV
     assert not whole.any() and not frozen.any()
     assert hq.hq_decode_prepack_weights(G32, 1, 32, 256, w["wq"], w["scales"], None, whole[:n]).any()
+
+
+def test_stream_of_another_device():
+    """The buffers are checked to be on the current device; a stream of another one would run the kernels there."""
+    class Stream:
+        cuda_stream, device_index = 0, 1
+    for call in (lambda st: hq.hq_gemv(G32, 0, 4, 256, 512, 16, 16, 16, stream=st),
+                 lambda st: hq.hq_moe_route(0, 4, 512, 8, 16, 0, None, 1, 1, 2, True, 1.0, 16, 16, stream=st),
+                 lambda st: hq.hq_moe_decode(G32, 1, 8, 16, 256, 512, 16, 16, None, 16, 16, 16, 16, 1 << 20, stream=st)):
+        with pytest.raises(hq.HQError, match="stream must be on the current device") as ei:
+            call(Stream())
+        assert ei.value.status == INV
