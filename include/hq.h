@@ -421,7 +421,9 @@ hq_status hq_moe_combine(int64_t T, int32_t topk, int32_t E, int64_t N, const in
  * hq_gemv and hq_moe_decode take every weight format with bf16 activations except the 2- and 3-bit
  * ones (INT4_SYM, UINT4_ASYM, FP4_E2M1 group 32, INT8_SYM and FP8_E4M3 per channel), and INT4_SYM and
  * UINT4_ASYM with group_size 32 or 64 as well, which hq_gemm and the grouped GEMMs do not; out_fmt
- * HQ_OUT_BF16, compute_flags 0.
+ * HQ_OUT_BF16, compute_flags 0. So weights in groups of 32 or 64 have no call made for a prompt's many rows:
+ * hq_gemv takes them in blocks of 16 and hq_moe_decode in calls of up to 16 tokens, each of which reads
+ * the weights again; a model that runs prompts on this library keeps group 128 (or MXFP4, INT8, FP8).
  * ------------------------------------------------------------------------------------------- */
 
 /* hq_prepacked_bytes / hq_prepack_weights for the descriptions of the decode calls (host; the same
@@ -500,7 +502,8 @@ hq_status hq_gemv(const hq_quant_desc* desc, int32_t op, int64_t M, int64_t N, i
  *   ws            hq_moe_decode_workspace_bytes(...) bytes, contents irrelevant on entry. Calls that
  *                 may run at the same time (other streams, replays of captured graphs) each need
  *                 their own.
- * T 1..HQ_MOE_DECODE_MAX_TOKENS (more: HQ_ERR_UNSUPPORTED; use the grouped GEMMs), topk 1..64,
+ * T 1..HQ_MOE_DECODE_MAX_TOKENS (more: HQ_ERR_UNSUPPORTED; use the grouped GEMMs, or calls of up to 16
+ * tokens for groups of 32 and 64, which the grouped GEMMs do not take), topk 1..64,
  * E 1..512, H and I multiples of 128, T * topk * I < 2^29. Pointers 16-byte aligned (ids and weights 4). T == 0 is a no-op.
  * The result does not depend on the order in which workgroups run.
  * ------------------------------------------------------------------------------------------- */

@@ -636,8 +636,10 @@ hq_status check_moe_decode(const hq_quant_desc* desc, int64_t T, int32_t topk, i
   if (s != HQ_OK) return s;
   if (T < 0) return fail(HQ_ERR_INVALID_ARGUMENT, "T=%lld out of range", (long long)T);
   if (T > HQ_MOE_DECODE_MAX_TOKENS)
-    return fail(HQ_ERR_UNSUPPORTED, "T=%lld: hq_moe_decode takes up to %d tokens (use the grouped GEMMs)", (long long)T,
-                HQ_MOE_DECODE_MAX_TOKENS);
+    return fail(HQ_ERR_UNSUPPORTED,
+                c->fine_group ? "T=%lld: hq_moe_decode takes up to %d tokens (no other call takes groups of 32 or 64: use calls of up to 16)"
+                              : "T=%lld: hq_moe_decode takes up to %d tokens (use the grouped GEMMs)",
+                (long long)T, HQ_MOE_DECODE_MAX_TOKENS);
   if (topk <= 0 || topk > 64 || E <= 0 || E > 512)
     return fail(HQ_ERR_INVALID_ARGUMENT, "topk=%d E=%d out of range", topk, E);
   if (H <= 0 || I <= 0 || H > (int64_t(1) << 23) || I > (int64_t(1) << 23))

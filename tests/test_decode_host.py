@@ -332,3 +332,14 @@ def test_stream_of_another_device():
         with pytest.raises(hq.HQError, match="stream must be on the current device") as ei:
             call(Stream())
         assert ei.value.status == INV
+
+
+def test_too_many_tokens_is_told_what_takes_them():
+    """The grouped GEMMs take no weights in groups of 32 or 64: that error may not send a caller there."""
+    call = lambda desc: hq.hq_moe_decode(desc, 17, 8, 16, 256, 512, 16, 16, None, 16, 16, 16, 16, 1 << 20, stream=0)  # noqa: E731
+    for fmt, (desc, group, _) in FORMATS.items():
+        with pytest.raises(hq.HQError) as ei:
+            call(desc)
+        fine = fmt.endswith(("_g32", "_g64"))
+        assert ei.value.status == UNS and ("grouped GEMMs" in str(ei.value)) == (not fine) and ("calls of up to 16" in str(ei.value)) == fine
+        assert (hq.hq_prepacked_bytes(desc, 16, 256, 512) == 0) == fine      # what the grouped GEMMs' prepack says
