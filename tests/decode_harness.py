@@ -73,6 +73,21 @@ def product_bound(x: np.ndarray, w: dict, fmt: str) -> np.ndarray:
     return 2.0 ** -23 * (128 + K // 128 + 16 + 8) * a
 
 
+def group_product_bound(x: np.ndarray, w: dict, fmt: str) -> np.ndarray:
+    """product_bound for long K, where INT4's offset form must not be charged to the whole sum. A group's two
+    offset sums, sum x (128 + q) and (128 + z) sum x, stay apart from the others: each of their terms (together
+    below 288 |x| before the scale) passes through at most G additions, and 8 more for the halves of a row, the
+    subtraction and the scale. What is added up over the K / G groups, 16 waves and 8 more steps is the groups'
+    values themselves, at most sum |x w|. Both at 2^-23 a step, as there; errors of errors: 2^-6 of it."""
+    _, group, _ = FORMATS[fmt]
+    if not fmt.startswith(("int4", "uint4")):
+        return product_bound(x, w, fmt)
+    ax = np.abs(oracle.decode_bf16(x) if x.dtype == np.uint16 else x)
+    offsets = (group + 8) * (ax @ magnitude(w, fmt).T)
+    chain = (x.shape[1] // group + 24) * (ax @ np.abs(dequant(w, fmt)).T)
+    return 2.0 ** -23 * (1 + 2.0 ** -6) * (offsets + chain)
+
+
 def prepack_host(desc, w: dict, N: int, K: int) -> np.ndarray:
     stack = w if isinstance(w, list) else [w]
     out = np.zeros(hq.hq_decode_prepacked_bytes(desc, len(stack), N, K), np.uint8)

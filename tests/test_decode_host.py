@@ -10,7 +10,7 @@ import oracle
 import quantized_gemm_prepacked_amd as hq
 import synth
 
-from decode_harness import FORMATS, dequant, prepack_host, random_weights, route_case
+from decode_harness import FORMATS, dequant, group_product_bound, prepack_host, product_bound, random_weights, route_case
 
 INV, UNS, WSP = hq.HQ_ERR_INVALID_ARGUMENT, hq.HQ_ERR_UNSUPPORTED, hq.HQ_ERR_WORKSPACE
 G32 = hq.DESC_W4A16_SYM_G32
@@ -343,3 +343,32 @@ def test_too_many_tokens_is_told_what_takes_them():
         fine = fmt.endswith(("_g32", "_g64"))
         assert ei.value.status == UNS and ("grouped GEMMs" in str(ei.value)) == (not fine) and ("calls of up to 16" in str(ei.value)) == fine
         assert (hq.hq_prepacked_bytes(desc, 16, 256, 512) == 0) == fine      # what the grouped GEMMs' prepack says
+
+
+@pytest.mark.parametrize("fmt,M,K", [("int4_g32", 3, 14336), ("uint4_g64", 1, 4096), ("uint4_g128", 13, 8192), ("uint4_g32", 16, 4096)])
+def test_large_products_check_sees_lost_terms(fmt, M, K):
+    """At the sizes of a model: a lost scale group breaks the elementwise bound, and a lost k the relative one
+    (2e-3 of the norm), which an exact result rounded once keeps."""
+    g = np.random.default_rng(9)
+    group = FORMATS[fmt][1]
+    w = random_weights(g, fmt, 208, K)
+    x = synth.normal_bf16(g, (M, K))
+    v = dequant(w, fmt)
+    ref = oracle.ref_gemv(x, v, False)
+    bound = group_product_bound(x, w, fmt)
+    assert (bound <= product_bound(x, w, fmt) * (1 + 2.0 ** -6)).all()
+    rms, allowed = np.sqrt((ref ** 2).mean()), bound + 2.0 ** -8 * (np.abs(ref) + bound) + 2.0 ** -134
+    worst = lambda got: float((np.abs(got - ref) / allowed).max())  # noqa: E731
+    rel = lambda got: float(np.linalg.norm(got - ref) / np.linalg.norm(ref))  # noqa: E731
+    rounded = oracle.decode_bf16(oracle.round_to_bf16(ref))
+    size = np.linalg.norm(oracle.decode_bf16(x), axis=0)     # of each k in x
+    assert worst(rounded) <= 1.0 and rel(rounded) < 2e-3
+    for k0 in (0, K // 2, K - group):
+        lost = v.copy()
+        lost[:, k0:k0 + group] = 0.0
+        got = oracle.ref_gemv(x, lost, False)
+        assert worst(got) > 1.0 and rel(got) > 2e-3, (k0, worst(got), rel(got), float(bound.mean() / rms))
+        k = k0 + int(np.argmax(size[k0:k0 + group]))         # (one whose x is next to nothing no check could see)
+        lost = v.copy()
+        lost[:, k] = 0.0
+        assert rel(oracle.ref_gemv(x, lost, False)) > 2e-3

@@ -8,7 +8,7 @@ import oracle
 import quantized_gemm_prepacked_amd as hq
 import synth
 
-from decode_harness import FORMATS, dequant, magnitude, prepack_host, product_bound, random_weights, route_case
+from decode_harness import FORMATS, dequant, group_product_bound, magnitude, prepack_host, product_bound, random_weights, route_case
 from gpu_harness import BF16_NAN_BITS, DEV, bf16_to_f64, check_float, say, to_dev
 
 pytestmark = pytest.mark.gpu
@@ -200,6 +200,23 @@ def test_gemv_large():
         cols = np.unique(np.concatenate([g.integers(0, N, 200), [0, 15, 16, N - 1]]))
         part = {k: None if v is None else v[cols] for k, v in w.items()}
         _check(got[:, cols], oracle.ref_gemv(x, dequant(part, fmt), False), product_bound(x, part, fmt), "sampled")
+
+
+@pytest.mark.parametrize("fmt,M,N,K", [("uint4_g64", 1, 14336, 4096), ("int4_g32", 3, 4096, 14336), ("uint4_g128", 13, 8208, 8192),
+                                       ("uint4_g32", 16, 12304, 4096)])     # the last: four tiles a workgroup
+def test_gemv_large_loses_nothing(fmt, M, N, K):
+    """The sizes a model has, by checks that a lost scale group and a lost k break (the host test of the
+    large products' checks plants both in the oracle)."""
+    g = np.random.default_rng(1150 + M)
+    w = random_weights(g, fmt, N, K)
+    x = synth.normal_bf16(g, (M, K))
+    say(f"[gemv large] {fmt} M={M} N={N} K={K}")
+    got = _gemv(FORMATS[fmt][0], False, x, to_dev(prepack_host(FORMATS[fmt][0], w, N, K)), N, K)
+    cols = np.unique(np.concatenate([g.integers(0, N, 200), [0, 15, 16, N - 1]]))
+    part = {k: None if v is None else v[cols] for k, v in w.items()}
+    ref = oracle.ref_gemv(x, dequant(part, fmt), False)
+    _check(got[:, cols], ref, group_product_bound(x, part, fmt), "sampled")
+    check_float(got[:, cols], ref, "sampled")
 
 
 def test_gemv_equals_gemm_weights():
