@@ -250,6 +250,28 @@ def test_gemv_rows_do_not_mix(fmt, M):
         assert not np.isfinite(bf16_to_f64(got[M - 1])).any()
 
 
+@pytest.mark.parametrize("fmt", list(FORMATS))
+@pytest.mark.parametrize("M", [2, 3, 4, 5, 16, 17])
+def test_gemv_one_bad_row(fmt, M):
+    """One bad row at a time, so that every other row is compared while clean: NaN in the last one, which a block
+    of rows repeats in its unused places, and infinity in the first. M = 17: a second block, of one row."""
+    g = np.random.default_rng(1350)
+    N, K = 64, 640
+    w = random_weights(g, fmt, N, K)
+    x = synth.normal_bf16(g, (M, K))
+    packed = to_dev(prepack_host(FORMATS[fmt][0], w, N, K))
+    for gated in (False, True):
+        clean = _gemv(FORMATS[fmt][0], gated, x, packed, N, K)
+        assert np.isfinite(bf16_to_f64(clean)).all()
+        for row, at, bits in ((M - 1, slice(None), 0x7FC0), (M - 1, 639, 0x7FC0), (0, 7, 0x7F80)):
+            bad = x.copy()
+            bad[row, at] = bits
+            got = _gemv(FORMATS[fmt][0], gated, bad, packed, N, K)
+            rest = np.arange(M) != row
+            assert rest.any() and np.array_equal(got[rest], clean[rest]), (gated, row)
+            assert not np.isfinite(bf16_to_f64(got[row])).all()
+
+
 def test_gated_extremes():
     """Gates far out on both sides: silu keeps its tiny products and never divides infinities."""
     g = np.random.default_rng(1400)
