@@ -601,3 +601,45 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for c in calls:
         assert np.array_equal(_bits(c["out"]), c["want"])
+
+
+@pytest.mark.parametrize("fmt,T", [("int4_g32", 1), ("uint4_g128", 4), ("mxfp4", 16), ("int8", 3)])
+def test_nothing_is_kept_between_calls(fmt, T):
+    """Every buffer overwritten in place between two calls, weights too: the second call's results are those
+    of fresh buffers, and every expert that is routed to counts."""
+    g = np.random.default_rng(3000 + T)
+    E, H, I, topk = 6, 384, 256, 3
+    one, two = Layer(3001, fmt, E, H, I), Layer(3002, fmt, E, H, I)
+    cases = [(synth.normal_bf16(g, (T, H)), _ids(g, T, topk, E), g.random((T, topk)).astype(np.float32)) for _ in range(2)]
+    fresh = two.run(*cases[1])
+    n = hq.hq_moe_decode_workspace_bytes(one.desc, T, topk, E, H, I)
+    x, ids, w = to_dev(cases[0][0].view(np.int16)), to_dev(cases[0][1]), to_dev(cases[0][2])
+    out, ws = torch.zeros((T, H), dtype=torch.int16, device=DEV), torch.zeros(n, dtype=torch.uint8, device=DEV)
+    gu, dn = one.gu_dev.clone(), one.dn_dev.clone()
+
+    def moe():
+        hq.hq_moe_decode(one.desc, T, topk, E, H, I, x, ids, w, gu, dn, out, ws, n)
+        torch.cuda.synchronize()
+        return _bits(out).copy()
+
+    assert np.array_equal(moe(), one.run(*cases[0]))
+    for old, new in zip((x, ids, w), (cases[1][0].view(np.int16), cases[1][1], cases[1][2])):
+        old.copy_(torch.from_numpy(new))
+    gu.copy_(two.gu_dev), dn.copy_(two.dn_dev)
+    assert np.array_equal(moe(), fresh)
+    # an expert's weights zeroed in place: exactly the tokens routed to it change
+    per = dn.numel() // E
+    for e in range(E):
+        kept = dn[e * per:(e + 1) * per].clone()
+        dn[e * per:(e + 1) * per] = 0
+        got = moe()
+        dn[e * per:(e + 1) * per] = kept
+        hit = (cases[1][1] == e).any(1)
+        assert np.array_equal((got != fresh).any(1), hit), e
+    a, b = (prepack_host(one.desc, random_weights(g, fmt, H, H), H, H) for _ in range(2))
+    packed, y = to_dev(a), torch.zeros((T, H), dtype=torch.int16, device=DEV)
+    for bits in (a, b):
+        packed.copy_(torch.from_numpy(bits))
+        hq.hq_gemv(one.desc, hq.HQ_GEMV_LINEAR, T, H, H, x, packed, y)
+        torch.cuda.synchronize()
+        assert np.array_equal(_bits(y), _gemv(one.desc, False, cases[1][0], to_dev(bits), H, H))
