@@ -479,7 +479,10 @@ typedef enum {
  * in blocks of 16 that each read the weights again. M <= 65536, N and K <= 2^24, M * N < 2^31.
  * NaN or infinity in a row of x reaches that row of y only; INT4 products are formed from codes offset by
  * 128 with the row's sum taken off, so there an infinity gives NaN (and a group's sums of activations
- * above 2^113 may overflow where the exact ones would not).
+ * above 2^113 may overflow where the exact ones would not; so may sums of codes times activations of 8-bit
+ * weights, whose channel scale is applied at the end).
+ * Where hq_gemm takes the description too, both take the same packed weights, and up to 16 rows this is the
+ * faster call (UINT4 with group 128: 1.1 to 1.9 times at the sizes measured).
  * x, w_packed and y 16-byte aligned; y must not overlap x. M == 0 is a no-op. No workspace.
  * ------------------------------------------------------------------------------------------- */
 hq_status hq_gemv(const hq_quant_desc* desc, int32_t op, int64_t M, int64_t N, int64_t K, const void* x,

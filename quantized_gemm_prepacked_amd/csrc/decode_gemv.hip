@@ -1,9 +1,10 @@
 // decode_gemv.hip -- hq_gemv: y = x . W^T for one to a few rows, plain or gated (silu(gate) * up).
 //
 // Bound by the packed weights' bytes from some 20 MB on: 14336 x 4096 at M = 1 in groups of 64 reads 31.8 MB
-// in 7.5 us (4.2 TB/s; a 2 GiB copy moves 4.9 on this card), the gated 2 x 14336 x 4096 at M = 3 66 MB in 12.6
-// (5.3); below, by a launch's own time (2.2 us for 256 x 512). With five rows or more the rows' copies
-// into LDS count too: 8208 x 8192 at M = 13 36.8 MB in 11.2 us (3.3 TB/s).
+// in 7.8 us (4.1 TB/s; a kernel that only reads that much takes 6.7), the gated 2 x 14336 x 4096 at M = 3 66 MB in
+// 12.4 (5.3 TB/s; 11.4); below, by a launch's own time (2.5 us for 256 x 512, 2.2 back to back). With five rows or
+// more the rows' copies into LDS count too, since every workgroup reads all of x: 8208 x 8192 at M = 13 takes 11.4
+// us for 36.8 MB (3.2 TB/s), with 171 workgroups copying 256 KiB each beside them.
 // A workgroup owns NT tiles of 16 output channels (gated: the gate and the up tile of the same
 // outputs, in pairs) and one row block; its NW waves take every NW-th K unit each (decode_ops.h) and
 // add their partial tiles through LDS, in wave order.
@@ -119,13 +120,15 @@ int tiles_per_workgroup(int tiles, int lo, int hi, bool ties_to_more) {
 // from HBM, us (NT x waves x D):
 //   up to 256 output tiles: one a workgroup, so every CU has one, and a deep ring (M = 1: 4096 x 14336 8.0 as
 //   1x8x4, 11.5 as 2x8x2, 15.2 as 4x8x2; 2048 x 8192 4.7, 6.2, 9.3); with two K units a wave or less a
-//   ring of two (2048 x 2048: 2.9, 3.2 as 1x8x4)
+//   ring of two (as 1x8x2 / 1x8x4: 2048 x 2048 2.87 / 3.16, 2048 x 2560 3.24 / 3.16; groups of 32 alike)
 //   more: two to four tiles share the activations' reads and row sums (M = 1: 14336 x 4096 7.5 as 2x8x2,
 //   8.5 as 1x8x4; M = 16: 28672 x 8192 26 as 4x8x2, 31 as 2x8x2, 48 as 1x8x3), as many as fill the CUs
 //   evenly (M = 16: 8192 x 8192 11.0 as 2x8x2, 13.7 as 4x8x2; one tile more, 8208 x 8192, 15.4 as 2x8x2,
-//   12.5 as 3x8x2, 13.9 as 4x8x2)
-//   gated: pairs of a gate and an up tile; more waves where K is long and pairs are few (M = 1: 2048 / 2
-//   outputs x 8192 6.0 as 2x16x2, 6.4 as 2x8x2)
+//   12.5 as 3x8x2, 13.9 as 4x8x2). Groups of 32 too, whose four tiles need the most registers (135 of them;
+//   12320 x 4096, M = 16: 9.6 as 4x8x2, 10.5 as 3x8x2)
+//   gated: pairs of a gate and an up tile; more waves where K is long and pairs are few (M = 1, as 2x16x2 / 2x8x2:
+//   64 pairs x 8192 6.1 / 6.4, x 6144 5.6 / 5.4; the other end, 255 pairs x 8192, is 8.5 / 8.4, and groups of 32
+//   gain nothing: 64 pairs x 8192 6.9 / 6.9)
 template <int F, bool GATED>
 hipError_t launch_rows(const GemvParams& p, hipStream_t s) {
   const int tiles = p.N / 16 / (GATED ? 2 : 1);

@@ -4,9 +4,10 @@
 //   down   out[t] = sum_j weight[t, j] * Wd act[t, j]
 //
 // Both stream expert weights through decode_ops.h, and reading them is what bounds them: at T = 1, 8 of
-// 32 experts of 7168 x 2048 INT4, up reads 121 MB at 6.1 TB/s and down 61 MB at 4.7 (a 2 GiB copy moves 4.9
-// TB/s on this card); at T = 16, 41 experts of 4096 x 1536 in groups of 32, 5.2 and 4.7 TB/s with the vector
-// ALU half busy. Below some 20 MB the two launches' own time (about 4 us each) is most of it.
+// 32 experts of 7168 x 2048 INT4, up reads 121 MB in 19.7 us (6.2 TB/s) and down 61 MB in 13.2 (4.6), where a kernel
+// that only reads takes 19.4 and 10.9; at T = 16, 41 experts of 4096 x 1536 in groups of 32, 5.2 and 5.0 TB/s with
+// the vector ALU 42 and 53 % busy. Below some 20 MB the two launches (2.3 us each) and their first loads' latency
+// are most of it: 8 experts of 2048 x 768 MXFP4, 13.5 and 7.0 MB, take 6.2 and 5.6 us.
 // With few tokens an expert is hit by one or a few of them, so its weights are read once for up to four
 // of its tokens (a pass; in the down launch two, unless experts are shared widely); further tokens take
 // further passes, whose weights come from the caches.
@@ -421,7 +422,8 @@ DownPlan down_plan(int64_t T, int32_t topk, int32_t E, int64_t H, int64_t I) {
   d.tiles = int((H / 16 + d.nt - 1) / d.nt);
   // Few output tiles leave CUs idle: then several workgroups share a tile's items, as long as a wave keeps
   // four units of distinct experts' weights (T = 16 top-8 of 128, 2048 x 768: 51 us as two, 57 as one; T = 4
-  // top-2 of 16, 2048 x 1024: 12.9 as two, with two units a wave, 12.2 as one).
+  // top-2 of 16, 2048 x 1024: 13.1 as two, with two units a wave, 12.2 as one; T = 1 top-8 of 64, 1024 x 2048: 14.6
+  // as three, 15.3 as two where a wave would have to keep eight).
   const int64_t units = std::min<int64_t>(T * topk, E) * (I / 128) / 16;
   d.splits = int(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(256 / d.tiles, units / 4), 16)));
   return d;
@@ -447,7 +449,9 @@ MoeWs moe_ws(const DownPlan& d, int64_t T, int32_t topk, int64_t I) {
 //         T > 1: 2x4x2 20.4 at T = 3, 4096 x 1408 and 53 at T = 16, 4096 x 1536 (1x8x4 25.9 / 91: with eight
 //         waves a wave has three or four units, and dead slots of the ring are a third of its loads)
 //   down  T = 1: 2x16x2 13.4 at 7168 x 2048 but 6.9 at 2048 x 768, where half the CUs have no tile; 1x16x3
-//         16.7 and 5.0 -- so two tiles a workgroup from H = 6144 on, where there are 192 workgroups
+//         16.7 and 5.0 -- so two tiles a workgroup from H = 6144 on, where there are 192 workgroups (whole call,
+//         I = 2048, one / two tiles: H = 4096 22.9 / 23.6, 5120 30.3 / 29.3, 6144 33.5 / 31.6; T = 3: 4096 43.1 /
+//         43.2, 5120 55.3 / 52.5, 6144 63.5 / 59.0: from 257 tiles on two would do)
 //         T > 1: 1x16x3 12.4 and 33 (2x16x2 16.3 / 48.6); with H = 7168 2x16x2 (T = 16 top-8 of 64: 253
 //         against 269 for both launches); passes of four tokens where an expert has over two on average (T = 16
 //         top-2 of 8, 4096 x 14336: 194 against 219 with passes of two)

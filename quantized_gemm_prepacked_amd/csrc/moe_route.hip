@@ -15,8 +15,9 @@
 // vector unit and one lane read (through LDS shuffles of 64-bit values and ids the same selection took
 // twice as long). A lane's values are sorted once, so that a maximum looks at its first only and the
 // winner moves up by one; of 64-bit keys the low halves are compared only where the high halves tie.
-// Measured: one row of 256 logits, top-8, 3.1 us (a launch alone takes 2.2); 4096 rows with bias and 4 of 8
-// groups 10.4 us, of which the groups are 1.8, the 64-bit sigmoids 2.6 and the eight rounds 2.2.
+// Measured back to back (alone under a tracer): one row of 256 logits, top-8, 3.0 us (3.1), where a launch alone
+// takes 2.2; 4096 rows with bias and 4 of 8 groups 10.4 us (11.3; its 4.5 MB would take 2.9), 8.6 without the groups
+// and 8.1 with one choice instead of eight; without bias and groups, on 32-bit keys, 5.2.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
