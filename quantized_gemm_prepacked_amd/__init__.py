@@ -380,11 +380,9 @@ def hq_decode_prepack_weights(desc, E, N, K, wq: np.ndarray, scales: np.ndarray,
         scales = _host_array(scales, groups, *_SCALE_TYPES[desc.scale_dtype], "scales")
         if zeros is not None and desc.has_zero_point:
             zeros = _host_array(zeros, groups, 1, "iu", "zeros")
-        if isinstance(out, np.ndarray):
-            whole, writable = out.flags.forc, out.flags.writeable
-        else:
-            whole, writable = out.is_contiguous() and out.device.type == "cpu", True
-        if not whole or not writable:
+        fit = (out.flags.forc and out.flags.writeable if isinstance(out, np.ndarray) else
+               out.is_contiguous() and out.device.type == "cpu" if isinstance(out, torch.Tensor) else True)
+        if not fit:
             raise HQError(HQ_ERR_INVALID_ARGUMENT, "out must be contiguous, writable and on the host")
     arrs = [None if a is None else np.ascontiguousarray(a) for a in (wq, scales, zeros)]
     _check(_c["hq_decode_prepack_weights"](_d(desc), E, N, K, *map(_ptr, arrs), _ptr(out), 0 if out is None else out.nbytes))

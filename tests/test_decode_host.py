@@ -372,3 +372,18 @@ def test_large_products_check_sees_lost_terms(fmt, M, K):
         lost = v.copy()
         lost[:, k] = 0.0
         assert rel(oracle.ref_gemv(x, lost, False)) > 2e-3
+
+
+def test_prepack_into_memory_of_one_s_own():
+    """Anything with a data_ptr() and its bytes (a mapped file, an arena) is taken as it is."""
+    g = np.random.default_rng(10)
+    w = random_weights(g, "int4_g32", 32, 256)
+    memory = np.zeros(hq.hq_decode_prepacked_bytes(G32, 1, 32, 256), np.uint8)
+
+    class Arena:
+        nbytes = memory.nbytes
+
+        def data_ptr(self):
+            return memory.ctypes.data
+    hq.hq_decode_prepack_weights(G32, 1, 32, 256, w["wq"], w["scales"], None, Arena())
+    assert np.array_equal(memory, prepack_host(G32, w, 32, 256))
