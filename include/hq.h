@@ -518,6 +518,120 @@ hq_status hq_moe_decode(const hq_quant_desc* desc, int64_t T, int32_t topk, int3
                         const void* w_gate_up, const void* w_down, void* out, void* ws,
                         size_t ws_bytes, hq_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * RMS norm of a decoder layer (device), with the addition to the residual stream before it and the
+ * activation quantization of the following GEMM behind it, in one launch:
+ *   h[m, k] = bf16( fp32( x[m, k] + residual[m, k] ) )   (residual NULL: h = x); written to residual_out
+ *   r[m]    = fp32( 1 / sqrt( sum_k h[m, k]^2 / K + eps ) )     (sum, division and root in binary64)
+ *   v[m, k] = fp32( fp32( h[m, k] * r[m] ) * weight[k] )        (weight NULL: 1)
+ *   HQ_ACT_BF16   y = bf16(v), [M, K]; y_scale and y_bf16 NULL
+ *   other act_fmt y, y_scale = the codes and scales of v by the rule of hq_quantize_activations for
+ *                 that format, in its layouts (the GEMM's `a` and `a_scale`); v is not rounded to bf16
+ *                 on the way. y_bf16, if not NULL, receives bf16(v) as well (the router of an MoE
+ *                 block reads it, where the experts read the codes).
+ * Since the sum is in binary64 a row's result does not depend on how the row is split over threads.
+ * act_fmt       HQ_ACT_BF16, HQ_ACT_INT8_PER_TOKEN, HQ_ACT_FP8E4M3_PER_TOKEN,
+ *               HQ_ACT_FP8E4M3_BLOCK128 (K % 128 == 0), HQ_ACT_MXFP8, HQ_ACT_MXFP4 (K % 32 == 0)
+ * x, residual, residual_out, y_bf16: bf16 [M, K] row-major; weight bf16 [K]; all 16-byte aligned, as y;
+ * y_scale fp32 (4-byte aligned), e8m0 bytes for the MX formats. K % 8 == 0, K <= 65536.
+ * residual_out is required with a residual and NULL without. It may be residual or x; y or y_bf16 may
+ * be x where residual_out is not; no other overlap. NaN and infinity in a row reach that row alone:
+ * its codes are unspecified, bf16 results follow the formula. M == 0 is a no-op. No workspace.
+ * ------------------------------------------------------------------------------------------- */
+hq_status hq_rms_norm(int32_t act_fmt, int64_t M, int64_t K, const void* x, const void* residual,
+                      const void* weight, float eps, void* residual_out, void* y, void* y_scale,
+                      void* y_bf16, hq_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * The attention part of a decoder layer over a paged cache of keys and values in 8 bits, with one
+ * scale for each page (a block of page_size tokens of one sequence) and head, K and V apart:
+ *   hq_kv_append   quantizes the keys and values of new tokens into the cache
+ *   hq_attention   attention of new tokens over the cache: one or a few tokens of each sequence
+ *                  (decode, drafted tokens), whole prompts, pieces of prompts, all mixed in one call
+ * Layouts (device, caller-allocated; P = page_size, D = head_dim):
+ *   k_pages   codes [num_pages, num_kv_heads, P, D]
+ *   v_pages   codes [num_pages, num_kv_heads, D, P]   (a token's values lie P bytes apart)
+ *   k_scales, v_scales   fp32 [num_pages, num_kv_heads]; value = code * scale
+ * A page is contiguous in all four: pages are copied, moved or given to another sequence by plain
+ * copies of these ranges. Contents on entry do not matter before a page's first append.
+ * A call's sequences b = 0 .. B-1:
+ *   cu       int32 [B + 1]: the new tokens of b are the rows cu[b] .. cu[b+1]-1 of k, v, q and out
+ *   kv_lens  int32 [B]: tokens of b in the cache, the new ones included: the new ones have positions
+ *            kv_lens[b] - n .. kv_lens[b] - 1 (n = cu[b+1] - cu[b]); a token whose position would be negative is
+ *            not stored and attends to nothing
+ *   page_table  int32 [B, table_width]: position p of b is in slot p % P of page page_table[b, p / P].
+ *            Entries outside [0, num_pages) are pages that do not exist: their tokens are not stored and
+ *            not attended to (pages freed behind a sliding window).
+ * These arrays are read on the device, and checked there: a sequence with cu[b] < 0, cu[b+1] < cu[b],
+ * cu[b+1] > T, more than max_new / max_q new tokens, kv_lens[b] < 0 or kv_lens[b] > table_width * P is
+ * left out (nothing of it is stored, its rows of out stay as they were). So are rows in no sequence.
+ * ------------------------------------------------------------------------------------------- */
+typedef enum {
+  HQ_KV_FP8_E4M3 = 0, /* OCP e4m3, largest code 448 */
+  HQ_KV_INT8 = 1      /* two's-complement INT8 in [-127, 127] */
+} hq_kv_fmt;
+
+typedef struct {
+  uint32_t struct_size;  /* = sizeof(hq_kv_desc)                       */
+  int32_t kv_fmt;        /* hq_kv_fmt                                  */
+  int32_t num_kv_heads;  /* 1..1024                                    */
+  int32_t head_dim;      /* 64, 96, 128, 192 or 256                    */
+  int32_t page_size;     /* tokens: 16, 32, 64, 128 or 256             */
+  int32_t num_pages;     /* pages of the cache, at least 1             */
+} hq_kv_desc;
+
+/* Bytes of k_pages (and of v_pages); 0 for a description that is not supported. */
+size_t hq_kv_cache_bytes(const hq_kv_desc* desc);
+
+/* ---------------------------------------------------------------------------------------------
+ * Append to the cache (device). For each page that receives tokens, head, and K and V apart, with Q =
+ * 448 (e4m3) or 127 (INT8) and a = fp32(the largest |value| of its new tokens / Q):
+ *   s = a                  if the page's first slot is among the new ones, or its scale is 0
+ *   s = scale * 2^e        otherwise, e >= 0 the smallest with a <= scale * 2^e
+ *   new codes              clamp(rne(fp32(value / s))), as hq_quantize_activations; 0 where s = 0
+ *   codes already there    rne(code * 2^-e): unchanged for e = 0; exact for e4m3 but for its subnormals, so a
+ *                          page that grows step by step keeps what it holds. INT8 codes lose e bits.
+ * Infinities count as the largest finite bf16 of their sign. NaN: in a key of an e4m3 cache the code
+ * 0x7F (NaN), otherwise 0. Slots behind the sequence's end are not written.
+ *   k, v       bf16, token rows kv_stride elements apart (>= num_kv_heads * D, a multiple of 8), heads
+ *              contiguous in a row: views of a fused projection's output as they are. T rows. 16-byte aligned.
+ *   max_new    at least the largest number of new tokens of a sequence
+ * A page that receives tokens must belong to one sequence of the call (else its contents are
+ * unspecified). B == 0, T == 0 or max_new == 0 is a no-op. No workspace, one launch.
+ * ------------------------------------------------------------------------------------------- */
+hq_status hq_kv_append(const hq_kv_desc* desc, int32_t B, int64_t T, int32_t max_new, const void* k,
+                       const void* v, int64_t kv_stride, const int32_t* cu, const int32_t* kv_lens,
+                       const int32_t* page_table, int32_t table_width, void* k_pages, void* v_pages,
+                       float* k_scales, float* v_scales, hq_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Attention over the cache (device), causal, with grouped heads (query head i reads head i / (Hq /
+ * num_kv_heads) of the cache):
+ *   out[t, i] = bf16( sum_j p_j v_j / sum_j p_j ),  p_j = exp( sm_scale * q[t, i] . k_j ),
+ * over the positions j <= pos(t) of t's sequence, with window > 0 only j > pos(t) - window. A row
+ * that sees no token gets zeros. fp32 accumulation and statistics; p_j * scale enters the product with the
+ * values as a bf16. NaN in a query's row reaches that row alone; a NaN key the rows that see it.
+ *   q        bf16, token rows q_stride elements apart (>= Hq * D, a multiple of 8), 16-byte aligned, T rows
+ *   out      bf16 [T, Hq, D], 16-byte aligned; may be q where q_stride = Hq * D
+ *   max_q    at least the largest number of query tokens of a sequence
+ *   max_kv   about the largest kv_lens of the call, table_width * P where it is not known (graphs that
+ *            are replayed as the sequences grow): it sets how many workgroups share a sequence, never what
+ *            is computed. Results differ in their last bits with it.
+ *   sm_scale finite; window 0 (none) or the number of positions seen, the token's own included
+ *   ws       hq_attention_workspace_bytes(...) bytes (may be 0 / NULL), 16-byte aligned, contents irrelevant on
+ *            entry. Calls that may run at the same time each need their own.
+ * Hq a multiple of num_kv_heads, at most 128 times it. B == 0, T == 0 or max_q == 0 is a no-op.
+ * The result does not depend on the order in which workgroups run.
+ * ------------------------------------------------------------------------------------------- */
+size_t hq_attention_workspace_bytes(const hq_kv_desc* desc, int32_t B, int64_t T, int32_t Hq,
+                                    int32_t max_q, int64_t max_kv);
+hq_status hq_attention(const hq_kv_desc* desc, int32_t B, int64_t T, int32_t Hq, int32_t max_q,
+                       int64_t max_kv, const void* q, int64_t q_stride, const int32_t* cu,
+                       const int32_t* kv_lens, const int32_t* page_table, int32_t table_width,
+                       const void* k_pages, const void* v_pages, const float* k_scales,
+                       const float* v_scales, float sm_scale, int32_t window, void* out, void* ws,
+                       size_t ws_bytes, hq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

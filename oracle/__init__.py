@@ -40,3 +40,4 @@ from .actquant import (  # noqa: F401
     quantize_fp8_block_act,
 )
 from .decode import dequant_int4_groups, ref_route, ref_gemv, ref_moe_decode  # noqa: F401
+from .layer import quantize_values, ref_attention, ref_kv_append, ref_rms_norm  # noqa: F401

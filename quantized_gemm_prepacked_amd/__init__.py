@@ -35,6 +35,7 @@ HQ_LOGITS_FP32, HQ_LOGITS_BF16 = range(2)
 HQ_SCORE_SOFTMAX, HQ_SCORE_SIGMOID = range(2)
 HQ_GEMV_LINEAR, HQ_GEMV_SILU_MUL = range(2)
 HQ_MOE_DECODE_MAX_TOKENS = 16
+HQ_KV_FP8_E4M3, HQ_KV_INT8 = range(2)
 
 EXPORTED = (
     "hq_prepacked_bytes", "hq_prepack_weights", "hq_gemm_workspace_bytes", "hq_gemm", "hq_gemm_noalloc",
@@ -45,6 +46,7 @@ EXPORTED = (
     "hq_load_tuning_table", "hq_gemm_plan", "hq_kernel_config_count",
     "hq_decode_prepacked_bytes", "hq_decode_prepack_weights", "hq_moe_route", "hq_gemv",
     "hq_moe_decode_workspace_bytes", "hq_moe_decode",
+    "hq_rms_norm", "hq_kv_cache_bytes", "hq_kv_append", "hq_attention_workspace_bytes", "hq_attention",
     "hq_last_error", "hq_version",
 )
 
@@ -78,6 +80,22 @@ def with_flags(desc, compute_flags):
                      desc.act_fmt, desc.out_fmt, compute_flags)
 
 
+class hq_kv_desc(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("kv_fmt", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+    ]
+
+
+def make_kv_desc(kv_fmt, num_kv_heads, head_dim, page_size, num_pages):
+    """A paged 8-bit cache of keys and values (the attention calls)."""
+    return hq_kv_desc(ctypes.sizeof(hq_kv_desc), kv_fmt, num_kv_heads, head_dim, page_size, num_pages)
+
+
 # The four supported combinations (plus the W8A8 raw-accumulator test mode).
 DESC_W4A16_SYM = make_desc(HQ_W_INT4_SYM, 128, HQ_SCALE_BF16, 0, HQ_ACT_BF16)
 DESC_W4A16_ASYM = make_desc(HQ_W_UINT4_ASYM, 128, HQ_SCALE_BF16, 1, HQ_ACT_BF16)
@@ -103,6 +121,7 @@ _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _SZ = ctypes.c_size_t
 _D = ctypes.POINTER(hq_quant_desc)
+_KV = ctypes.POINTER(hq_kv_desc)
 
 
 def _sig(name, res, *args):
@@ -144,6 +163,12 @@ _c = {
     "hq_moe_decode_workspace_bytes": _sig("hq_moe_decode_workspace_bytes", _SZ, _D, _I64, _I32, _I32, _I64, _I64),
     "hq_moe_decode": _sig("hq_moe_decode", ctypes.c_int, _D, _I64, _I32, _I32, _I64, _I64, _P, _P, _P, _P, _P, _P, _P,
                           _SZ, _P),
+    "hq_rms_norm": _sig("hq_rms_norm", ctypes.c_int, _I32, _I64, _I64, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P),
+    "hq_kv_cache_bytes": _sig("hq_kv_cache_bytes", _SZ, _KV),
+    "hq_kv_append": _sig("hq_kv_append", ctypes.c_int, _KV, _I32, _I64, _I32, _P, _P, _I64, _P, _P, _P, _I32, _P, _P, _P, _P, _P),
+    "hq_attention_workspace_bytes": _sig("hq_attention_workspace_bytes", _SZ, _KV, _I32, _I64, _I32, _I32, _I64),
+    "hq_attention": _sig("hq_attention", ctypes.c_int, _KV, _I32, _I64, _I32, _I32, _I64, _P, _I64, _P, _P, _P, _I32, _P, _P, _P, _P,
+                         ctypes.c_float, _I32, _P, _P, _SZ, _P),
     "hq_last_error": _sig("hq_last_error", ctypes.c_char_p),
     "hq_version": _sig("hq_version", _I32),
 }
@@ -416,3 +441,75 @@ def hq_moe_decode(desc, T, topk, E, H, I, x, topk_ids, topk_weights, w_gate_up, 
                                _at(w_gate_up, _packed_bytes(desc, E, 2 * I, H), _BYTES, dev, "w_gate_up"),
                                _at(w_down, _packed_bytes(desc, E, H, I), _BYTES, dev, "w_down"), _at(out, T * H, _BF16, dev, "out"),
                                _at(ws, ws_bytes, _BYTES, dev, "ws"), ws_bytes, _stream_at(stream, dev)))
+
+
+# ---- around the products: norm, cache, attention ------------------------------------------------
+_E8M0 = (1, (torch.uint8,))
+#: act_fmt -> element type of y, columns of x that one element of y holds, and the same of the scales (0: one a row)
+_NORM_OUT = {
+    HQ_ACT_BF16: (_BF16, 1, None, 0),
+    HQ_ACT_INT8_PER_TOKEN: ((1, (torch.int8, torch.uint8)), 1, _FP32, 0),
+    HQ_ACT_FP8E4M3_PER_TOKEN: ((1, (torch.float8_e4m3fn, torch.uint8, torch.int8)), 1, _FP32, 0),
+    HQ_ACT_FP8E4M3_BLOCK128: ((1, (torch.float8_e4m3fn, torch.uint8, torch.int8)), 1, _FP32, 128),
+    HQ_ACT_MXFP8: ((1, (torch.float8_e4m3fn, torch.uint8, torch.int8)), 1, _E8M0, 32),
+    HQ_ACT_MXFP4: ((1, (torch.uint8, torch.int8)), 2, _E8M0, 32),
+}
+
+
+def hq_rms_norm(act_fmt, M, K, x, residual, weight, eps, residual_out, y, y_scale=None, y_bf16=None, stream=None):
+    dev, n = _here(), M * K
+    kind, per, scale, block = _NORM_OUT.get(act_fmt, (_BYTES, 1, _BYTES, 0))
+    _check(_c["hq_rms_norm"](act_fmt, M, K, _at(x, n, _BF16, dev, "x"), _at(residual, n, _BF16, dev, "residual"), _at(weight, K, _BF16, dev, "weight"),
+                             eps, _at(residual_out, n, _BF16, dev, "residual_out"), _at(y, n // per, kind, dev, "y"),
+                             _at(y_scale, n // block if block else M, scale or _FP32, dev, "y_scale"), _at(y_bf16, n, _BF16, dev, "y_bf16"),
+                             _stream_at(stream, dev)))
+
+
+def hq_kv_cache_bytes(desc) -> int:
+    return _c["hq_kv_cache_bytes"](_d(desc))
+
+
+def _rows_at(x, rows, width, stride, dev, what):
+    """Device address of `rows` bf16 rows of `width` elements, `stride` elements apart: a tensor of such rows, or a
+    view of some columns of a wider one. What the tensor's own memory has to hold is checked, as _at does."""
+    if not isinstance(x, torch.Tensor):
+        return _at(x, rows * width, _BF16, dev, what)
+    inner, dense = 1, True
+    for n, step in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
+        dense &= n == 1 or step == inner
+        inner *= n
+    why = (f"holds {x.dtype}, not {torch.bfloat16}" if x.dtype not in _BF16[1] else
+           f"holds {tuple(x.shape)}, {rows} rows of {width} are needed" if x.dim() < 2 or x.shape[0] < rows or inner < width else
+           "must be contiguous within a row" if not dense else
+           f"has rows {x.stride(0)} elements apart, not {stride}" if rows > 1 and x.stride(0) != stride else
+           "must be on the current device" if x.get_device() != dev else None)
+    if why:
+        raise HQError(HQ_ERR_INVALID_ARGUMENT, f"{what} {why}")
+    return x.data_ptr()
+
+
+def _cache_at(desc, B, cu, kv_lens, page_table, table_width, k_pages, v_pages, k_scales, v_scales, dev):
+    codes, scales = hq_kv_cache_bytes(desc), desc.num_pages * desc.num_kv_heads
+    return (_at(cu, B + 1, _INT32, dev, "cu"), _at(kv_lens, B, _INT32, dev, "kv_lens"), _at(page_table, B * table_width, _INT32, dev, "page_table"),
+            table_width, _at(k_pages, codes, _BYTES, dev, "k_pages"), _at(v_pages, codes, _BYTES, dev, "v_pages"),
+            _at(k_scales, scales, _FP32, dev, "k_scales"), _at(v_scales, scales, _FP32, dev, "v_scales"))
+
+
+def hq_kv_append(desc, B, T, max_new, k, v, kv_stride, cu, kv_lens, page_table, table_width, k_pages, v_pages, k_scales, v_scales, stream=None):
+    dev, width = _here(), desc.num_kv_heads * desc.head_dim
+    _check(_c["hq_kv_append"](_d(desc), B, T, max_new, _rows_at(k, T, width, kv_stride, dev, "k"), _rows_at(v, T, width, kv_stride, dev, "v"), kv_stride,
+                              *_cache_at(desc, B, cu, kv_lens, page_table, table_width, k_pages, v_pages, k_scales, v_scales, dev),
+                              _stream_at(stream, dev)))
+
+
+def hq_attention_workspace_bytes(desc, B, T, Hq, max_q, max_kv) -> int:
+    return _c["hq_attention_workspace_bytes"](_d(desc), B, T, Hq, max_q, max_kv)
+
+
+def hq_attention(desc, B, T, Hq, max_q, max_kv, q, q_stride, cu, kv_lens, page_table, table_width, k_pages, v_pages, k_scales, v_scales, sm_scale,
+                 window, out, ws=None, ws_bytes=0, stream=None):
+    dev, width = _here(), Hq * desc.head_dim
+    _check(_c["hq_attention"](_d(desc), B, T, Hq, max_q, max_kv, _rows_at(q, T, width, q_stride, dev, "q"), q_stride,
+                              *_cache_at(desc, B, cu, kv_lens, page_table, table_width, k_pages, v_pages, k_scales, v_scales, dev),
+                              sm_scale, window, _at(out, T * width, _BF16, dev, "out"), _at(ws, ws_bytes, _BYTES, dev, "ws"), ws_bytes,
+                              _stream_at(stream, dev)))

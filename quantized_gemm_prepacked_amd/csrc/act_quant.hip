@@ -157,12 +157,6 @@ __global__ __launch_bounds__(kThreads) void silu_quant_kernel(const uint16_t* __
     *reinterpret_cast<uint2*>(qr + i) = quant8<ACT>(gated8(gr, I, i), s);
 }
 
-// e2m1 magnitude code of a >= 0 (exact binary32), ties to the even code, saturating at 6.
-__device__ __forceinline__ uint32_t e2m1_code(float a) {
-  return uint32_t(a > 0.25f) + uint32_t(a >= 0.75f) + uint32_t(a > 1.25f) + uint32_t(a >= 1.75f) +
-         uint32_t(a > 2.5f) + uint32_t(a >= 3.5f) + uint32_t(a > 5.0f);
-}
-
 __global__ __launch_bounds__(kThreads) void act_quant_mxfp4_kernel(const uint16_t* __restrict__ x,
                                                                    uint8_t* __restrict__ xq,
                                                                    uint8_t* __restrict__ xs,

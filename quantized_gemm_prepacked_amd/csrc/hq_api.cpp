@@ -690,4 +690,179 @@ hq_status hq_moe_decode(const hq_quant_desc* desc, int64_t T, int32_t topk, int3
   return check_hip(hq::launch_moe_decode(m, static_cast<hipStream_t>(stream)), "hq_moe_decode launch");
 }
 
+hq_status hq_rms_norm(int32_t act_fmt, int64_t M, int64_t K, const void* x, const void* residual, const void* weight,
+                      float eps, void* residual_out, void* y, void* y_scale, void* y_bf16, hq_stream_t stream) {
+  if (act_fmt < HQ_ACT_BF16 || act_fmt > HQ_ACT_FP8E4M3_BLOCK128) return fail(HQ_ERR_INVALID_ARGUMENT, "unknown act_fmt %d", act_fmt);
+  const bool mx = act_fmt == HQ_ACT_MXFP4 || act_fmt == HQ_ACT_MXFP8;
+  const int unit = act_fmt == HQ_ACT_FP8E4M3_BLOCK128 ? 128 : mx ? 32 : 8;
+  if (M < 0 || M > kMaxDim || K <= 0 || K > kMaxDim)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "M=%lld K=%lld out of range", (long long)M, (long long)K);
+  if (K % unit != 0 || K > 65536)
+    return fail(HQ_ERR_UNSUPPORTED, "K=%lld must be a multiple of %d for this format, and at most 65536", (long long)K, unit);
+  if (M * K > (int64_t(1) << 40)) return fail(HQ_ERR_UNSUPPORTED, "M*K must stay below 2^40");
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return fail(HQ_ERR_INVALID_ARGUMENT, "eps must be positive and finite");
+  if ((residual != nullptr) != (residual_out != nullptr))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "residual_out must be given with a residual, and only then");
+  if (act_fmt == HQ_ACT_BF16 && (y_scale || y_bf16))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "y_scale and y_bf16 must be NULL for HQ_ACT_BF16");
+  if (M == 0) return ok();
+  if (!x || !y) return fail(HQ_ERR_INVALID_ARGUMENT, "x and y must be non-NULL");
+  if (act_fmt != HQ_ACT_BF16 && !y_scale) return fail(HQ_ERR_INVALID_ARGUMENT, "y_scale must be non-NULL for this format");
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) || !aligned16(y) || !aligned16(y_bf16) ||
+      (!mx && (reinterpret_cast<uintptr_t>(y_scale) & 3u)))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "buffers must be 16-byte aligned, fp32 scales 4-byte aligned");
+  if (y == residual_out || y == residual || y_bf16 == y || (y_bf16 && (y_bf16 == residual_out || y_bf16 == residual)) ||
+      (act_fmt != HQ_ACT_BF16 && y == x) || (residual_out == x && (y == x || y_bf16 == x)))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "outputs must not share a buffer with each other or the residual, codes not with x");
+  hq::RmsNormCall a{};
+  a.act_fmt = act_fmt;
+  a.M = M;
+  a.K = K;
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.eps = eps;
+  a.residual_out = residual_out;
+  a.y = y;
+  a.y_scale = y_scale;
+  a.y_bf16 = y_bf16;
+  return check_hip(hq::launch_rms_norm(a, static_cast<hipStream_t>(stream)), "hq_rms_norm launch");
+}
+
+namespace {
+// The cache's description, and the sizes and device arrays that name a call's sequences.
+hq_status check_kv(const hq_kv_desc* d, hq::KvCall* c) {
+  if (!d) return fail(HQ_ERR_INVALID_ARGUMENT, "desc is NULL");
+  if (d->struct_size != sizeof(hq_kv_desc))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "desc->struct_size %u != %zu", d->struct_size, sizeof(hq_kv_desc));
+  if (d->kv_fmt != HQ_KV_FP8_E4M3 && d->kv_fmt != HQ_KV_INT8) return fail(HQ_ERR_INVALID_ARGUMENT, "unknown kv_fmt %d", d->kv_fmt);
+  if (d->num_kv_heads <= 0 || d->num_kv_heads > 1024 || d->num_pages <= 0 || d->num_pages > kMaxDim)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "num_kv_heads=%d num_pages=%d out of range", d->num_kv_heads, d->num_pages);
+  if (d->head_dim != 64 && d->head_dim != 96 && d->head_dim != 128 && d->head_dim != 192 && d->head_dim != 256)
+    return fail(HQ_ERR_UNSUPPORTED, "head_dim=%d: 64, 96, 128, 192 or 256", d->head_dim);
+  int shift = 4;
+  while (shift <= 8 && d->page_size != 1 << shift) ++shift;
+  if (shift > 8) return fail(HQ_ERR_UNSUPPORTED, "page_size=%d: 16, 32, 64, 128 or 256", d->page_size);
+  c->fmt = d->kv_fmt;
+  c->H = d->num_kv_heads;
+  c->D = d->head_dim;
+  c->page_shift = shift;
+  c->num_pages = d->num_pages;
+  return HQ_OK;
+}
+
+hq_status check_sequences(int32_t B, int64_t T, int32_t max_new, const char* what, hq::KvCall* c) {
+  if (B < 0 || B > 65535 || T < 0 || T > (int64_t(1) << 24) || max_new < 0 || max_new > (1 << 24))
+    return fail(HQ_ERR_INVALID_ARGUMENT, "B=%d T=%lld %s=%d out of range", B, (long long)T, what, max_new);
+  c->B = B;
+  c->T = T;
+  c->max_new = int(std::min<int64_t>(max_new, T));
+  return HQ_OK;
+}
+
+hq_status check_cache(const int32_t* cu, const int32_t* kv_lens, const int32_t* page_table, int32_t table_width, const void* k_pages,
+                      const void* v_pages, const float* k_scales, const float* v_scales, hq::KvCall* c) {
+  if (table_width <= 0 || (int64_t(table_width) << c->page_shift) > kMaxDim)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "table_width=%d: at least 1, and at most 2^30 positions", table_width);
+  if (!cu || !kv_lens || !page_table || !k_pages || !v_pages || !k_scales || !v_scales)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "cu, kv_lens, page_table, k_pages, v_pages, k_scales and v_scales must be non-NULL");
+  if (!aligned16(k_pages) || !aligned16(v_pages)) return fail(HQ_ERR_INVALID_ARGUMENT, "k_pages and v_pages must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(cu) | reinterpret_cast<uintptr_t>(kv_lens) | reinterpret_cast<uintptr_t>(page_table) |
+       reinterpret_cast<uintptr_t>(k_scales) | reinterpret_cast<uintptr_t>(v_scales)) & 3u)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "cu, kv_lens, page_table, k_scales and v_scales must be 4-byte aligned");
+  c->cu = cu;
+  c->kv_lens = kv_lens;
+  c->table = page_table;
+  c->width = table_width;
+  c->capacity = table_width << c->page_shift;
+  c->k_pages = const_cast<void*>(k_pages);
+  c->v_pages = const_cast<void*>(v_pages);
+  c->k_scales = const_cast<float*>(k_scales);
+  c->v_scales = const_cast<float*>(v_scales);
+  return HQ_OK;
+}
+
+hq_status check_attention(const hq_kv_desc* desc, int32_t B, int64_t T, int32_t Hq, int32_t max_q, int64_t max_kv, hq::KvCall* c) {
+  hq_status s = check_kv(desc, c);
+  if (s != HQ_OK) return s;
+  if ((s = check_sequences(B, T, max_q, "max_q", c)) != HQ_OK) return s;
+  if (Hq <= 0 || Hq % c->H != 0 || Hq / c->H > 128)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "Hq=%d must be a multiple of num_kv_heads=%d, at most 128 times it", Hq, c->H);
+  if (max_kv < 0 || max_kv > kMaxDim) return fail(HQ_ERR_INVALID_ARGUMENT, "max_kv=%lld out of range", (long long)max_kv);
+  if (T * Hq * c->D >= (int64_t(1) << 40)) return fail(HQ_ERR_UNSUPPORTED, "T*Hq*head_dim must stay below 2^40");
+  c->Hq = Hq;
+  c->G = Hq / c->H;
+  // a launch holds fewer than 2^32 threads
+  if (hq::attention_groups(*c) > (int64_t(1) << 22))
+    return fail(HQ_ERR_UNSUPPORTED, "B=%d max_q=%d Hq=%d: too many rows for one call", B, max_q, Hq);
+  return HQ_OK;
+}
+}  // namespace
+
+size_t hq_kv_cache_bytes(const hq_kv_desc* desc) {
+  hq::KvCall c{};
+  if (check_kv(desc, &c) != HQ_OK) return 0;
+  return size_t(c.num_pages) * size_t(c.H) * (size_t(c.D) << c.page_shift);
+}
+
+hq_status hq_kv_append(const hq_kv_desc* desc, int32_t B, int64_t T, int32_t max_new, const void* k, const void* v,
+                       int64_t kv_stride, const int32_t* cu, const int32_t* kv_lens, const int32_t* page_table,
+                       int32_t table_width, void* k_pages, void* v_pages, float* k_scales, float* v_scales,
+                       hq_stream_t stream) {
+  hq::KvCall c{};
+  hq_status s = check_kv(desc, &c);
+  if (s != HQ_OK) return s;
+  if ((s = check_sequences(B, T, max_new, "max_new", &c)) != HQ_OK) return s;
+  if (kv_stride < int64_t(c.H) * c.D || kv_stride > kMaxDim || kv_stride % 8 != 0)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "kv_stride=%lld: at least num_kv_heads * head_dim, a multiple of 8", (long long)kv_stride);
+  if (B == 0 || T == 0 || max_new == 0) return ok();
+  if ((s = check_cache(cu, kv_lens, page_table, table_width, k_pages, v_pages, k_scales, v_scales, &c)) != HQ_OK) return s;
+  // a launch holds fewer than 2^32 threads
+  if (((int64_t(c.max_new) >> c.page_shift) + 2) * c.H * B > (int64_t(1) << 22))
+    return fail(HQ_ERR_UNSUPPORTED, "B=%d max_new=%d: too many pages for one call", B, max_new);
+  if (!k || !v) return fail(HQ_ERR_INVALID_ARGUMENT, "k and v must be non-NULL");
+  if (!aligned16(k) || !aligned16(v)) return fail(HQ_ERR_INVALID_ARGUMENT, "k and v must be 16-byte aligned");
+  c.k = k;
+  c.v = v;
+  c.kv_stride = kv_stride;
+  return check_hip(hq::launch_kv_append(c, static_cast<hipStream_t>(stream)), "hq_kv_append launch");
+}
+
+size_t hq_attention_workspace_bytes(const hq_kv_desc* desc, int32_t B, int64_t T, int32_t Hq, int32_t max_q, int64_t max_kv) {
+  hq::KvCall c{};
+  if (check_attention(desc, B, T, Hq, max_q, max_kv, &c) != HQ_OK || B == 0 || T == 0 || max_q == 0) return 0;
+  return hq::plan_attention(c, max_kv).ws_bytes;
+}
+
+hq_status hq_attention(const hq_kv_desc* desc, int32_t B, int64_t T, int32_t Hq, int32_t max_q, int64_t max_kv,
+                       const void* q, int64_t q_stride, const int32_t* cu, const int32_t* kv_lens,
+                       const int32_t* page_table, int32_t table_width, const void* k_pages, const void* v_pages,
+                       const float* k_scales, const float* v_scales, float sm_scale, int32_t window, void* out, void* ws,
+                       size_t ws_bytes, hq_stream_t stream) {
+  hq::KvCall c{};
+  hq_status s = check_attention(desc, B, T, Hq, max_q, max_kv, &c);
+  if (s != HQ_OK) return s;
+  if (q_stride < int64_t(Hq) * c.D || q_stride > kMaxDim || q_stride % 8 != 0)
+    return fail(HQ_ERR_INVALID_ARGUMENT, "q_stride=%lld: at least Hq * head_dim, a multiple of 8", (long long)q_stride);
+  if (!std::isfinite(sm_scale)) return fail(HQ_ERR_INVALID_ARGUMENT, "sm_scale must be finite");
+  if (window < 0) return fail(HQ_ERR_INVALID_ARGUMENT, "window=%d must not be negative", window);
+  if (B == 0 || T == 0 || max_q == 0) return ok();
+  if ((s = check_cache(cu, kv_lens, page_table, table_width, k_pages, v_pages, k_scales, v_scales, &c)) != HQ_OK) return s;
+  if (!q || !out) return fail(HQ_ERR_INVALID_ARGUMENT, "q and out must be non-NULL");
+  if (!aligned16(q) || !aligned16(out) || !aligned16(ws)) return fail(HQ_ERR_INVALID_ARGUMENT, "q, out and ws must be 16-byte aligned");
+  if (out == q && q_stride != int64_t(Hq) * c.D) return fail(HQ_ERR_INVALID_ARGUMENT, "out may be q only where q_stride is Hq * head_dim");
+  const hq::AttentionPlan p = hq::plan_attention(c, max_kv);
+  if (ws_bytes < p.ws_bytes || (p.ws_bytes && !ws)) return fail(HQ_ERR_WORKSPACE, "workspace %zu < required %zu", ws ? ws_bytes : size_t(0), p.ws_bytes);
+  c.q = q;
+  c.q_stride = q_stride;
+  c.scale_log2 = float(double(sm_scale) * 1.4426950408889634);
+  c.window = window;
+  c.out = out;
+  c.n_split = p.n_split;
+  c.by_token = p.by_token;
+  c.ws_o = static_cast<float*>(ws);
+  c.ws_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.ml_offset);
+  return check_hip(hq::launch_attention(c, static_cast<hipStream_t>(stream)), "hq_attention launch");
+}
+
 }  // extern "C"

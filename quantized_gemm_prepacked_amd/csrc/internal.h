@@ -132,6 +132,56 @@ struct MoeDecodeCall {
 size_t moe_decode_ws_bytes(const Combo& c, int64_t T, int32_t topk, int32_t E, int64_t H, int64_t I);
 hipError_t launch_moe_decode(const MoeDecodeCall& m, hipStream_t s);
 
+// hq_rms_norm, validated.
+struct RmsNormCall {
+  int act_fmt;
+  int64_t M, K;
+  const void* x;
+  const void* residual;
+  const void* weight;
+  float eps;
+  void* residual_out;
+  void* y;
+  void* y_scale;
+  void* y_bf16;
+};
+hipError_t launch_rms_norm(const RmsNormCall& a, hipStream_t s);
+
+// hq_kv_append / hq_attention, validated.
+struct KvCall {
+  int fmt, H, D, page_shift, num_pages;   // the cache
+  int B, max_new;
+  int64_t T;
+  const int32_t* cu;
+  const int32_t* kv_lens;
+  const int32_t* table;
+  int width, capacity;                    // pages and positions of a sequence, at most
+  void* k_pages;
+  void* v_pages;
+  float* k_scales;
+  float* v_scales;
+  const void* k;                          // append
+  const void* v;
+  int64_t kv_stride;
+  const void* q;                          // attention
+  int64_t q_stride;
+  int Hq, G, window, n_split;
+  bool by_token;                          // partial results by row of q (else by sequence and token)
+  float scale_log2;                       // sm_scale * log2(e)
+  void* out;
+  float* ws_o;                            // partial results: [row][part][D], and (maximum, sum) of each part
+  float* ws_ml;
+};
+hipError_t launch_kv_append(const KvCall& c, hipStream_t s);
+struct AttentionPlan {
+  int n_split;
+  bool by_token;
+  size_t ml_offset, ws_bytes;
+};
+int64_t attention_groups(const KvCall& c);   // workgroups without a split of the positions
+AttentionPlan plan_attention(const KvCall& c, int64_t max_kv);
+hipError_t launch_attention(const KvCall& c, hipStream_t s);
+
 hipError_t launch_moe_align(const int32_t* topk_ids, int64_t T, int32_t topk, int32_t E,
                             int32_t block_m, int32_t* sorted_ids, int32_t* block_expert,
                             int32_t* expert_offsets, int32_t* num_padded, void* ws,
