@@ -526,8 +526,9 @@ hq_status hq_moe_decode(const hq_quant_desc* desc, int64_t T, int32_t topk, int3
  *   v[m, k] = fp32( fp32( h[m, k] * r[m] ) * weight[k] )        (weight NULL: 1)
  *   HQ_ACT_BF16   y = bf16(v), [M, K]; y_scale and y_bf16 NULL
  *   other act_fmt y, y_scale = the codes and scales of v by the rule of hq_quantize_activations for
- *                 that format, in its layouts (the GEMM's `a` and `a_scale`); v is not rounded to bf16
- *                 on the way. y_bf16, if not NULL, receives bf16(v) as well (the router of an MoE
+ *                 that format, in its layouts (the GEMM's `a` and `a_scale`), but fp32 scales are the
+ *                 product fp32( max|v| * fp32(1 / Q) ), at most a unit in the last place off that
+ *                 call's quotient; v is not rounded to bf16 on the way. y_bf16, if not NULL, receives bf16(v) as well (the router of an MoE
  *                 block reads it, where the experts read the codes).
  * Since the sum is in binary64 a row's result does not depend on how the row is split over threads.
  * act_fmt       HQ_ACT_BF16, HQ_ACT_INT8_PER_TOKEN, HQ_ACT_FP8E4M3_PER_TOKEN,
@@ -585,7 +586,7 @@ size_t hq_kv_cache_bytes(const hq_kv_desc* desc);
 
 /* ---------------------------------------------------------------------------------------------
  * Append to the cache (device). For each page that receives tokens, head, and K and V apart, with Q =
- * 448 (e4m3) or 127 (INT8) and a = fp32(the largest |value| of its new tokens / Q):
+ * 448 (e4m3) or 127 (INT8) and a = fp32(the largest |value| of its new tokens * fp32(1 / Q)):
  *   s = a                  if the page's first slot is among the new ones, or its scale is 0
  *   s = scale * 2^e        otherwise, e >= 0 the smallest with a <= scale * 2^e
  *   new codes              clamp(rne(fp32(value / s))), as hq_quantize_activations; 0 where s = 0

@@ -29,8 +29,8 @@ def ref_rms_norm(x: np.ndarray, residual, weight, eps: float):
 
 
 def _scaled(v: np.ndarray, largest: float):
-    """(v / s, s) with s = fp32(max |v| / largest) over the last axis, 1 where that is 0."""
-    s = (np.abs(v).max(-1) / np.float32(largest)).astype(np.float32)
+    """(v / s, s) with s = fp32(max |v| * fp32(1 / largest)) over the last axis, 1 where that is 0."""
+    s = np.abs(v).max(-1).astype(np.float32) * (np.float32(1) / np.float32(largest))
     s = np.where(s == 0, np.float32(1), s).astype(np.float32)
     return (v / s[..., None]).astype(np.float32), s
 
@@ -58,7 +58,7 @@ def quantize_values(v: np.ndarray, fmt: str):
 
 
 # ---- the cache ----------------------------------------------------------------------------------
-LARGEST = {"fp8": np.float32(448), "int8": np.float32(127)}
+UNIT = {"fp8": np.float32(1) / np.float32(448), "int8": np.float32(1) / np.float32(127)}
 
 
 def _codes(q: np.ndarray, fmt: str) -> np.ndarray:
@@ -85,7 +85,6 @@ def ref_kv_append(fmt: str, x: np.ndarray, is_value: bool, cu, lens, table, page
     pages, scales = pages.copy(), scales.copy()
     T, H, D = x.shape
     P = pages.shape[3] if is_value else pages.shape[2]
-    Q = LARGEST[fmt]
     for b, first, n, length in _sequences(cu, lens, T, T if max_new is None else max_new, table.shape[1] * P):
         start = max(length - n, 0)
         for p in range(start // P, -(-length // P)):
@@ -98,7 +97,7 @@ def ref_kv_append(fmt: str, x: np.ndarray, is_value: bool, cu, lens, table, page
                 nan = (bits & 0x7FFF) > 0x7F80
                 bits = np.where((bits & 0x7FFF) == 0x7F80, bits - 1, bits)       # infinities
                 v = np.where(nan, 0.0, decode_bf16(np.where(nan, 0, bits).astype(np.uint16))).astype(np.float32)
-                need = np.float32(np.abs(v).max() / Q)
+                need = np.abs(v).max() * UNIT[fmt]
                 old = pages[page, h].T if is_value else pages[page, h]           # [P, D], a view
                 s = need
                 if lo > p * P and scales[page, h] != 0:

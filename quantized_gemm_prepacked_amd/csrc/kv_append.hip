@@ -43,7 +43,7 @@ __device__ __forceinline__ uint32_t regrown(uint32_t code, float down) {
 
 template <int FMT, int THREADS>
 __global__ __launch_bounds__(THREADS) void kv_append_kernel(KvCall c) {
-  constexpr float kLargest = FMT == HQ_KV_INT8 ? 127.0f : 448.0f;
+  constexpr float kUnit = FMT == HQ_KV_INT8 ? 1.0f / 127.0f : 1.0f / 448.0f;
   const int b = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
   const int head = int(blockIdx.x % unsigned(c.H));
@@ -77,7 +77,7 @@ __global__ __launch_bounds__(THREADS) void kv_append_kernel(KvCall c) {
 #pragma unroll
     for (int w = 0; w < THREADS / 64; ++w) top = max(top, tops[w]);
   }
-  const float need = __uint_as_float(top << 16) / kLargest;
+  const float need = __uint_as_float(top << 16) * kUnit;
   float s = need, down = 1.0f;
   if (slot0 != 0) {
     const float held = *scale;

@@ -39,10 +39,10 @@ __device__ __forceinline__ T row_reduce(T v, T* slot, F join) {
   return v;
 }
 
-// The scale s of a row or block whose largest |v| is amax, and 1 / s for quotient().
+// The scale of a row or block whose largest |v| is amax.
 template <int ACT>
 __device__ __forceinline__ float scale_of(float amax) {
-  const float s = amax / (ACT == HQ_ACT_INT8_PER_TOKEN ? 127.0f : 448.0f);
+  const float s = amax * (ACT == HQ_ACT_INT8_PER_TOKEN ? 1.0f / 127.0f : 1.0f / 448.0f);
   return s == 0.0f ? 1.0f : s;
 }
 
