@@ -120,13 +120,14 @@ def ref_kv_append(fmt: str, x: np.ndarray, is_value: bool, cu, lens, table, page
 def ref_attention(fmt: str, q: np.ndarray, cu, lens, table, k_pages, v_pages, k_scales, v_scales, sm_scale: float, window: int, out: np.ndarray,
                   max_q=None):
     """Attention row by row in float64. q: bf16 bits [T, Hq, D]; out: float64 [T, Hq, D], rows that are left out keep what
-    they hold. Returns (out, size, spread, reach) with, per output value, size = sum p |v| / sum p and spread = sqrt(sum
-    (p v)^2) / sum p (which bound the effect of rounding each p), and per row reach = max over the seen j of sm_scale *
-    sum |q k| (which bounds that of rounding in the scores)."""
+    they hold. Returns (out, size, spread, grain, reach) with, per output value, size = sum p |v| / sum p and spread = sqrt(sum
+    (p v)^2) / sum p (which bound the effect of rounding each weight p * scale relative to itself), grain = max (p * scale)
+    * sum |code| / sum p (relative to the row's largest), and per row reach = max over the seen j of sm_scale * sum |q k|
+    (which bounds that of rounding in the scores)."""
     out = out.copy()
     T, Hq, D = q.shape
     n, H, P, _ = k_pages.shape
-    size, spread, reach = np.zeros(out.shape), np.zeros(out.shape), np.zeros((T, Hq))
+    size, spread, grain, reach = np.zeros(out.shape), np.zeros(out.shape), np.zeros(out.shape), np.zeros((T, Hq))
     qv = decode_bf16(q)
     for b, first, count, length in _sequences(cu, lens, T, T if max_q is None else max_q, table.shape[1] * P):
         j = np.arange(length)
@@ -137,7 +138,8 @@ def ref_attention(fmt: str, q: np.ndarray, cu, lens, table, k_pages, v_pages, k_
             # codes of slots that hold nothing may be anything: only what a row sees enters
             with np.errstate(invalid="ignore"):
                 k = _values(k_pages[at, h, j % P], fmt) * k_scales[at, h].astype(np.float64)[:, None]
-                v = _values(v_pages[at, h, :, j % P], fmt) * v_scales[at, h].astype(np.float64)[:, None]
+                code, scale = _values(v_pages[at, h, :, j % P], fmt), v_scales[at, h].astype(np.float64)
+                v = code * scale[:, None]
             for i in range(count):
                 pos = length - count + i
                 seen = there & (j <= pos) & ((j > pos - window) if window else True)
@@ -151,5 +153,6 @@ def ref_attention(fmt: str, q: np.ndarray, cu, lens, table, k_pages, v_pages, k_
                     out[r, c] = p @ v[seen] / p.sum()
                     size[r, c] = p @ np.abs(v[seen]) / p.sum()
                     spread[r, c] = np.sqrt((p * p) @ (v[seen] ** 2)) / p.sum()
+                    grain[r, c] = (p * scale[seen]).max() * np.abs(code[seen]).sum(0) / p.sum()
                     reach[r, c] = abs(sm_scale) * (np.abs(k[seen]) @ np.abs(qv[r, c])).max()
-    return out, size, spread, reach
+    return out, size, spread, grain, reach

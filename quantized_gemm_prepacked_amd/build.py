@@ -20,7 +20,7 @@ OUT = os.path.join(PKG, "libhq.so")
 PROBE_OUT = os.path.join(PKG, "libhq_probe.so")
 BUILD = os.path.join(PKG, "_build")
 
-SOURCES = ["hq_api.cpp", "prepack.cpp", "gemm_dispatch.hip", "gemm_skinny.hip", "gemm_tiled.hip", "gemm_pipe.hip", "gemm_pingpong.hip", "moe_align.hip", "moe_layer.hip", "act_quant.hip", "moe_route.hip", "decode_gemv.hip", "decode_moe.hip", "rms_norm.hip", "kv_append.hip", "attention.hip", "tuning_table.cpp"]
+SOURCES = ["hq_api.cpp", "prepack.cpp", "gemm_dispatch.hip", "gemm_skinny.hip", "gemm_tiled.hip", "gemm_pipe.hip", "gemm_pingpong.hip", "moe_align.hip", "moe_layer.hip", "act_quant.hip", "moe_route.hip", "decode_gemv.hip", "decode_moe.hip", "rms_norm.hip", "kv_append.hip", "attention.hip", "attention_tile.hip", "tuning_table.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

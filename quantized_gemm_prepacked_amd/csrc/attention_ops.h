@@ -1,0 +1,199 @@
+// attention_ops.h -- what the two attention kernels share: the lane layout of a block's scores, the running
+// softmax of its rows, and how a sequence's positions are shared out.
+//
+// A wave works on NQ tiles of 16 rows (query tokens times the heads that share a head of the cache) and blocks of 64
+// positions. In every product a row is a matrix column: lane l holds, for row l % 16 of each tile, the 16 scores of
+// positions 16 (l / 16) .. + 15 of the block (element r of vector i: position 4 i + r of those). 16 positions never
+// cross a page, so a lane has one scale of K, a factor of its scores, and one of V, a factor of its weights. The scores
+// leave the first product as the second one takes them: nothing is exchanged between lanes but the row's maxima.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_ops.h"
+#include "internal.h"
+#include "kv_cache.h"
+
+namespace hq {
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kBlock = 64;   // positions of a block
+
+// Eight codes as bf16 (keys, beside the queries) or as fp16 (values): exact in both.
+template <int FMT>
+__device__ __forceinline__ bf16x8 codes_bf16(uint32_t lo, uint32_t hi) {
+  if constexpr (FMT == HQ_KV_INT8) return dequant_int8x8(lo, hi);
+  else return dequant_fp8x8(lo, hi);
+}
+
+template <int FMT>
+__device__ __forceinline__ f16x8 codes_f16(uint32_t lo, uint32_t hi) {
+  if constexpr (FMT == HQ_KV_INT8) {
+    // 0x6400 | u is 1024 + u in fp16; u = code + 128
+    const auto two = [](uint32_t u, uint32_t sel) {
+      return __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, sel)) - f16x2{_Float16(1152), _Float16(1152)};
+    };
+    lo ^= 0x80808080u;
+    hi ^= 0x80808080u;
+    const f16x2 a = two(lo, 0x04010400u), b = two(lo, 0x04030402u), c = two(hi, 0x04010400u), d = two(hi, 0x04030402u);
+    return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+  } else {
+    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false), b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+    const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false), d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+    return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+  }
+}
+
+__device__ __forceinline__ f32x4 mfma_f16(f16x8 a, f16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }   // results below 2^-126 are 0
+
+// Maximum and sum over the four lanes that hold one row (lanes l, l ^ 16, l ^ 32, l ^ 48).
+template <class F>
+__device__ __forceinline__ float over_quarters(float v, F join) {
+  auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = join(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return join(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+__device__ __forceinline__ float row_max(float v) {
+  return over_quarters(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float row_sum(float v) {
+  return over_quarters(v, [](float a, float b) { return a + b; });
+}
+
+// Running softmax of the rows a lane holds. With x = sm_scale * log2(e) * q . k and s_v the scale of the position's values:
+//   top = max x,  sum = sum 2^(x - top)  (this lane's positions),
+//   ref = max (x + log2 s_v),  acc = sum 2^(x + log2 s_v - ref) * code.
+// The weights 2^(x + log2 s_v - ref) enter the product with the codes as fp16: the largest of a row is 1, each is off by 2^-11
+// of itself or 2^-25 of the largest, whatever the scales (a bf16 weight, off by 2^-8, made the result's error half as
+// large again as the rounding of the result itself). Statistics and sums are fp32.
+template <int NQ, int TILES>
+struct Rows {
+  f32x4 acc[NQ][TILES];
+  float top[NQ], ref[NQ], sum[NQ];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      top[n] = ref[n] = -INFINITY;
+      sum[n] = 0.0f;
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) acc[n][t] = f32x4{0, 0, 0, 0};
+    }
+  }
+
+  // A block's scores (products of q and k codes; ks >= 0 makes them x; -infinity where masked, then ks = 1) become weights.
+  // lv = log2 of the values' scale, -infinity where that is 0 or there is no page.
+  __device__ __forceinline__ void step(const f32x4 (&score)[NQ][4], float ks, float lv, f16x8 (&weight)[NQ][2]) {
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      float m = score[n][0][0];
+#pragma unroll
+      for (int e = 1; e < 16; ++e) m = fmaxf(m, score[n][e >> 2][e & 3]);
+      m *= ks;
+      const float top1 = fmaxf(top[n], row_max(m)), ref1 = fmaxf(ref[n], row_max(m + lv));
+      // rows that have seen nothing yet have maxima of -infinity
+      const float at = top1 == -INFINITY ? 0.0f : top1, wat = ref1 == -INFINITY ? 0.0f : ref1;
+      const float shrink = exp2_fast(top[n] - at), wshrink = exp2_fast(ref[n] - wat);
+      if (__any(top1 > top[n] || ref1 > ref[n])) {
+        sum[n] *= shrink;
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[n][t][r] *= wshrink;
+      }
+      top[n] = top1;
+      ref[n] = ref1;
+      const float f = exp2_fast(lv + (at - wat));
+      float p[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) p[e] = exp2_fast(fmaf(score[n][e >> 2][e & 3], ks, -at));
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        f16x8 w;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const f32x2 two = {p[8 * u + j] * f, p[8 * u + j + 1] * f};
+          const f16x2 h = __builtin_convertvector(two, f16x2);
+          w[j] = h[0];
+          w[j + 1] = h[1];
+        }
+        weight[n][u] = w;
+      }
+      sum[n] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7])) + (((p[8] + p[9]) + (p[10] + p[11])) + ((p[12] + p[13]) + (p[14] + p[15])));
+    }
+  }
+
+  // What turns acc into sum 2^(x - top) * value.
+  __device__ __forceinline__ float unit(int n) const { return ref[n] == -INFINITY ? 0.0f : exp2f(ref[n] - top[n]); }
+};
+
+// Scores of positions that row `pos` (a position) does not see become -infinity, the others x. vg: the lane's first position.
+template <int NQ>
+__device__ __forceinline__ void mask_scores(f32x4 (&score)[NQ][4], const int (&pos)[NQ], int vg, int window, bool there, float ks) {
+#pragma unroll
+  for (int n = 0; n < NQ; ++n)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int t = vg + e;
+      const bool seen = there && t <= pos[n] && (window == 0 || t > pos[n] - window);
+      score[n][e >> 2][e & 3] = seen ? score[n][e >> 2][e & 3] * ks : -INFINITY;
+    }
+}
+
+// 16 codes of values (positions vg ..) with those behind the sequence's end, which are whatever the page holds, made 0: a NaN
+// there times a weight of 0 is NaN.
+__device__ __forceinline__ u32x4 live_codes(u32x4 v, int live) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int left = live - 4 * w;
+    v[w] &= left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+  }
+  return v;
+}
+
+// The blocks that the rows [r0, r0 + rows) of a sequence see, and how they are shared out: part s takes the blocks
+// first + s * each .. The join reads the same numbers.
+struct Share {
+  int first, end, each, parts;
+};
+
+__device__ __forceinline__ Share share_of(const KvCall& c, const KvSeq& q, int r0, int rows) {
+  const int last = min(r0 + rows, q.n * c.G) - 1;
+  const int hi = q.len - q.n + last / c.G;                    // position of the last row
+  const int lo = q.len - q.n + r0 / c.G - c.window + 1;       // first position that the first row sees
+  Share s;
+  s.first = c.window > 0 ? max(lo, 0) / kBlock : 0;
+  s.end = hi < 0 ? s.first : hi / kBlock + 1;
+  const int blocks = s.end - s.first;
+  s.each = max(c.each, (blocks + c.n_split - 1) / c.n_split);
+  s.parts = max((blocks + s.each - 1) / s.each, 1);
+  return s;
+}
+
+// Where the partial results of (token i of sequence b, query head) begin, in rows of n_split parts.
+__device__ __forceinline__ int64_t part_row(const KvCall& c, const KvSeq& q, int b, int i, int head) {
+  const int64_t token = c.by_token ? int64_t(q.first) + i : int64_t(b) * c.hi_n + i;
+  return (token * c.Hq + head) * c.n_split;
+}
+
+// The sequences of this launch: those with lo_n .. hi_n new tokens.
+__device__ __forceinline__ KvSeq attention_sequence(const KvCall& c, int b) {
+  KvSeq q = kv_sequence(c, b);
+  if (q.n < c.lo_n || q.n > c.hi_n) q.n = 0;
+  return q;
+}
+
+// 16-byte piece of a query row, negated where sm_scale is negative (its size alone is a factor of the keys' scale).
+__device__ __forceinline__ bf16x8 query8(const void* p, uint32_t sign) {
+  u32x4 v = ldg16(p);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] ^= sign;
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+}  // namespace hq

@@ -855,14 +855,11 @@ hq_status hq_attention(const hq_kv_desc* desc, int32_t B, int64_t T, int32_t Hq,
   if (ws_bytes < p.ws_bytes || (p.ws_bytes && !ws)) return fail(HQ_ERR_WORKSPACE, "workspace %zu < required %zu", ws ? ws_bytes : size_t(0), p.ws_bytes);
   c.q = q;
   c.q_stride = q_stride;
-  c.scale_log2 = float(double(sm_scale) * 1.4426950408889634);
+  c.scale_log2 = float(std::fabs(double(sm_scale)) * 1.4426950408889634);
+  c.q_sign = sm_scale < 0.0f ? 0x80008000u : 0u;
   c.window = window;
   c.out = out;
-  c.n_split = p.n_split;
-  c.by_token = p.by_token;
-  c.ws_o = static_cast<float*>(ws);
-  c.ws_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.ml_offset);
-  return check_hip(hq::launch_attention(c, static_cast<hipStream_t>(stream)), "hq_attention launch");
+  return check_hip(hq::launch_attention(c, p, static_cast<uint8_t*>(ws), static_cast<hipStream_t>(stream)), "hq_attention launch");
 }
 
 }  // extern "C"

@@ -165,22 +165,28 @@ struct KvCall {
   int64_t kv_stride;
   const void* q;                          // attention
   int64_t q_stride;
-  int Hq, G, window, n_split;
-  bool by_token;                          // partial results by row of q (else by sequence and token)
-  float scale_log2;                       // sm_scale * log2(e)
+  int Hq, G, window;
+  float scale_log2;                       // |sm_scale| * log2(e)
+  uint32_t q_sign;                        // sm_scale < 0: the signs of two bf16
   void* out;
-  float* ws_o;                            // partial results: [row][part][D], and (maximum, sum) of each part
+  int lo_n, hi_n;                         // one launch: sequences with that many new tokens,
+  int n_split, each;                      // parts of the positions at most, and blocks of a part at least,
+  bool by_token;                          // partial results by row of q (else by sequence and token),
+  float* ws_o;                            // [row][part][D], and (maximum, sum) of each part
   float* ws_ml;
 };
 hipError_t launch_kv_append(const KvCall& c, hipStream_t s);
+int64_t attention_groups(const KvCall& c);   // workgroups without a split of the positions, at most
+// Sequences of up to `few` new tokens have a launch of their own, those with more (many) another.
 struct AttentionPlan {
-  int n_split;
-  bool by_token;
-  size_t ml_offset, ws_bytes;
+  int few;
+  bool many, few_by_token;
+  int few_split, few_each, many_split, many_each;
+  size_t few_o, few_ml, many_o, many_ml, ws_bytes;
 };
-int64_t attention_groups(const KvCall& c);   // workgroups without a split of the positions
 AttentionPlan plan_attention(const KvCall& c, int64_t max_kv);
-hipError_t launch_attention(const KvCall& c, hipStream_t s);
+hipError_t launch_attention(const KvCall& c, const AttentionPlan& p, uint8_t* ws, hipStream_t s);
+hipError_t launch_attention_tiles(const KvCall& c, hipStream_t s);
 
 hipError_t launch_moe_align(const int32_t* topk_ids, int64_t T, int32_t topk, int32_t E,
                             int32_t block_m, int32_t* sorted_ids, int32_t* block_expert,

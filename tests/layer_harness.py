@@ -49,29 +49,31 @@ def kv_case(g: np.random.Generator, fmt: str, H: int, D: int, P: int, new: list,
             "k_scales": k_scales, "v_scales": v_scales}
 
 
-def attention_bounds(ref, size, spread, reach, D: int, tokens: int):
+def attention_bounds(ref, size, spread, grain, reach, D: int, tokens: int):
     """(elementwise, squared per element) bounds of a result's error.
     Score: a dot product of D terms in fp32, each addition off by 2^-23 of the terms' size (a matrix instruction may
     truncate), and its two factors, the subtraction of the maximum and the exponential, together at most 8 steps more:
     each p off by 2 * 2^-23 (D + 8) reach relative (the factor 2 for the exponential's curvature and log2 e), plus 2^-21 for
-    the exponential itself. p * scale rounded to bf16: 2^-8. Sums over the tokens: at most tokens / 32 + 40 additions one after
+    the exponential itself. p * scale as an fp16 relative to the row's largest: off by 2^-11 of itself or 2^-25 of that. Sums over the tokens: at most tokens / 32 + 40 additions one after
     another in a lane and 64 joins, 2^-23 each, of sum p |v| and sum p. The result rounded to bf16: 2^-8 of it, 2^-134 where
     it is subnormal.
-    Squared: the rounding errors of the p's are independent, uniform at most: variance (2^-8)^2 / 3 of each (p v)^2; the
-    result's likewise; the fp32 terms in full."""
+    Squared: the rounding errors of the p's are independent, uniform at most: variance (2^-11)^2 / 3 of each (p v)^2;
+    the result's (2^-8)^2 / 3 of its square, and (2^-134)^2 / 3 where it is subnormal (steps of 2^-133, so off by 2^-134 at
+    most, whatever its size); the fp32 terms and the grain in full."""
     p = 2.0 ** -22 * (D + 8) * reach[..., None] + 2.0 ** -21
     chain = 2.0 ** -23 * (tokens / 32 + 104)
     fp32 = (p + chain) * (size + np.abs(ref))
-    hard = fp32 * 1.01 + 2.0 ** -8 * size * (1 + 2 * p)
+    fp32 = fp32 + 2.0 ** -25 * grain
+    hard = fp32 * 1.01 + 2.0 ** -11 * size * (1 + 2 * p)
     hard = hard + 2.0 ** -8 * (np.abs(ref) + hard) + 2.0 ** -134
-    return hard, 2.0 ** -16 / 3 * (spread ** 2 + ref ** 2) + fp32 ** 2
+    return hard, 2.0 ** -22 / 3 * spread ** 2 + 2.0 ** -16 / 3 * ref ** 2 + 2.0 ** -268 / 3 + fp32 ** 2
 
 
-def check_attention(got, ref, size, spread, reach, D, tokens, what, say=print):
+def check_attention(got, ref, size, spread, grain, reach, D, tokens, what, say=print):
     """Every element within the worst case; and the whole within twice the expected size of the errors (a lost or doubled
     token of n alike moves the result by 1 / sqrt(n) of its size)."""
     assert np.isfinite(got).all(), f"{what}: non-finite output"
-    hard, var = attention_bounds(ref, size, spread, reach, D, tokens)
+    hard, var = attention_bounds(ref, size, spread, grain, reach, D, tokens)
     err = np.abs(got - ref)
     worst = float((err / hard).max()) if err.size else 0.0
     rms = float(np.sqrt((err ** 2).sum() / var.sum())) if var.sum() > 0 else float(err.max() if err.size else 0.0)

@@ -418,3 +418,22 @@ def test_layer_prompt_and_decode_in_graphs():
                     one["out"], one["ws"], one["n"])
     torch.cuda.synchronize()
     assert bool((one["out"] == before).all())
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+def test_value_scales_far_apart(fmt):
+    """Pages whose values are many powers of two apart, pages of zeros (scale 0), keys' scales of 0: weights are rounded relative to
+    the row's largest p * scale, wherever that is."""
+    g = np.random.default_rng(16)
+    for new, lens in (([1, 3], [700, 90]), ([60, 33], [200, 400])):
+        c = kv_case(g, fmt, 2, 64, 16, new, lens, peaky=0.8)
+        live = ~np.isnan(c["v_scales"])
+        for exponents in ((-40, 40), (-3, 3), (-140, -120), (100, 110)):
+            d = dict(c)
+            d["v_scales"] = np.where(live, np.ldexp(c["v_scales"], g.integers(*exponents, c["v_scales"].shape)), np.nan).astype(np.float32)
+            d["k_scales"] = c["k_scales"].copy()
+            zero = live & (g.random(live.shape) < 0.2)
+            d["v_scales"][zero] = 0
+            d["v_pages"] = np.where(zero[:, :, None, None], 0, c["v_pages"]).astype(np.uint8)
+            d["k_scales"][live & (g.random(live.shape) < 0.1)] = 0
+            _check(d, normal_rows(g, c["T"], 6, 64), what=f"{fmt} scales 2^{exponents}")

@@ -139,7 +139,7 @@ def test_attention_oracle_empty_rows_and_left_out():
 
 
 # ---- what the bounds can see ------------------------------------------------------------------
-@pytest.mark.parametrize("tokens", [40, 300])
+@pytest.mark.parametrize("tokens", [40, 1000])
 def test_bounds_see_mistakes(tokens):
     """An exact result rounded once passes both bounds; a lost last token, a token too many, a wrong head and a wrong page scale
     break the expected size."""
@@ -148,8 +148,8 @@ def test_bounds_see_mistakes(tokens):
     q = normal_rows(g, 4, 8, 64)
     run = lambda lens=tokens, **k: oracle.ref_attention("int8", k.get("q", q), c["cu"], [lens], c["table"], c["k_pages"], c["v_pages"],  # noqa: E731
                                                         k.get("ks", c["k_scales"]), k.get("vs", c["v_scales"]), 0.125, k.get("window", 0), np.zeros(q.shape))
-    ref, size, spread, reach = run()
-    hard, var = attention_bounds(ref, size, spread, reach, 64, tokens)
+    ref, size, spread, grain, reach = run()
+    hard, var = attention_bounds(ref, size, spread, grain, reach, 64, tokens)
     rms = lambda got: float(np.sqrt(((got - ref) ** 2).sum() / var.sum()))  # noqa: E731
     rounded = oracle.decode_bf16(oracle.round_to_bf16(ref))
     assert (np.abs(rounded - ref) <= hard).all() and rms(rounded) < 1.0
