@@ -444,25 +444,47 @@ def hq_moe_decode(desc, T, topk, E, H, I, x, topk_ids, topk_weights, w_gate_up, 
 
 
 # ---- around the products: norm, cache, attention ------------------------------------------------
+# These calls take up to a dozen buffers each: a tensor that fits is passed on by the expressions below, a third of
+# what _at and _rows_at cost; whatever else it is (an address, raw bits, a tensor that does not fit) is left to them.
+_Tensor, _bf16, _fp32, _int32 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32
 _E8M0 = (1, (torch.uint8,))
+_CODES8 = (1, (torch.float8_e4m3fn, torch.uint8, torch.int8))
 #: act_fmt -> element type of y, columns of x that one element of y holds, and the same of the scales (0: one a row)
 _NORM_OUT = {
     HQ_ACT_BF16: (_BF16, 1, None, 0),
     HQ_ACT_INT8_PER_TOKEN: ((1, (torch.int8, torch.uint8)), 1, _FP32, 0),
-    HQ_ACT_FP8E4M3_PER_TOKEN: ((1, (torch.float8_e4m3fn, torch.uint8, torch.int8)), 1, _FP32, 0),
-    HQ_ACT_FP8E4M3_BLOCK128: ((1, (torch.float8_e4m3fn, torch.uint8, torch.int8)), 1, _FP32, 128),
-    HQ_ACT_MXFP8: ((1, (torch.float8_e4m3fn, torch.uint8, torch.int8)), 1, _E8M0, 32),
+    HQ_ACT_FP8E4M3_PER_TOKEN: (_CODES8, 1, _FP32, 0),
+    HQ_ACT_FP8E4M3_BLOCK128: (_CODES8, 1, _FP32, 128),
+    HQ_ACT_MXFP8: (_CODES8, 1, _E8M0, 32),
     HQ_ACT_MXFP4: ((1, (torch.uint8, torch.int8)), 2, _E8M0, 32),
 }
+
+
+def _typed_at(x, count, dtype, kind, dev, what):
+    """_at for a kind whose usual tensor type is `dtype`."""
+    if x.__class__ is _Tensor and x.dtype is dtype and x.numel() >= count and x.is_contiguous() and x.get_device() == dev:
+        return x.data_ptr()
+    return _at(x, count, kind, dev, what)
+
+
+def _bytes_at(x, count, dev, what):
+    """_at for buffers of any type."""
+    if x.__class__ is _Tensor and x.numel() >= count and x.is_contiguous() and x.get_device() == dev:
+        return x.data_ptr()
+    return _at(x, count, _BYTES, dev, what)
 
 
 def hq_rms_norm(act_fmt, M, K, x, residual, weight, eps, residual_out, y, y_scale=None, y_bf16=None, stream=None):
     dev, n = _here(), M * K
     kind, per, scale, block = _NORM_OUT.get(act_fmt, (_BYTES, 1, _BYTES, 0))
-    _check(_c["hq_rms_norm"](act_fmt, M, K, _at(x, n, _BF16, dev, "x"), _at(residual, n, _BF16, dev, "residual"), _at(weight, K, _BF16, dev, "weight"),
-                             eps, _at(residual_out, n, _BF16, dev, "residual_out"), _at(y, n // per, kind, dev, "y"),
-                             _at(y_scale, n // block if block else M, scale or _FP32, dev, "y_scale"), _at(y_bf16, n, _BF16, dev, "y_bf16"),
-                             _stream_at(stream, dev)))
+    _check(_c["hq_rms_norm"](
+        act_fmt, M, K, _typed_at(x, n, _bf16, _BF16, dev, "x"),
+        None if residual is None else _typed_at(residual, n, _bf16, _BF16, dev, "residual"),
+        None if weight is None else _typed_at(weight, K, _bf16, _BF16, dev, "weight"), eps,
+        None if residual_out is None else _typed_at(residual_out, n, _bf16, _BF16, dev, "residual_out"),
+        _typed_at(y, n // per, kind[1][0] if kind[1] else None, kind, dev, "y"),
+        None if y_scale is None else _typed_at(y_scale, n // block if block else M, _fp32 if scale is _FP32 else torch.uint8, scale or _FP32, dev, "y_scale"),
+        None if y_bf16 is None else _typed_at(y_bf16, n, _bf16, _BF16, dev, "y_bf16"), _stream_at(stream, dev)))
 
 
 def hq_kv_cache_bytes(desc) -> int:
@@ -472,6 +494,10 @@ def hq_kv_cache_bytes(desc) -> int:
 def _rows_at(x, rows, width, stride, dev, what):
     """Device address of `rows` bf16 rows of `width` elements, `stride` elements apart: a tensor of such rows, or a
     view of some columns of a wider one. What the tensor's own memory has to hold is checked, as _at does."""
+    if x.__class__ is _Tensor and x.dtype is _bf16 and x.get_device() == dev:
+        shape, steps = x.shape, x.stride()
+        if len(shape) == 3 and shape[0] >= rows and steps[0] == stride and steps[2] == 1 and steps[1] == shape[2] and shape[1] * shape[2] >= width:
+            return x.data_ptr()
     if not isinstance(x, torch.Tensor):
         return _at(x, rows * width, _BF16, dev, what)
     inner, dense = 1, True
@@ -489,10 +515,12 @@ def _rows_at(x, rows, width, stride, dev, what):
 
 
 def _cache_at(desc, B, cu, kv_lens, page_table, table_width, k_pages, v_pages, k_scales, v_scales, dev):
-    codes, scales = hq_kv_cache_bytes(desc), desc.num_pages * desc.num_kv_heads
-    return (_at(cu, B + 1, _INT32, dev, "cu"), _at(kv_lens, B, _INT32, dev, "kv_lens"), _at(page_table, B * table_width, _INT32, dev, "page_table"),
-            table_width, _at(k_pages, codes, _BYTES, dev, "k_pages"), _at(v_pages, codes, _BYTES, dev, "v_pages"),
-            _at(k_scales, scales, _FP32, dev, "k_scales"), _at(v_scales, scales, _FP32, dev, "v_scales"))
+    scales = desc.num_pages * desc.num_kv_heads
+    codes = scales * desc.page_size * desc.head_dim      # hq_kv_cache_bytes, which the call checks
+    return (_typed_at(cu, B + 1, _int32, _INT32, dev, "cu"), _typed_at(kv_lens, B, _int32, _INT32, dev, "kv_lens"),
+            _typed_at(page_table, B * table_width, _int32, _INT32, dev, "page_table"), table_width,
+            _bytes_at(k_pages, codes, dev, "k_pages"), _bytes_at(v_pages, codes, dev, "v_pages"),
+            _typed_at(k_scales, scales, _fp32, _FP32, dev, "k_scales"), _typed_at(v_scales, scales, _fp32, _FP32, dev, "v_scales"))
 
 
 def hq_kv_append(desc, B, T, max_new, k, v, kv_stride, cu, kv_lens, page_table, table_width, k_pages, v_pages, k_scales, v_scales, stream=None):
@@ -511,5 +539,5 @@ def hq_attention(desc, B, T, Hq, max_q, max_kv, q, q_stride, cu, kv_lens, page_t
     dev, width = _here(), Hq * desc.head_dim
     _check(_c["hq_attention"](_d(desc), B, T, Hq, max_q, max_kv, _rows_at(q, T, width, q_stride, dev, "q"), q_stride,
                               *_cache_at(desc, B, cu, kv_lens, page_table, table_width, k_pages, v_pages, k_scales, v_scales, dev),
-                              sm_scale, window, _at(out, T * width, _BF16, dev, "out"), _at(ws, ws_bytes, _BYTES, dev, "ws"), ws_bytes,
-                              _stream_at(stream, dev)))
+                              sm_scale, window, _typed_at(out, T * width, _bf16, _BF16, dev, "out"), None if ws is None else _bytes_at(ws, ws_bytes, dev, "ws"),
+                              ws_bytes, _stream_at(stream, dev)))

@@ -23,6 +23,9 @@ namespace hq {
 namespace {
 
 constexpr int kWaves = 4;
+constexpr int kFewRows = 32;     // rows of a head that one workgroup takes here; more go to the tiled kernel
+constexpr int kTileRows = 128;   // rows of a workgroup of the tiled kernel
+constexpr int kMaxSplit = 128;
 
 template <int D, int FMT, int NQ>
 __global__ __launch_bounds__(kWaves * 64) void attention_kernel(KvCall c) {
@@ -31,10 +34,11 @@ __global__ __launch_bounds__(kWaves * 64) void attention_kernel(KvCall c) {
   const int b = blockIdx.y;
   const KvSeq sq = attention_sequence(c, b);
   // heads next to each other, so that with eight of them a head's workgroups run on one XCD and share its L2
-  const int head = int(blockIdx.x % unsigned(c.H)), part = int(blockIdx.x / unsigned(c.H));
+  const int head = int(blockIdx.x % unsigned(c.H)), part = int(blockIdx.x / unsigned(c.H) % unsigned(c.n_split));
+  const int r0 = int(blockIdx.x / unsigned(c.H) / unsigned(c.n_split)) * 16 * NQ;
   const int rows = sq.n * c.G;
-  if (rows == 0) return;
-  const Share sh = share_of(c, sq, 0, 16 * NQ);
+  if (r0 >= rows) return;
+  const Share sh = share_of(c, sq, r0, 16 * NQ);
   if (part >= sh.parts) return;
   // the wave is the same for all its lanes: blocks, addresses and branches that go by it are scalar
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 15, quarter = lane >> 4;
@@ -84,14 +88,14 @@ __global__ __launch_bounds__(kWaves * 64) void attention_kernel(KvCall c) {
   int pos[NQ];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    const int r = 16 * n + col;
+    const int r = r0 + 16 * n + col;
     const int i = r / c.G, g = r - i * c.G;
     pos[n] = r < rows ? before + i : -1;
     const auto* qp = static_cast<const uint16_t*>(c.q) + (int64_t(sq.first) + i) * c.q_stride + int64_t(head * c.G + g) * D + quarter * (D / 4);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) qf[n][s] = r < rows ? query8(qp + 8 * s, c.q_sign) : bf16x8{};
   }
-  const int pos_last = before + (rows - 1) / c.G;
+  const int pos_first = before + r0 / c.G, pos_last = before + (min(r0 + 16 * NQ, rows) - 1) / c.G;
 
   if (blk < end) {
     load_keys(blk);
@@ -117,7 +121,7 @@ __global__ __launch_bounds__(kWaves * 64) void attention_kernel(KvCall c) {
     if (blk + kWaves < end) load_keys(blk + kWaves);
     float f = ks * c.scale_log2;
     const float lv = there ? log2f(vs) : -INFINITY;
-    if (base + kBlock - 1 > before || (c.window > 0 && base <= pos_last - c.window) || __any(!there)) {
+    if (base + kBlock - 1 > pos_first || (c.window > 0 && base <= pos_last - c.window) || __any(!there)) {
       mask_scores<NQ>(score, pos, vg, c.window, there, f);
       f = 1.0f;
       const int live = there ? sq.len - vg : 0;
@@ -161,7 +165,7 @@ __global__ __launch_bounds__(kWaves * 64) void attention_kernel(KvCall c) {
     __syncthreads();
     for (int e = threadIdx.x; e < 16 * (D / 4); e += kWaves * 64) {
       const int row = e / (D / 4), d = (e % (D / 4)) * 4;
-      const int r = 16 * n + row;
+      const int r = r0 + 16 * n + row;
       if (r >= rows) continue;
       float m = tops[0][row];
 #pragma unroll
@@ -191,68 +195,85 @@ __global__ __launch_bounds__(kWaves * 64) void attention_kernel(KvCall c) {
   }
 }
 
-// The parts of a row joined: one wave a (token, query head).
+// The parts of a row joined: one workgroup a (token, query head), its waves taking parts in turn, a lane D / 64 channels.
 template <int D>
-__global__ __launch_bounds__(256) void attention_join_kernel(KvCall c, int tile_rows) {
+__global__ __launch_bounds__(kWaves * 64) void attention_join_kernel(KvCall c, int tile_rows) {
+  constexpr int kEach = (D + 63) / 64;
+  __shared__ float parts[kWaves][kEach * 64];
   const int b = blockIdx.y;
   const KvSeq sq = attention_sequence(c, b);
-  const int head = int(blockIdx.x % unsigned(c.H)), r = int(blockIdx.x / unsigned(c.H)) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int head = int(blockIdx.x % unsigned(c.H)), r = int(blockIdx.x / unsigned(c.H));
   if (r >= sq.n * c.G) return;
   const Share sh = share_of(c, sq, r / tile_rows * tile_rows, tile_rows);
   if (sh.parts == 1) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int i = r / c.G, h = head * c.G + r % c.G;
   const int64_t at = part_row(c, sq, b, i, h);
-  // a lane has part `lane` of the first 64, its maximum and sum
-  float m = -INFINITY;
-  for (int s = lane; s < sh.parts; s += 64) m = fmaxf(m, c.ws_ml[2 * (at + s)]);
+  static_assert(kMaxSplit <= 2 * 64, "a lane holds two parts' maxima");
+  const float2 none = make_float2(-INFINITY, 0.0f);
+  const auto* all = reinterpret_cast<const float2*>(c.ws_ml) + at;
+  const float2 ml0 = lane < sh.parts ? all[lane] : none, ml1 = lane + 64 < sh.parts ? all[lane + 64] : none;
+  float m = fmaxf(ml0.x, ml1.x);
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
   const float ref = m == -INFINITY ? 0.0f : m;
-  constexpr int kEach = (D + 63) / 64;
-  float o[kEach] = {}, total = 0.0f;
-#pragma unroll 4
-  for (int s = 0; s < sh.parts; ++s) {
-    const float2 ml = *reinterpret_cast<const float2*>(c.ws_ml + 2 * (at + s));
-    const float f = exp2_fast(ml.x - ref);
-    total += f * ml.y;
+  const float f0 = exp2_fast(ml0.x - ref), f1 = exp2_fast(ml1.x - ref);
+  float total = f0 * ml0.y + f1 * ml1.y;
 #pragma unroll
-    for (int j = 0; j < kEach; ++j)
-      if (lane + 64 * j < D) o[j] += f * c.ws_o[(at + s) * D + lane + 64 * j];
+  for (int off = 32; off > 0; off >>= 1) total += __shfl_xor(total, off, 64);
+  float o[kEach] = {};
+  constexpr int kAhead = 4;   // parts asked for together
+  for (int s0 = wave; s0 < sh.parts; s0 += kAhead * kWaves) {
+    float x[kAhead][kEach];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const int s = s0 + a * kWaves;
+        x[a][j] = s < sh.parts && (D % 64 == 0 || lane + 64 * j < D) ? c.ws_o[(at + s) * D + lane + 64 * j] : 0.0f;
+      }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int s = s0 + a * kWaves;
+      if (s >= sh.parts) break;
+      const float f = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s < 64 ? f0 : f1), s & 63));
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) o[j] += f * x[a][j];
+    }
   }
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
-  for (int j = 0; j < kEach; ++j)
-    if (lane + 64 * j < D) static_cast<uint16_t*>(c.out)[((int64_t(sq.first) + i) * c.Hq + h) * D + lane + 64 * j] = f32_to_bf16_rne(o[j] * inv);
+  for (int j = 0; j < kEach; ++j) parts[wave][lane + 64 * j] = o[j];
+  __syncthreads();
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  auto* out = static_cast<uint16_t*>(c.out) + ((int64_t(sq.first) + i) * c.Hq + h) * D;
+  for (int d = threadIdx.x; d < D; d += kWaves * 64)
+    out[d] = f32_to_bf16_rne(((parts[0][d] + parts[1][d]) + (parts[2][d] + parts[3][d])) * inv);
 }
 
 template <int D>
 hipError_t join(const KvCall& c, int tile_rows, hipStream_t s) {
   const int64_t rows = int64_t(c.hi_n) * c.G;
   if (c.n_split > 1)
-    hipLaunchKernelGGL((attention_join_kernel<D>), dim3(unsigned((rows + 3) / 4) * unsigned(c.H), unsigned(c.B)), dim3(256), 0, s, c, tile_rows);
+    hipLaunchKernelGGL((attention_join_kernel<D>), dim3(unsigned(rows) * unsigned(c.H), unsigned(c.B)), dim3(kWaves * 64), 0, s, c, tile_rows);
   return hipGetLastError();
 }
 
 template <int D, int FMT>
-hipError_t go(const KvCall& c, hipStream_t s) {
-  const dim3 grid(unsigned(c.n_split) * unsigned(c.H), unsigned(c.B));
-  const bool two = c.hi_n * c.G > 16;
-  if (two) hipLaunchKernelGGL((attention_kernel<D, FMT, 2>), grid, dim3(kWaves * 64), 0, s, c);
+hipError_t go(const KvCall& c, bool wide, hipStream_t s) {
+  const int rows = wide ? 32 : 16;
+  const dim3 grid(unsigned((c.hi_n * c.G + rows - 1) / rows) * unsigned(c.n_split) * unsigned(c.H), unsigned(c.B));
+  if (wide) hipLaunchKernelGGL((attention_kernel<D, FMT, 2>), grid, dim3(kWaves * 64), 0, s, c);
   else hipLaunchKernelGGL((attention_kernel<D, FMT, 1>), grid, dim3(kWaves * 64), 0, s, c);
   const hipError_t e = hipGetLastError();
-  return e == hipSuccess ? join<D>(c, 32, s) : e;
+  return e == hipSuccess ? join<D>(c, rows, s) : e;
 }
 
 template <int D>
-hipError_t pick(const KvCall& c, hipStream_t s) {
-  return c.fmt == HQ_KV_INT8 ? go<D, HQ_KV_INT8>(c, s) : go<D, HQ_KV_FP8_E4M3>(c, s);
+hipError_t pick(const KvCall& c, bool wide, hipStream_t s) {
+  return c.fmt == HQ_KV_INT8 ? go<D, HQ_KV_INT8>(c, wide, s) : go<D, HQ_KV_FP8_E4M3>(c, wide, s);
 }
 
 }  // namespace
-
-constexpr int kFewRows = 32;    // rows of a head that one workgroup takes here; more go to the tiled kernel
-constexpr int kTileRows = 128;   // rows of a workgroup of the tiled kernel
-constexpr int kMaxSplit = 128;
 
 int64_t attention_groups(const KvCall& c) {
   const int64_t tiles = (int64_t(c.max_new) * c.G + kTileRows - 1) / kTileRows;
@@ -260,10 +281,12 @@ int64_t attention_groups(const KvCall& c) {
 }
 
 namespace {
-// Parts of the positions: enough workgroups for the card, each with at least `least` blocks.
+// Parts of the positions: no more workgroups than run at once, each with at least `least` blocks. With more, the last ones
+// run alone: one token on 131072 positions with 512 / 768 / 1024 / 2048 workgroups 56.7 / 60.8 / 65.1 / 65.1 us; 16 tokens on
+// 30000 72.9 / 82.2 / 87.3 / 81.9; D = 256, 4 tokens on 20000 with 256 / 512 / 1024: 33.6 / 42.5 / 48.1.
 void split_of(int64_t groups, int64_t wanted, int64_t least, int64_t max_kv, int* n_split, int* each) {
   const int64_t blocks = std::max<int64_t>((max_kv + kBlock - 1) / kBlock, 1);
-  int64_t n = std::max<int64_t>((wanted + groups - 1) / groups, 1);
+  int64_t n = std::max<int64_t>(wanted / groups, 1);
   n = std::min<int64_t>(std::min(n, (blocks + least - 1) / least), kMaxSplit);
   *each = int((blocks + n - 1) / n);
   *n_split = int(n);
@@ -273,6 +296,8 @@ void split_of(int64_t groups, int64_t wanted, int64_t least, int64_t max_kv, int
 AttentionPlan plan_attention(const KvCall& c, int64_t max_kv) {
   AttentionPlan p{};
   const int64_t most = int64_t(c.max_new) * c.G;
+  // what a workgroup's rows see, at most; a window may begin and end inside a block
+  if (c.window > 0) max_kv = std::min(max_kv, int64_t(c.window) + std::min<int64_t>(c.max_new, kTileRows) + kBlock);
   // sequences with few rows among others with many have their own launch
   p.few = most <= kFewRows ? c.max_new : c.B > 1 ? kFewRows / c.G : 0;
   p.many = c.max_new > p.few;
@@ -284,7 +309,15 @@ AttentionPlan plan_attention(const KvCall& c, int64_t max_kv) {
     at = *ml + (size_t(slots) * c.Hq * n_split * 8 + 15) / 16 * 16;
   };
   if (p.few) {
-    split_of(int64_t(c.B) * c.H, 2048, 2 * kWaves, max_kv, &p.few_split, &p.few_each);
+    // two workgroups a CU, one where its registers leave room for no more (D = 256). With more, the last ones run alone: one
+    // token on 131072 positions with 512 / 768 / 1024 / 2048 workgroups 56.7 / 60.8 / 65.1 / 65.1 us; 16 tokens on 30000
+    // 72.9 / 82.2 / 87.3 / 81.9; D = 256, 4 tokens on 20000 with 256 / 512 / 1024: 33.6 / 42.5 / 48.1.
+    const int resident = c.D > 192 ? 256 : 512;      // two workgroups a CU, one where its registers leave room for no more
+    split_of(int64_t(c.B) * c.H, resident, kWaves, max_kv, &p.few_split, &p.few_each);
+    // More than 16 rows: in two workgroups, which both read the keys and values, while the card is not full of them (32 rows, us in
+    // one / in two: D = 128, 1 sequence of 2000 11.8 / 10.2, 2 of 8000 16.7 / 15.6, 16 of 2000 25.8 / 28.0; D = 256, 4 of 3000
+    // 19.2 / 14.8, 8 of 3000 23.1 / 27.9).
+    p.few_wide = p.few * c.G > 16 && int64_t(c.B) * c.H * p.few_split >= resident;
     p.few_by_token = c.T <= int64_t(c.B) * p.few;
     room(p.few_by_token ? c.T : int64_t(c.B) * p.few, p.few_split, &p.few_o, &p.few_ml);
   }
@@ -310,11 +343,11 @@ hipError_t launch_attention(const KvCall& call, const AttentionPlan& p, uint8_t*
     c.ws_ml = reinterpret_cast<float*>(ws + p.few_ml);
     hipError_t e;
     switch (c.D) {
-      case 64: e = pick<64>(c, s); break;
-      case 96: e = pick<96>(c, s); break;
-      case 128: e = pick<128>(c, s); break;
-      case 192: e = pick<192>(c, s); break;
-      default: e = pick<256>(c, s);
+      case 64: e = pick<64>(c, p.few_wide, s); break;
+      case 96: e = pick<96>(c, p.few_wide, s); break;
+      case 128: e = pick<128>(c, p.few_wide, s); break;
+      case 192: e = pick<192>(c, p.few_wide, s); break;
+      default: e = pick<256>(c, p.few_wide, s);
     }
     if (e != hipSuccess) return e;
   }

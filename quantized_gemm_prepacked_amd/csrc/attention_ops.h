@@ -66,11 +66,15 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 // Running softmax of the rows a lane holds. With x = sm_scale * log2(e) * q . k and s_v the scale of the position's values:
-//   top = max x,  sum = sum 2^(x - top)  (this lane's positions),
-//   ref = max (x + log2 s_v),  acc = sum 2^(x + log2 s_v - ref) * code.
-// The weights 2^(x + log2 s_v - ref) enter the product with the codes as fp16: the largest of a row is 1, each is off by 2^-11
-// of itself or 2^-25 of the largest, whatever the scales (a bf16 weight, off by 2^-8, made the result's error half as
-// large again as the rounding of the result itself). Statistics and sums are fp32.
+//   sum = sum 2^(x - top)  (this lane's positions),   acc = sum 2^(x + log2 s_v - ref) * code,
+// with references top and ref within kSlack of the maxima of x and of x + log2 s_v seen so far: the maxima are taken over
+// a row's four lanes, and what was summed before is brought to new references, only in blocks where one moves by more than
+// that (the first and a few others), at the price of weights up to 2^kSlack.
+// The weights 2^(x + log2 s_v - ref) enter the product with the codes as fp16: each is off by 2^-11 of itself or 2^-25 of the
+// row's largest, whatever the scales (a bf16 weight, off by 2^-8, made the result's error half as large again as the
+// rounding of the result itself). Statistics and sums are fp32.
+constexpr float kSlack = 8.0f;
+
 template <int NQ, int TILES>
 struct Rows {
   f32x4 acc[NQ][TILES];
@@ -95,36 +99,51 @@ struct Rows {
 #pragma unroll
       for (int e = 1; e < 16; ++e) m = fmaxf(m, score[n][e >> 2][e & 3]);
       m *= ks;
-      const float top1 = fmaxf(top[n], row_max(m)), ref1 = fmaxf(ref[n], row_max(m + lv));
-      // rows that have seen nothing yet have maxima of -infinity
-      const float at = top1 == -INFINITY ? 0.0f : top1, wat = ref1 == -INFINITY ? 0.0f : ref1;
-      const float shrink = exp2_fast(top[n] - at), wshrink = exp2_fast(ref[n] - wat);
-      if (__any(top1 > top[n] || ref1 > ref[n])) {
-        sum[n] *= shrink;
+      if (__any(m > top[n] + kSlack || m + lv > ref[n] + kSlack)) {
+        // (a row goes by its own maxima: what the tile's other rows hold does not change its bits)
+        const float rm = row_max(m), rw = row_max(m + lv);
+        const bool moves = rm > top[n] + kSlack || rw > ref[n] + kSlack;
+        const float top1 = moves ? fmaxf(top[n], rm) : top[n], ref1 = moves ? fmaxf(ref[n], rw) : ref[n];
+        // where a row had seen nothing, sum and acc are 0
+        const float shrink = top[n] == -INFINITY ? 1.0f : exp2_fast(top[n] - top1), wshrink = ref[n] == -INFINITY ? 1.0f : exp2_fast(ref[n] - ref1);
+        if (__any(shrink != 1.0f || wshrink != 1.0f)) {
+          sum[n] *= shrink;
 #pragma unroll
-        for (int t = 0; t < TILES; ++t)
+          for (int t = 0; t < TILES; ++t)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[n][t][r] *= wshrink;
+            for (int r = 0; r < 4; ++r) acc[n][t][r] *= wshrink;
+        }
+        top[n] = top1;
+        ref[n] = ref1;
       }
-      top[n] = top1;
-      ref[n] = ref1;
-      const float f = exp2_fast(lv + (at - wat));
+      // rows that have seen nothing yet have references of -infinity
+      const float at = top[n] == -INFINITY ? 0.0f : top[n], wat = ref[n] == -INFINITY ? 0.0f : ref[n];
+      const float e = lv + (at - wat);      // log2 of weight / 2^(x - top)
+      // Scales so far apart (or 0) that a weight vanishes where its part of the sum does not: the two apart, else one from the other.
+      const bool far = !(e > -60.0f);
+      const float start = far ? -at : lv - wat;
       float p[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) p[e] = exp2_fast(fmaf(score[n][e >> 2][e & 3], ks, -at));
+      for (int k = 0; k < 16; ++k) p[k] = exp2_fast(fmaf(score[n][k >> 2][k & 3], ks, start));
+      const float s = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7])) + (((p[8] + p[9]) + (p[10] + p[11])) + ((p[12] + p[13]) + (p[14] + p[15])));
+      sum[n] = fmaf(s, far ? 1.0f : exp2_fast(-e), sum[n]);
+      if (__any(far)) {
+        const float f = far ? exp2_fast(e) : 1.0f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) p[k] *= f;
+      }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         f16x8 w;
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-          const f32x2 two = {p[8 * u + j] * f, p[8 * u + j + 1] * f};
+          const f32x2 two = {p[8 * u + j], p[8 * u + j + 1]};
           const f16x2 h = __builtin_convertvector(two, f16x2);
           w[j] = h[0];
           w[j + 1] = h[1];
         }
         weight[n][u] = w;
       }
-      sum[n] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7])) + (((p[8] + p[9]) + (p[10] + p[11])) + ((p[12] + p[13]) + (p[14] + p[15])));
     }
   }
 

@@ -7,7 +7,9 @@
 // once by the whole workgroup (keys to bf16, values to fp16), and handed to the waves through two LDS buffers in turn, so
 // that there is one barrier a block. Products, lane layout and softmax are those of the few-row kernel.
 //
-// LDS rows are 16 bytes longer than their values: the sixteen rows that one read touches start in different banks.
+// Bank conflicts: gfx950 serves a 16-byte LDS read of a wave 16 lanes at a time, eight of one lane group and the other
+// eight of the next (lanes 0-3, 12-15 and 20-27; 4-11, 16-19 and 28-31; and so the upper half). Rows are stored with
+// their 16-byte chunks exchanged by a key that sends these sixteen to sixteen different bank groups.
 #include <hip/hip_runtime.h>
 
 #include "attention_ops.h"
@@ -27,13 +29,27 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// Byte of chunk s of lane group q (a quarter of the channels, D / 32 chunks) of key row `row`. The chunks of a row: keys of the
+// row's eight lanes of one group and of the other eight are two sets that the difference between the groups' chunks maps to
+// themselves. Head sizes that are no power of two: a plane for each group, of rows an odd number of chunks long.
+template <int D>
+__device__ __forceinline__ int key_at(int row, int q, int s) {
+  const int c = q * (D / 32) + s;
+  if constexpr (D == 64) return row * 128 + ((c ^ (((row >> 1) + 2) & 7)) << 4);
+  else if constexpr (D == 128) return row * 256 + ((c ^ ((row + 4) & 15)) << 4);
+  else if constexpr (D == 256) return row * 512 + ((c ^ ((row & 15) ^ ((row & 8) >> 1))) << 4);
+  else return ((q * kBlock + row) * (D / 32 | 1) + s) << 4;
+}
+// Byte of half u of the 16 positions of lane group q of channel d.
+__device__ __forceinline__ int value_at(int d, int q, int u) { return d * 128 + (((2 * q + u) ^ (((d >> 1) + 2) & 7)) << 4); }
+
 template <int D, int FMT>
 __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_tile_kernel(KvCall c) {
   constexpr int kSteps = D / 32, kTiles = D / 16;
-  constexpr int kKeyRow = 2 * D + 16, kValueRow = 2 * kBlock + 16;      // bytes of an LDS row
-  constexpr int kKeys = kBlock * kKeyRow, kBuffer = kKeys + D * kValueRow;
+  constexpr int kKeys = (D & (D - 1)) == 0 ? kBlock * D * 2 : 4 * kBlock * (D / 32 | 1) * 16;
+  constexpr int kBuffer = kKeys + D * kBlock * 2;
   constexpr int kPieces = (D * 4 + kWaves * 64 - 1) / (kWaves * 64);    // 16-byte pieces of values a thread stages
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][kBuffer];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kBuffer];
   const int b = blockIdx.y;
   const KvSeq sq = attention_sequence(c, b);
   const int head = int(blockIdx.x % unsigned(c.H)), part = int(blockIdx.x / unsigned(c.H) % unsigned(c.n_split));
@@ -49,51 +65,64 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_tile_
   const int end = min(sh.first + (part + 1) * sh.each, sh.end);
   const int32_t* table = c.table + int64_t(b) * c.width;
 
-  // Staging: a thread takes a quarter of one key's channels, and 16-byte pieces of values (channel, 16 positions).
+  // Staging: a thread takes a quarter of one key's channels (the 16 keys of a wave are of one page), and 16-byte pieces of
+  // values (channel, 16 positions). Pages are asked for two blocks ahead, codes and scales one.
   const int key = tid >> 2, piece = tid & 3;
   const int key_row = 16 * ((key >> 2) & 3) + 4 * (key >> 4) + (key & 3);
+  int spage, vpage;        // of this lane's positions, and of its piece of values
   uint2 kc[kSteps];
   u32x4 vc[kPieces];
   int live;                // positions of this thread's values that exist
   float ks, vs;            // scales of this lane's positions
   bool there;
+  const auto load_pages = [&](int blk) {
+    const int sg = blk * kBlock + 16 * quarter, vg = blk * kBlock + 16 * piece;
+    const int most = sq.len - 1;
+    spage = table[min(sg, most) >> shift];      // (of the last page where there is none: not used)
+    vpage = table[min(vg, most) >> shift];
+  };
+  const uint8_t* const kp = static_cast<const uint8_t*>(c.k_pages) + ((int64_t(head) << shift) + (key & 15)) * D + piece * (D / 4);
+  const uint8_t* const vp = static_cast<const uint8_t*>(c.v_pages) + ((int64_t(head) * D + (tid >> 2)) << shift);
   const auto load = [&](int blk) {
     const int base = blk * kBlock;
-    const int kg = base + key, vg = base + 16 * piece, sg = base + 16 * quarter;
-    int kpage = kg < sq.len ? table[kg >> shift] : -1, vpage = vg < sq.len ? table[vg >> shift] : -1, spage = sg < sq.len ? table[sg >> shift] : -1;
-    if (kpage < 0 || kpage >= c.num_pages) kpage = 0;
-    live = vpage >= 0 && vpage < c.num_pages ? sq.len - vg : 0;
-    if (live == 0) vpage = 0;
-    there = spage >= 0 && spage < c.num_pages;
-    if (!there) spage = 0;
-    const uint8_t* kp = static_cast<const uint8_t*>(c.k_pages) + ((int64_t(kpage) * c.H + head) * P + (kg & (P - 1))) * D + piece * (D / 4);
-    const uint8_t* vp = static_cast<const uint8_t*>(c.v_pages) + (int64_t(vpage) * c.H + head) * D * P + (vg & (P - 1));
+    const int kg = base + 16 * wave, vg = base + 16 * piece, sg = base + 16 * quarter;
+    there = sg < sq.len && spage >= 0 && spage < c.num_pages;
+    const bool vthere = vg < sq.len && vpage >= 0 && vpage < c.num_pages;
+    live = vthere ? sq.len - vg : 0;
+    const uint32_t page = there ? spage : 0, from = vthere ? vpage : 0;
+    const uint32_t kpage = __builtin_amdgcn_readlane(page, 16 * wave);
+    const uint8_t* k = kp + uint64_t(kpage) * c.page_bytes + (kg & (P - 1)) * D;
+    const uint8_t* v = vp + uint64_t(from) * c.page_bytes + (vg & (P - 1));
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) kc[s] = *reinterpret_cast<const uint2*>(kp + 8 * s);
+    for (int s = 0; s < kSteps; ++s) kc[s] = *reinterpret_cast<const uint2*>(k + 8 * s);
 #pragma unroll
-    for (int e = 0; e < kPieces; ++e) {
-      const int d = (tid + e * kWaves * 64) >> 2;
-      if (D % 64 == 0 || d < D) vc[e] = ldg16(vp + int64_t(d) * P);
-    }
-    ks = c.k_scales[int64_t(spage) * c.H + head];
-    vs = c.v_scales[int64_t(spage) * c.H + head];
+    for (int e = 0; e < kPieces; ++e)
+      if (D % 64 == 0 || (tid >> 2) + 64 * e < D) vc[e] = ldg16(v + (int64_t(64 * e) << shift));
+    const uint64_t at = uint64_t(page) * unsigned(c.H) + unsigned(head);
+    ks = c.k_scales[at];
+    vs = c.v_scales[at];
   };
   const auto store = [&](uint8_t* to) {
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-      *reinterpret_cast<bf16x8*>(to + key_row * kKeyRow + piece * (D / 2) + 16 * s) = codes_bf16<FMT>(kc[s].x, kc[s].y);
+    for (int s = 0; s < kSteps; ++s) *reinterpret_cast<bf16x8*>(to + key_at<D>(key_row, piece, s)) = codes_bf16<FMT>(kc[s].x, kc[s].y);
+    if (__any(live < 16)) {
+#pragma unroll
+      for (int e = 0; e < kPieces; ++e) vc[e] = live_codes(vc[e], live);
+    }
 #pragma unroll
     for (int e = 0; e < kPieces; ++e) {
-      const int d = (tid + e * kWaves * 64) >> 2;
+      const int d = (tid >> 2) + 64 * e;
       if (D % 64 != 0 && d >= D) break;
-      const u32x4 v = live >= 16 ? vc[e] : live_codes(vc[e], live);
-      f16x8* at = reinterpret_cast<f16x8*>(to + kKeys + d * kValueRow + piece * 32);
-      at[0] = codes_f16<FMT>(v[0], v[1]);
-      at[1] = codes_f16<FMT>(v[2], v[3]);
+      *reinterpret_cast<f16x8*>(to + kKeys + value_at(d, piece, 0)) = codes_f16<FMT>(vc[e][0], vc[e][1]);
+      *reinterpret_cast<f16x8*>(to + kKeys + value_at(d, piece, 1)) = codes_f16<FMT>(vc[e][2], vc[e][3]);
     }
   };
   int blk = sh.first + part * sh.each;
-  if (blk < end) load(blk);
+  if (blk < end) {
+    load_pages(blk);
+    load(blk);
+    load_pages(blk + 1);
+  }
 
   bf16x8 qf[kNQ][kSteps];
   int pos[kNQ];
@@ -113,12 +142,15 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_tile_
   Rows<kNQ, kTiles> st;
   st.clear();
   for (int buffer = 0; blk < end; ++blk, buffer ^= 1) {
-    uint8_t* at = lds[buffer];
+    uint8_t* at = lds + buffer * kBuffer;
     store(at);
     float f = ks * c.scale_log2;
     const float lv = there ? log2f(vs) : -INFINITY;
     const bool here = there;
-    if (blk + 1 < end) load(blk + 1);
+    if (blk + 1 < end) {
+      load(blk + 1);
+      load_pages(blk + 2);
+    }
     lds_barrier();
     const int base = blk * kBlock, vg = base + 16 * quarter;
     // blocks that none of the wave's rows sees
@@ -130,7 +162,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_tile_
       for (int n = 0; n < kNQ; ++n) score[n][i] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const bf16x8 kf = *reinterpret_cast<const bf16x8*>(at + (16 * i + col) * kKeyRow + quarter * (D / 2) + 16 * s);
+        const bf16x8 kf = *reinterpret_cast<const bf16x8*>(at + key_at<D>(16 * i + col, quarter, s));
 #pragma unroll
         for (int n = 0; n < kNQ; ++n) score[n][i] = mfma_bf16(kf, qf[n][s], score[n][i]);
       }
@@ -145,7 +177,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_tile_
     for (int t = 0; t < kTiles; ++t)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const f16x8 vf = *reinterpret_cast<const f16x8*>(at + kKeys + (16 * t + col) * kValueRow + quarter * 32 + 16 * u);
+        const f16x8 vf = *reinterpret_cast<const f16x8*>(at + kKeys + value_at(16 * t + col, quarter, u));
 #pragma unroll
         for (int n = 0; n < kNQ; ++n) st.acc[n][t] = mfma_f16(vf, weight[n][u], st.acc[n][t]);
       }

@@ -748,6 +748,7 @@ hq_status check_kv(const hq_kv_desc* d, hq::KvCall* c) {
   c->D = d->head_dim;
   c->page_shift = shift;
   c->num_pages = d->num_pages;
+  c->page_bytes = uint32_t(d->num_kv_heads) * uint32_t(d->head_dim) << shift;      // at most 2^26
   return HQ_OK;
 }
 
@@ -851,13 +852,13 @@ hq_status hq_attention(const hq_kv_desc* desc, int32_t B, int64_t T, int32_t Hq,
   if (!q || !out) return fail(HQ_ERR_INVALID_ARGUMENT, "q and out must be non-NULL");
   if (!aligned16(q) || !aligned16(out) || !aligned16(ws)) return fail(HQ_ERR_INVALID_ARGUMENT, "q, out and ws must be 16-byte aligned");
   if (out == q && q_stride != int64_t(Hq) * c.D) return fail(HQ_ERR_INVALID_ARGUMENT, "out may be q only where q_stride is Hq * head_dim");
+  c.window = window;   // with one the plan never has more parts than without, which is what the workspace is sized for
   const hq::AttentionPlan p = hq::plan_attention(c, max_kv);
   if (ws_bytes < p.ws_bytes || (p.ws_bytes && !ws)) return fail(HQ_ERR_WORKSPACE, "workspace %zu < required %zu", ws ? ws_bytes : size_t(0), p.ws_bytes);
   c.q = q;
   c.q_stride = q_stride;
   c.scale_log2 = float(std::fabs(double(sm_scale)) * 1.4426950408889634);
   c.q_sign = sm_scale < 0.0f ? 0x80008000u : 0u;
-  c.window = window;
   c.out = out;
   return check_hip(hq::launch_attention(c, p, static_cast<uint8_t*>(ws), static_cast<hipStream_t>(stream)), "hq_attention launch");
 }

@@ -156,6 +156,7 @@ struct KvCall {
   const int32_t* kv_lens;
   const int32_t* table;
   int width, capacity;                    // pages and positions of a sequence, at most
+  uint32_t page_bytes;                    // codes of a page, all heads
   void* k_pages;
   void* v_pages;
   float* k_scales;
@@ -180,7 +181,7 @@ int64_t attention_groups(const KvCall& c);   // workgroups without a split of th
 // Sequences of up to `few` new tokens have a launch of their own, those with more (many) another.
 struct AttentionPlan {
   int few;
-  bool many, few_by_token;
+  bool many, few_by_token, few_wide;      // few_wide: 32 rows a workgroup, not 16
   int few_split, few_each, many_split, many_each;
   size_t few_o, few_ml, many_o, many_ml, ws_bytes;
 };
