@@ -24,7 +24,6 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kFewRows = 32;     // rows of a head that one workgroup takes here; more go to the tiled kernel
-constexpr int kTileRows = 128;   // rows of a workgroup of the tiled kernel
 constexpr int kMaxSplit = 128;
 
 template <int D, int FMT, int NQ>
@@ -170,12 +169,11 @@ __global__ __launch_bounds__(kWaves * 64) void attention_kernel(KvCall c) {
       float m = tops[0][row];
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) m = fmaxf(m, tops[w][row]);
-      const float at = m == -INFINITY ? 0.0f : m;
       float total = 0.0f;
       f32x4 o = {0, 0, 0, 0};
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        const float f = exp2_fast(tops[w][row] - at);
+        const float f = exp2_fast(tops[w][row] - m);
         total += f * sums[w][row];
         const f32x4 x = *reinterpret_cast<const f32x4*>(&parts[w][row][d]);
 #pragma unroll
@@ -187,9 +185,9 @@ __global__ __launch_bounds__(kWaves * 64) void attention_kernel(KvCall c) {
         const uint2 w = {f32x2_to_bf16x2_rne(o[0] * inv, o[1] * inv), f32x2_to_bf16x2_rne(o[2] * inv, o[3] * inv)};
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(c.out) + ((int64_t(sq.first) + i) * c.Hq + h) * D + d) = w;
       } else {
-        const int64_t at2 = part_row(c, sq, b, i, h) + part;
-        *reinterpret_cast<f32x4*>(c.ws_o + at2 * D + d) = o;
-        if (d == 0) *reinterpret_cast<float2*>(c.ws_ml + 2 * at2) = make_float2(m, total);
+        const int64_t at = part_row(c, sq, b, i, h) + part;
+        *reinterpret_cast<f32x4*>(c.ws_o + at * D + d) = o;
+        if (d == 0) *reinterpret_cast<float2*>(c.ws_ml + 2 * at) = make_float2(m, total);
       }
     }
   }
@@ -216,8 +214,7 @@ __global__ __launch_bounds__(kWaves * 64) void attention_join_kernel(KvCall c, i
   float m = fmaxf(ml0.x, ml1.x);
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-  const float ref = m == -INFINITY ? 0.0f : m;
-  const float f0 = exp2_fast(ml0.x - ref), f1 = exp2_fast(ml1.x - ref);
+  const float f0 = exp2_fast(ml0.x - m), f1 = exp2_fast(ml1.x - m);
   float total = f0 * ml0.y + f1 * ml1.y;
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) total += __shfl_xor(total, off, 64);
@@ -276,8 +273,8 @@ hipError_t pick(const KvCall& c, bool wide, hipStream_t s) {
 }  // namespace
 
 int64_t attention_groups(const KvCall& c) {
-  const int64_t tiles = (int64_t(c.max_new) * c.G + kTileRows - 1) / kTileRows;
-  return tiles * c.H * c.B;
+  const int tile = attention_tile_rows(c);
+  return (int64_t(c.max_new) * c.G + tile - 1) / tile * c.H * c.B;
 }
 
 namespace {
@@ -297,7 +294,7 @@ AttentionPlan plan_attention(const KvCall& c, int64_t max_kv) {
   AttentionPlan p{};
   const int64_t most = int64_t(c.max_new) * c.G;
   // what a workgroup's rows see, at most; a window may begin and end inside a block
-  if (c.window > 0) max_kv = std::min(max_kv, int64_t(c.window) + std::min<int64_t>(c.max_new, kTileRows) + kBlock);
+  if (c.window > 0) max_kv = std::min(max_kv, int64_t(c.window) + std::min<int64_t>(c.max_new, 256) + kBlock);
   // sequences with few rows among others with many have their own launch
   p.few = most <= kFewRows ? c.max_new : c.B > 1 ? kFewRows / c.G : 0;
   p.many = c.max_new > p.few;
@@ -323,8 +320,9 @@ AttentionPlan plan_attention(const KvCall& c, int64_t max_kv) {
   }
   if (p.many) {
     // tiles there can be: of T rows, with one broken tile a sequence
-    const int64_t tiles = std::min(attention_groups(c), (c.T * c.G / kTileRows + c.B) * c.H);
-    split_of(tiles, 512, 8, max_kv, &p.many_split, &p.many_each);
+    const int tile = attention_tile_rows(c);
+    const int64_t tiles = std::min(attention_groups(c), (c.T * c.G / tile + c.B) * c.H);
+    split_of(tiles, tile == 256 || c.D > 128 ? 256 : 512, 8, max_kv, &p.many_split, &p.many_each);
     room(c.T, p.many_split, &p.many_o, &p.many_ml);
   }
   p.ws_bytes = at;
@@ -363,11 +361,11 @@ hipError_t launch_attention(const KvCall& call, const AttentionPlan& p, uint8_t*
     const hipError_t e = launch_attention_tiles(c, s);
     if (e != hipSuccess) return e;
     switch (c.D) {
-      case 64: return join<64>(c, kTileRows, s);
-      case 96: return join<96>(c, kTileRows, s);
-      case 128: return join<128>(c, kTileRows, s);
-      case 192: return join<192>(c, kTileRows, s);
-      default: return join<256>(c, kTileRows, s);
+      case 64: return join<64>(c, attention_tile_rows(c), s);
+      case 96: return join<96>(c, attention_tile_rows(c), s);
+      case 128: return join<128>(c, attention_tile_rows(c), s);
+      case 192: return join<192>(c, attention_tile_rows(c), s);
+      default: return join<256>(c, attention_tile_rows(c), s);
     }
   }
   return hipSuccess;

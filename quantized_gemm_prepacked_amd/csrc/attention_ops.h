@@ -74,6 +74,8 @@ __device__ __forceinline__ float row_sum(float v) {
 // row's largest, whatever the scales (a bf16 weight, off by 2^-8, made the result's error half as large again as the
 // rounding of the result itself). Statistics and sums are fp32.
 constexpr float kSlack = 8.0f;
+constexpr float kFar = -60.0f;
+constexpr float kNone = -3e38f;     // reference of a row that has seen nothing: its scores are -infinity, its sums 0
 
 template <int NQ, int TILES>
 struct Rows {
@@ -83,72 +85,87 @@ struct Rows {
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      top[n] = ref[n] = -INFINITY;
+      top[n] = ref[n] = kNone;
       sum[n] = 0.0f;
 #pragma unroll
       for (int t = 0; t < TILES; ++t) acc[n][t] = f32x4{0, 0, 0, 0};
     }
   }
 
-  // A block's scores (products of q and k codes; ks >= 0 makes them x; -infinity where masked, then ks = 1) become weights.
-  // lv = log2 of the values' scale, -infinity where that is 0 or there is no page.
+  // A block's scores to weights. Scores are products of q and k codes, ks >= 0 makes them x (where masked they are -infinity or
+  // x already, and ks is 1); lv = log2 of the values' scale, -infinity where that is 0 or there is no page.
   __device__ __forceinline__ void step(const f32x4 (&score)[NQ][4], float ks, float lv, f16x8 (&weight)[NQ][2]) {
+    float m[NQ], start[NQ], e[NQ];
+    bool rare = false;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      float m = score[n][0][0];
+      m[n] = score[n][0][0];
 #pragma unroll
-      for (int e = 1; e < 16; ++e) m = fmaxf(m, score[n][e >> 2][e & 3]);
-      m *= ks;
-      if (__any(m > top[n] + kSlack || m + lv > ref[n] + kSlack)) {
-        // (a row goes by its own maxima: what the tile's other rows hold does not change its bits)
-        const float rm = row_max(m), rw = row_max(m + lv);
+      for (int k = 1; k < 16; ++k) m[n] = fmaxf(m[n], score[n][k >> 2][k & 3]);
+      m[n] *= ks;
+      start[n] = lv - ref[n];
+      e[n] = lv + (top[n] - ref[n]);      // log2 of weight / 2^(x - top)
+      rare |= !(m[n] <= top[n] + kSlack && m[n] + start[n] <= kSlack && e[n] > kFar);
+    }
+    const bool any_rare = __any(rare);
+    if (any_rare) {
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        // new references; a row goes by its own maxima: what the tile's other rows hold does not change its bits
+        const float rm = row_max(m[n]), rw = row_max(m[n] + lv);
         const bool moves = rm > top[n] + kSlack || rw > ref[n] + kSlack;
         const float top1 = moves ? fmaxf(top[n], rm) : top[n], ref1 = moves ? fmaxf(ref[n], rw) : ref[n];
-        // where a row had seen nothing, sum and acc are 0
-        const float shrink = top[n] == -INFINITY ? 1.0f : exp2_fast(top[n] - top1), wshrink = ref[n] == -INFINITY ? 1.0f : exp2_fast(ref[n] - ref1);
-        if (__any(shrink != 1.0f || wshrink != 1.0f)) {
-          sum[n] *= shrink;
+        if (__any(moves && top[n] > kNone)) {      // (where a row had seen nothing, sum and acc are 0)
+          sum[n] *= exp2_fast(top[n] - top1);
+          const float shrink = exp2_fast(ref[n] - ref1);
 #pragma unroll
           for (int t = 0; t < TILES; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[n][t][r] *= wshrink;
+            for (int r = 0; r < 4; ++r) acc[n][t][r] *= shrink;
         }
         top[n] = top1;
         ref[n] = ref1;
-      }
-      // rows that have seen nothing yet have references of -infinity
-      const float at = top[n] == -INFINITY ? 0.0f : top[n], wat = ref[n] == -INFINITY ? 0.0f : ref[n];
-      const float e = lv + (at - wat);      // log2 of weight / 2^(x - top)
-      // Scales so far apart (or 0) that a weight vanishes where its part of the sum does not: the two apart, else one from the other.
-      const bool far = !(e > -60.0f);
-      const float start = far ? -at : lv - wat;
-      float p[16];
+        start[n] = lv - ref1;
+        e[n] = lv + (top1 - ref1);
+        // Scales so far apart (or 0) that a weight vanishes where its part of the sum does not: that part by itself.
+        if (__any(!(e[n] > kFar))) {
+          float s = 0.0f;
+          const float at = top1 > kNone ? top1 : 0.0f;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) p[k] = exp2_fast(fmaf(score[n][k >> 2][k & 3], ks, start));
-      const float s = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7])) + (((p[8] + p[9]) + (p[10] + p[11])) + ((p[12] + p[13]) + (p[14] + p[15])));
-      sum[n] = fmaf(s, far ? 1.0f : exp2_fast(-e), sum[n]);
-      if (__any(far)) {
-        const float f = far ? exp2_fast(e) : 1.0f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) p[k] *= f;
+          for (int k = 0; k < 16; ++k) s += exp2_fast(fmaf(score[n][k >> 2][k & 3], ks, -at));
+          sum[n] += e[n] > kFar ? 0.0f : s;
+        }
       }
+    }
+    float p[NQ][16];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) p[n][k] = exp2_fast(fmaf(score[n][k >> 2][k & 3], ks, start[n]));
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const float* v = p[n];
+      const float s = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7])) + (((v[8] + v[9]) + (v[10] + v[11])) + ((v[12] + v[13]) + (v[14] + v[15])));
+      sum[n] = fmaf(s, e[n] > kFar ? exp2_fast(-e[n]) : 0.0f, sum[n]);
+    }
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         f16x8 w;
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-          const f32x2 two = {p[8 * u + j], p[8 * u + j + 1]};
+          const f32x2 two = {p[n][8 * u + j], p[n][8 * u + j + 1]};
           const f16x2 h = __builtin_convertvector(two, f16x2);
           w[j] = h[0];
           w[j + 1] = h[1];
         }
         weight[n][u] = w;
       }
-    }
   }
 
   // What turns acc into sum 2^(x - top) * value.
-  __device__ __forceinline__ float unit(int n) const { return ref[n] == -INFINITY ? 0.0f : exp2f(ref[n] - top[n]); }
+  __device__ __forceinline__ float unit(int n) const { return ref[n] > kNone ? exp2f(ref[n] - top[n]) : 0.0f; }
 };
 
 // Scores of positions that row `pos` (a position) does not see become -infinity, the others x. vg: the lane's first position.

@@ -24,9 +24,11 @@ constexpr int kTileRows = 16 * kNQ * kWaves;
 
 // LDS writes of all waves before, LDS reads after; loads from memory stay in flight.
 __device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 // Byte of chunk s of lane group q (a quarter of the channels, D / 32 chunks) of key row `row`. The chunks of a row: keys of the
@@ -42,6 +44,53 @@ __device__ __forceinline__ int key_at(int row, int q, int s) {
 }
 // Byte of half u of the 16 positions of lane group q of channel d.
 __device__ __forceinline__ int value_at(int d, int q, int u) { return d * 128 + (((2 * q + u) ^ (((d >> 1) + 2) & 7)) << 4); }
+
+// The order of a product's instructions: six LDS reads first, then two matrix instructions for each further read, so that a read's
+// result is waited for while others are on their way.
+template <int READS>
+__device__ __forceinline__ void reads_ahead() {
+  constexpr int kAhead = 6;
+  __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+  for (int g = 0; g < READS - kAhead; ++g) {
+    __builtin_amdgcn_sched_group_barrier(0x008, kNQ, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, kNQ * kAhead, 0);
+}
+
+// A wave's rows, r = w0 .., to out, or to the parts.
+template <int D>
+__device__ __forceinline__ void write_rows(const KvCall& c, const KvSeq& sq, const Share& sh, int b, int head, int part, int w0, int rows,
+                                           const Rows<kNQ, D / 16>& st) {
+  const int lane = threadIdx.x & 63, col = lane & 15, quarter = lane >> 4;
+#pragma unroll
+  for (int n = 0; n < kNQ; ++n) {
+    const int r = w0 + 16 * n + col;
+    const float total = row_sum(st.sum[n]), unit = st.unit(n);
+    if (r >= rows) continue;
+    const int i = r / c.G, h = head * c.G + r % c.G;
+    if (sh.parts == 1) {
+      const float inv = total == 0.0f ? 0.0f : unit / total;
+      auto* out = static_cast<uint16_t*>(c.out) + ((int64_t(sq.first) + i) * c.Hq + h) * D + 4 * quarter;
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t) {
+        const f32x4& o = st.acc[n][t];
+        *reinterpret_cast<uint2*>(out + 16 * t) = make_uint2(f32x2_to_bf16x2_rne(o[0] * inv, o[1] * inv), f32x2_to_bf16x2_rne(o[2] * inv, o[3] * inv));
+      }
+    } else {
+      const int64_t to = part_row(c, sq, b, i, h) + part;
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t) {
+        f32x4 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = st.acc[n][t][j] * unit;
+        *reinterpret_cast<f32x4*>(c.ws_o + to * D + 16 * t + 4 * quarter) = o;
+      }
+      if (quarter == 0) *reinterpret_cast<float2*>(c.ws_ml + 2 * to) = make_float2(st.top[n], total);
+    }
+  }
+}
 
 template <int D, int FMT>
 __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_tile_kernel(KvCall c) {
@@ -69,36 +118,32 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_tile_
   // values (channel, 16 positions). Pages are asked for two blocks ahead, codes and scales one.
   const int key = tid >> 2, piece = tid & 3;
   const int key_row = 16 * ((key >> 2) & 3) + 4 * (key >> 4) + (key & 3);
-  int spage, vpage;        // of this lane's positions, and of its piece of values
+  int kpage = 0, vpage = 0, spage = 0;     // of the wave's keys, the thread's values, the lane's positions in the blocks loaded next
   uint2 kc[kSteps];
   u32x4 vc[kPieces];
   int live;                // positions of this thread's values that exist
   float ks, vs;            // scales of this lane's positions
   bool there;
-  const auto load_pages = [&](int blk) {
-    const int sg = blk * kBlock + 16 * quarter, vg = blk * kBlock + 16 * piece;
-    const int most = sq.len - 1;
-    spage = table[min(sg, most) >> shift];      // (of the last page where there is none: not used)
-    vpage = table[min(vg, most) >> shift];
-  };
-  const uint8_t* const kp = static_cast<const uint8_t*>(c.k_pages) + ((int64_t(head) << shift) + (key & 15)) * D + piece * (D / 4);
+  int zero;     // (vector loads of the pages: a scalar one would be waited for at the next barrier, with the LDS writes)
+  asm volatile("v_mov_b32 %0, 0" : "=v"(zero));
+  const auto page_of = [&](int position) { return table[(min(position, sq.len - 1) + zero) >> shift]; };     // (past the end: the last page, not used)
+  const uint32_t key_offset = unsigned(((head << shift) + (key & 15)) * D + piece * (D / 4));
   const uint8_t* const vp = static_cast<const uint8_t*>(c.v_pages) + ((int64_t(head) * D + (tid >> 2)) << shift);
-  const auto load = [&](int blk) {
-    const int base = blk * kBlock;
-    const int kg = base + 16 * wave, vg = base + 16 * piece, sg = base + 16 * quarter;
-    there = sg < sq.len && spage >= 0 && spage < c.num_pages;
-    const bool vthere = vg < sq.len && vpage >= 0 && vpage < c.num_pages;
-    live = vthere ? sq.len - vg : 0;
-    const uint32_t page = there ? spage : 0, from = vthere ? vpage : 0;
-    const uint32_t kpage = __builtin_amdgcn_readlane(page, 16 * wave);
-    const uint8_t* k = kp + uint64_t(kpage) * c.page_bytes + (kg & (P - 1)) * D;
+  const auto load_codes = [&](int blk) {
+    const int vg = blk * kBlock + 16 * piece;
+    live = unsigned(vpage) < unsigned(c.num_pages) ? sq.len - vg : 0;
+    const uint32_t from = live > 0 ? vpage : 0, wanted = __builtin_amdgcn_readfirstlane(kpage), page = wanted < unsigned(c.num_pages) ? wanted : 0;
+    const uint8_t* k = static_cast<const uint8_t*>(c.k_pages) + uint64_t(page) * c.page_bytes + ((blk * kBlock + 16 * wave) & (P - 1)) * D;
     const uint8_t* v = vp + uint64_t(from) * c.page_bytes + (vg & (P - 1));
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) kc[s] = *reinterpret_cast<const uint2*>(k + 8 * s);
+    for (int s = 0; s < kSteps; ++s) kc[s] = *reinterpret_cast<const uint2*>(k + key_offset + 8 * s);
 #pragma unroll
     for (int e = 0; e < kPieces; ++e)
       if (D % 64 == 0 || (tid >> 2) + 64 * e < D) vc[e] = ldg16(v + (int64_t(64 * e) << shift));
-    const uint64_t at = uint64_t(page) * unsigned(c.H) + unsigned(head);
+  };
+  const auto load_scales = [&](int blk) {
+    there = blk * kBlock + 16 * quarter < sq.len && unsigned(spage) < unsigned(c.num_pages);
+    const uint64_t at = uint64_t(there ? spage : 0) * unsigned(c.H) + unsigned(head);
     ks = c.k_scales[at];
     vs = c.v_scales[at];
   };
@@ -118,10 +163,17 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_tile_
     }
   };
   int blk = sh.first + part * sh.each;
+  const auto load_code_pages = [&](int at) {
+    kpage = page_of(at * kBlock + 16 * wave);
+    vpage = page_of(at * kBlock + 16 * piece);
+  };
   if (blk < end) {
-    load_pages(blk);
-    load(blk);
-    load_pages(blk + 1);
+    load_code_pages(blk);
+    spage = page_of(blk * kBlock + 16 * quarter);
+    load_codes(blk);
+    load_scales(blk);
+    load_code_pages(blk + 1);
+    spage = page_of((blk + 1) * kBlock + 16 * quarter);
   }
 
   bf16x8 qf[kNQ][kSteps];
@@ -144,91 +196,264 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_tile_
   for (int buffer = 0; blk < end; ++blk, buffer ^= 1) {
     uint8_t* at = lds + buffer * kBuffer;
     store(at);
-    float f = ks * c.scale_log2;
-    const float lv = there ? log2f(vs) : -INFINITY;
-    const bool here = there;
-    if (blk + 1 < end) {
-      load(blk + 1);
-      load_pages(blk + 2);
-    }
+    load_codes(blk + 1);
+    load_code_pages(blk + 2);
     lds_barrier();
     const int base = blk * kBlock, vg = base + 16 * quarter;
-    // blocks that none of the wave's rows sees
-    if (base > pos_last || (c.window > 0 && base + kBlock - 1 <= pos_first - c.window)) continue;
-    f32x4 score[kNQ][4];
+    // (blocks that none of the wave's rows sees are left out)
+    if (base <= pos_last && (c.window == 0 || base + kBlock - 1 > pos_first - c.window)) {
+      f32x4 score[kNQ][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int n = 0; n < kNQ; ++n) score[n][i] = f32x4{0, 0, 0, 0};
+        for (int n = 0; n < kNQ; ++n) score[n][i] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const bf16x8 kf = *reinterpret_cast<const bf16x8*>(at + key_at<D>(16 * i + col, quarter, s));
+        for (int s = 0; s < kSteps; ++s) {
+          const bf16x8 kf = *reinterpret_cast<const bf16x8*>(at + key_at<D>(16 * i + col, quarter, s));
 #pragma unroll
-        for (int n = 0; n < kNQ; ++n) score[n][i] = mfma_bf16(kf, qf[n][s], score[n][i]);
+          for (int n = 0; n < kNQ; ++n) score[n][i] = mfma_bf16(kf, qf[n][s], score[n][i]);
+        }
       }
-    }
-    if (base + kBlock - 1 > pos_first || (c.window > 0 && base <= pos_last - c.window) || __any(!here)) {
-      mask_scores<kNQ>(score, pos, vg, c.window, here, f);
-      f = 1.0f;
-    }
-    f16x8 weight[kNQ][2];
-    st.step(score, f, lv, weight);
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const f16x8 vf = *reinterpret_cast<const f16x8*>(at + kKeys + value_at(16 * t + col, quarter, u));
-#pragma unroll
-        for (int n = 0; n < kNQ; ++n) st.acc[n][t] = mfma_f16(vf, weight[n][u], st.acc[n][t]);
+      reads_ahead<4 * kSteps>();
+      float f = ks * c.scale_log2;
+      const float lv = there ? log2f(vs) : -INFINITY;
+      if (base + kBlock - 1 > pos_first || (c.window > 0 && base <= pos_last - c.window) || __any(!there)) {
+        mask_scores<kNQ>(score, pos, vg, c.window, there, f);
+        f = 1.0f;
       }
+      f16x8 weight[kNQ][2];
+      st.step(score, f, lv, weight);
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const f16x8 vf = *reinterpret_cast<const f16x8*>(at + kKeys + value_at(16 * t + col, quarter, u));
+#pragma unroll
+          for (int n = 0; n < kNQ; ++n) st.acc[n][t] = mfma_f16(vf, weight[n][u], st.acc[n][t]);
+        }
+      reads_ahead<2 * kTiles>();
+    }
+    // (after the last use of this block's: into the same registers, without a copy that would wait for them)
+    load_scales(blk + 1);
+    spage = page_of((blk + 2) * kBlock + 16 * quarter);
   }
 
+  write_rows<D>(c, sq, sh, b, head, part, w0, rows, st);
+}
+
+// Eight waves, 32 rows each, two on a SIMD: waves 0-3 and 4-7 half a turn apart, so that one wave of a SIMD multiplies (values of block
+// k - 1, keys of block k) while the other has its exponentials, maxima and conversions. A barrier ends each half. Every wave
+// converts its share of the keys of k + 2 and the values of k + 1 in the second half of its turn k: they are complete before
+// the first reader's turn, and with three LDS buffers the one they go to was left by its last reader a half turn before.
+template <int D, int FMT>
+__global__ __launch_bounds__(512, 2) void attention_paired_kernel(KvCall c) {
+  constexpr int kSteps = D / 32, kTiles = D / 16, kRows = 8 * 16 * kNQ;
+  constexpr int kKeys = kBlock * D * 2, kValues = D * kBlock * 2;
+  constexpr int kChunks = D / 64;                                       // 16-byte chunks of bf16 keys a thread stages
+  __shared__ __attribute__((aligned(16))) uint8_t lds[3 * (kKeys + kValues)];
+  const int b = blockIdx.y;
+  const KvSeq sq = attention_sequence(c, b);
+  const int head = int(blockIdx.x % unsigned(c.H)), part = int(blockIdx.x / unsigned(c.H) % unsigned(c.n_split));
+  const int rows = sq.n * c.G, tiles = (rows + kRows - 1) / kRows;
+  // a sequence's last tiles, which see most, first
+  const int r0 = (tiles - 1 - int(blockIdx.x / unsigned(c.H) / unsigned(c.n_split))) * kRows;
+  if (r0 < 0) return;
+  const Share sh = share_of(c, sq, r0, kRows);
+  if (part >= sh.parts) return;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, col = lane & 15, quarter = lane >> 4;
+  const int shift = c.page_shift, P = 1 << shift;
+  const int before = sq.len - sq.n, most = sq.len - 1;
+  const int first = sh.first + part * sh.each, end = min(first + sh.each, sh.end);
+  const int32_t* table = c.table + int64_t(b) * c.width;
+
+  // Staging: a thread takes an eighth of one key's channels (the 8 keys of a wave are of one page, whose address is scalar), and one
+  // 16-byte piece of values (channel, 16 positions).
+  const int key = tid >> 3, eighth = tid & 7, piece = tid & 3;
+  const int key_row = 16 * ((key >> 2) & 3) + 4 * (key >> 4) + (key & 3);
+  uint2 kc[kChunks];
+  u32x4 vc;
+  int live = 16;                        // positions of this thread's values that exist
+  float ks = 0, vs = 0;                 // scales of this lane's positions
+  bool there = false;
+  int kpage = 0, vpage = 0, spage = 0;
+  // Page of a position (past the end: the last page, not used). Asked for by vector loads, the wave's own too: a scalar one would be
+  // waited for at the next barrier, with the LDS writes.
+  int zero;
+  asm volatile("v_mov_b32 %0, 0" : "=v"(zero));
+  const auto page_of = [&](int position) { return table[(min(position, most) + zero) >> shift]; };
+  const uint32_t key_offset = unsigned(((head << shift) + (key & 15)) * D + eighth * (D / 8));
+  const uint8_t* const vp = static_cast<const uint8_t*>(c.v_pages) + ((int64_t(head) * D + (tid >> 2)) << shift);
+  const auto load_keys = [&](int blk) {
+    const uint32_t from = __builtin_amdgcn_readfirstlane(kpage);
+    const uint32_t page = from < unsigned(c.num_pages) ? from : 0;
+    const uint8_t* k = static_cast<const uint8_t*>(c.k_pages) + uint64_t(page) * c.page_bytes + ((blk * kBlock + 16 * (wave >> 1)) & (P - 1)) * D;
+#pragma unroll
+    for (int s = 0; s < kChunks; ++s) kc[s] = *reinterpret_cast<const uint2*>(k + key_offset + 8 * s);
+  };
+  const auto load_values = [&](int blk) {
+    const int vg = blk * kBlock + 16 * piece;
+    live = unsigned(vpage) < unsigned(c.num_pages) ? sq.len - vg : 0;
+    const uint32_t from = live > 0 ? vpage : 0;
+    if (D == 128 || wave < D / 16) vc = ldg16(vp + uint64_t(from) * c.page_bytes + (vg & (P - 1)));
+  };
+  const auto load_scales = [&](int blk) {
+    there = blk * kBlock + 16 * quarter <= most && unsigned(spage) < unsigned(c.num_pages);
+    const uint64_t at = uint64_t(there ? spage : 0) * unsigned(c.H) + unsigned(head);
+    ks = c.k_scales[at];
+    vs = c.v_scales[at];
+  };
+  const auto store_keys = [&](uint8_t* to) {
+#pragma unroll
+    for (int s = 0; s < kChunks; ++s) {
+      const int chunk = eighth * kChunks + s;
+      *reinterpret_cast<bf16x8*>(to + key_at<D>(key_row, chunk / kSteps, chunk % kSteps)) = codes_bf16<FMT>(kc[s].x, kc[s].y);
+    }
+  };
+  const auto store_values = [&](uint8_t* to) {
+    if (D == 128 || wave < D / 16) {
+      if (__any(live < 16)) vc = live_codes(vc, live);
+      *reinterpret_cast<f16x8*>(to + value_at(tid >> 2, piece, 0)) = codes_f16<FMT>(vc[0], vc[1]);
+      *reinterpret_cast<f16x8*>(to + value_at(tid >> 2, piece, 1)) = codes_f16<FMT>(vc[2], vc[3]);
+    }
+  };
+
+  bf16x8 qf[kNQ][kSteps];
+  int pos[kNQ];
+  const int w0 = r0 + wave * 16 * kNQ;      // the wave's first row
 #pragma unroll
   for (int n = 0; n < kNQ; ++n) {
     const int r = w0 + 16 * n + col;
-    const float total = row_sum(st.sum[n]), unit = st.unit(n);
-    if (r >= rows) continue;
-    const int i = r / c.G, h = head * c.G + r % c.G;
-    if (sh.parts == 1) {
-      const float inv = total == 0.0f ? 0.0f : unit / total;
-      auto* out = static_cast<uint16_t*>(c.out) + ((int64_t(sq.first) + i) * c.Hq + h) * D + 4 * quarter;
+    const int i = r / c.G, g = r - i * c.G;
+    pos[n] = r < rows ? before + i : -1;
+    const auto* qp = static_cast<const uint16_t*>(c.q) + (int64_t(sq.first) + i) * c.q_stride + int64_t(head * c.G + g) * D + quarter * (D / 4);
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        const f32x4& o = st.acc[n][t];
-        *reinterpret_cast<uint2*>(out + 16 * t) = make_uint2(f32x2_to_bf16x2_rne(o[0] * inv, o[1] * inv), f32x2_to_bf16x2_rne(o[2] * inv, o[3] * inv));
+    for (int s = 0; s < kSteps; ++s) qf[n][s] = r < rows ? query8(qp + 8 * s, c.q_sign) : bf16x8{};
+  }
+  const int pos_first = before + w0 / c.G;
+  const int pos_last = w0 < rows ? before + (min(w0 + 16 * kNQ, rows) - 1) / c.G : -1;
+  // whether one of the wave's rows sees a block
+  const auto sees = [&](int blk) { return blk * kBlock <= pos_last && (c.window == 0 || blk * kBlock + kBlock - 1 > pos_first - c.window); };
+
+  Rows<kNQ, kTiles> st;
+  st.clear();
+  if (first < end) {
+    uint8_t* const values = lds + 3 * kKeys;
+    kpage = page_of(first * kBlock + 16 * (wave >> 1));
+    vpage = page_of(first * kBlock + 16 * piece);
+    spage = page_of(first * kBlock + 16 * quarter);
+    load_keys(first);
+    load_values(first);
+    load_scales(first);
+    kpage = page_of((first + 1) * kBlock + 16 * (wave >> 1));
+    vpage = page_of((first + 1) * kBlock + 16 * piece);
+    spage = page_of((first + 1) * kBlock + 16 * quarter);
+    store_keys(lds);
+    store_values(values);
+    load_keys(first + 1);
+    kpage = page_of((first + 2) * kBlock + 16 * (wave >> 1));
+    load_values(first + 1);
+    vpage = page_of((first + 2) * kBlock + 16 * piece);
+    store_keys(lds + kKeys);
+    load_keys(first + 2);
+    kpage = page_of((first + 3) * kBlock + 16 * (wave >> 1));
+    lds_barrier();
+    if (wave >= 4) lds_barrier();
+    f32x4 score[kNQ][4];
+    f16x8 weight[kNQ][2];
+    bool seen = false;                  // block k - 1, whose weights the wave has
+    int at = 0, next = 2;               // buffers of keys k and k + 2; block j's keys and values are in buffers j mod 3, k - 1 and k + 2 in the same
+    for (int blk = first; blk <= end; ++blk) {
+      if (seen) {
+        const uint8_t* v = values + next * kValues;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const f16x8 vf = *reinterpret_cast<const f16x8*>(v + value_at(16 * t + col, quarter, u));
+#pragma unroll
+            for (int n = 0; n < kNQ; ++n) st.acc[n][t] = mfma_f16(vf, weight[n][u], st.acc[n][t]);
+          }
+        reads_ahead<2 * kTiles>();
       }
-    } else {
-      const int64_t to = part_row(c, sq, b, i, h) + part;
+      seen = blk < end && sees(blk);
+      if (seen) {
+        const uint8_t* k = lds + at * kKeys;
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        f32x4 o;
+        for (int i = 0; i < 4; ++i) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = st.acc[n][t][j] * unit;
-        *reinterpret_cast<f32x4*>(c.ws_o + to * D + 16 * t + 4 * quarter) = o;
+          for (int n = 0; n < kNQ; ++n) score[n][i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) {
+            const bf16x8 kf = *reinterpret_cast<const bf16x8*>(k + key_at<D>(16 * i + col, quarter, s));
+#pragma unroll
+            for (int n = 0; n < kNQ; ++n) score[n][i] = mfma_bf16(kf, qf[n][s], score[n][i]);
+          }
+        }
+        reads_ahead<4 * kSteps>();
       }
-      if (quarter == 0) *reinterpret_cast<float2*>(c.ws_ml + 2 * to) = make_float2(st.top[n], total);
+      lds_barrier();
+      if (blk < end) {
+        const int base = blk * kBlock;
+        store_keys(lds + next * kKeys);
+        store_values(values + (at == 2 ? 0 : at + 1) * kValues);
+        load_keys(blk + 3);
+        load_values(blk + 2);
+        kpage = page_of((blk + 4) * kBlock + 16 * (wave >> 1));
+        vpage = page_of((blk + 3) * kBlock + 16 * piece);
+        if (seen) {
+          float f = ks * c.scale_log2;
+          const float lv = there ? log2f(vs) : -INFINITY;
+          if (base + kBlock - 1 > pos_first || (c.window > 0 && base <= pos_last - c.window) || __any(!there)) {
+            mask_scores<kNQ>(score, pos, base + 16 * quarter, c.window, there, f);
+            f = 1.0f;
+          }
+          st.step(score, f, lv, weight);
+        }
+        // (after the last use of this block's: into the same registers, without a copy that would wait for them)
+        load_scales(blk + 1);
+        spage = page_of((blk + 2) * kBlock + 16 * quarter);
+      }
+      lds_barrier();
+      at = at == 2 ? 0 : at + 1;
+      next = next == 2 ? 0 : next + 1;
+    }
+    if (wave < 4) lds_barrier();
+  }
+
+  write_rows<D>(c, sq, sh, b, head, part, w0, rows, st);
+}
+
+template <int D, int FMT>
+hipError_t go(const KvCall& c, hipStream_t s) {
+  const int64_t rows = int64_t(c.hi_n) * c.G;
+  const int tile = attention_tile_rows(c);
+  const dim3 grid(unsigned((rows + tile - 1) / tile) * unsigned(c.n_split) * unsigned(c.H), unsigned(c.B));
+  if constexpr (D == 64 || D == 128) {
+    if (tile == 256) {
+      hipLaunchKernelGGL((attention_paired_kernel<D, FMT>), grid, dim3(512), 0, s, c);
+      return hipGetLastError();
     }
   }
+  hipLaunchKernelGGL((attention_tile_kernel<D, FMT>), grid, dim3(kWaves * 64), 0, s, c);
+  return hipGetLastError();
 }
 
 template <int D>
-hipError_t go(const KvCall& c, hipStream_t s) {
-  const int64_t rows = int64_t(c.hi_n) * c.G;
-  const dim3 grid(unsigned((rows + kTileRows - 1) / kTileRows) * unsigned(c.n_split) * unsigned(c.H), unsigned(c.B));
-  if (c.fmt == HQ_KV_INT8) hipLaunchKernelGGL((attention_tile_kernel<D, HQ_KV_INT8>), grid, dim3(kWaves * 64), 0, s, c);
-  else hipLaunchKernelGGL((attention_tile_kernel<D, HQ_KV_FP8_E4M3>), grid, dim3(kWaves * 64), 0, s, c);
-  return hipGetLastError();
+hipError_t pick(const KvCall& c, hipStream_t s) {
+  return c.fmt == HQ_KV_INT8 ? go<D, HQ_KV_INT8>(c, s) : go<D, HQ_KV_FP8_E4M3>(c, s);
 }
 
 }  // namespace
 
+int attention_tile_rows(const KvCall& c) { return (c.D == 64 || c.D == 128) && int64_t(c.max_new) * c.G > kTileRows ? 256 : kTileRows; }
+
 hipError_t launch_attention_tiles(const KvCall& c, hipStream_t s) {
   switch (c.D) {
-    case 64: return go<64>(c, s);
-    case 96: return go<96>(c, s);
-    case 128: return go<128>(c, s);
-    case 192: return go<192>(c, s);
-    default: return go<256>(c, s);
+    case 64: return pick<64>(c, s);
+    case 96: return pick<96>(c, s);
+    case 128: return pick<128>(c, s);
+    case 192: return pick<192>(c, s);
+    default: return pick<256>(c, s);
   }
 }
 

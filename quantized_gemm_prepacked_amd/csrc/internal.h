@@ -177,6 +177,7 @@ struct KvCall {
   float* ws_ml;
 };
 hipError_t launch_kv_append(const KvCall& c, hipStream_t s);
+int attention_tile_rows(const KvCall& c);    // rows of a workgroup of the tiled kernels
 int64_t attention_groups(const KvCall& c);   // workgroups without a split of the positions, at most
 // Sequences of up to `few` new tokens have a launch of their own, those with more (many) another.
 struct AttentionPlan {
