@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kFewRows = 32;     // rows of a head that one workgroup takes here; more go to the tiled kernel
+constexpr int kTileRows = 128;   // rows of a workgroup of the tiled kernel, of its paired form twice that
 constexpr int kMaxSplit = 128;
 
 template <int D, int FMT, int NQ>
@@ -272,10 +273,7 @@ hipError_t pick(const KvCall& c, bool wide, hipStream_t s) {
 
 }  // namespace
 
-int64_t attention_groups(const KvCall& c) {
-  const int tile = attention_tile_rows(c);
-  return (int64_t(c.max_new) * c.G + tile - 1) / tile * c.H * c.B;
-}
+int64_t attention_groups(const KvCall& c) { return (int64_t(c.max_new) * c.G + kTileRows - 1) / kTileRows * c.H * c.B; }
 
 namespace {
 // Parts of the positions: no more workgroups than run at once, each with at least `least` blocks. With more, the last ones
@@ -319,10 +317,14 @@ AttentionPlan plan_attention(const KvCall& c, int64_t max_kv) {
     room(p.few_by_token ? c.T : int64_t(c.B) * p.few, p.few_split, &p.few_o, &p.few_ml);
   }
   if (p.many) {
+    // The kernel of 256 rows a workgroup for one long sequence: it is a tenth faster where the card is full of even work (1024 x 8
+    // rows on 16000: 541 / 598 us, 4096 x 4 on 30000 2012 / 2222, 512 x 8 on 60000 1007 / 1122, a prompt of 8192 x 4 563 / 571),
+    // level at 256 x 4 on 8000 and 64 x 4 on 20000, and slower where tiles are few or uneven (a prompt of 2048 x 4 83 / 65, 4
+    // prompts of 4500 527 / 513, 4 x 512 x 8 on 16000 1019 / 915).
+    p.tile_rows = c.D == 128 && c.B == 1 && most >= 1024 && max_kv >= 4096 ? 2 * kTileRows : kTileRows;
     // tiles there can be: of T rows, with one broken tile a sequence
-    const int tile = attention_tile_rows(c);
-    const int64_t tiles = std::min(attention_groups(c), (c.T * c.G / tile + c.B) * c.H);
-    split_of(tiles, tile == 256 || c.D > 128 ? 256 : 512, 8, max_kv, &p.many_split, &p.many_each);
+    const int64_t tiles = std::min((most + p.tile_rows - 1) / p.tile_rows * c.B, c.T * c.G / p.tile_rows + c.B) * c.H;
+    split_of(tiles, p.tile_rows > kTileRows || c.D > 128 ? 256 : 512, 8, max_kv, &p.many_split, &p.many_each);
     room(c.T, p.many_split, &p.many_o, &p.many_ml);
   }
   p.ws_bytes = at;
@@ -353,6 +355,7 @@ hipError_t launch_attention(const KvCall& call, const AttentionPlan& p, uint8_t*
     KvCall c = call;
     c.lo_n = p.few + 1;
     c.hi_n = c.max_new;
+    c.tile_rows = p.tile_rows;
     c.n_split = p.many_split;
     c.each = p.many_each;
     c.by_token = true;
@@ -361,11 +364,11 @@ hipError_t launch_attention(const KvCall& call, const AttentionPlan& p, uint8_t*
     const hipError_t e = launch_attention_tiles(c, s);
     if (e != hipSuccess) return e;
     switch (c.D) {
-      case 64: return join<64>(c, attention_tile_rows(c), s);
-      case 96: return join<96>(c, attention_tile_rows(c), s);
-      case 128: return join<128>(c, attention_tile_rows(c), s);
-      case 192: return join<192>(c, attention_tile_rows(c), s);
-      default: return join<256>(c, attention_tile_rows(c), s);
+      case 64: return join<64>(c, p.tile_rows, s);
+      case 96: return join<96>(c, p.tile_rows, s);
+      case 128: return join<128>(c, p.tile_rows, s);
+      case 192: return join<192>(c, p.tile_rows, s);
+      default: return join<256>(c, p.tile_rows, s);
     }
   }
   return hipSuccess;

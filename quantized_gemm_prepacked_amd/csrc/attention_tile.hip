@@ -31,6 +31,19 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// A workgroup's part of the work. One sequence after the other, its last tiles first, which see most. Heads next to each other: with
+// eight of them a head's workgroups run on one XCD, whose L2 then holds one head of one or two sequences (with all sequences' tiles
+// in turn instead, 4 prompts of 4500 take 690 us, not 505).
+struct Place {
+  int head, b, part, r0;
+};
+
+__device__ __forceinline__ Place place_of(const KvCall& c, int tile_rows) {
+  const unsigned heads = unsigned(c.H), parts = unsigned(c.n_split);
+  const unsigned tile = (gridDim.x - 1 - blockIdx.x) / (heads * parts);
+  return {int(blockIdx.x % heads), int(blockIdx.y), int(blockIdx.x / heads % parts), int(tile) * tile_rows};
+}
+
 // Byte of chunk s of lane group q (a quarter of the channels, D / 32 chunks) of key row `row`. The chunks of a row: keys of the
 // row's eight lanes of one group and of the other eight are two sets that the difference between the groups' chunks maps to
 // themselves. Head sizes that are no power of two: a plane for each group, of rows an odd number of chunks long.
@@ -99,13 +112,11 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_tile_
   constexpr int kBuffer = kKeys + D * kBlock * 2;
   constexpr int kPieces = (D * 4 + kWaves * 64 - 1) / (kWaves * 64);    // 16-byte pieces of values a thread stages
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kBuffer];
-  const int b = blockIdx.y;
+  const Place place = place_of(c, kTileRows);
+  const int head = place.head, b = place.b, part = place.part, r0 = place.r0;
   const KvSeq sq = attention_sequence(c, b);
-  const int head = int(blockIdx.x % unsigned(c.H)), part = int(blockIdx.x / unsigned(c.H) % unsigned(c.n_split));
-  const int rows = sq.n * c.G, tiles = (rows + kTileRows - 1) / kTileRows;
-  // a sequence's last tiles, which see most, first
-  const int r0 = (tiles - 1 - int(blockIdx.x / unsigned(c.H) / unsigned(c.n_split))) * kTileRows;
-  if (r0 < 0) return;
+  const int rows = sq.n * c.G;
+  if (r0 >= rows) return;
   const Share sh = share_of(c, sq, r0, kTileRows);
   if (part >= sh.parts) return;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, col = lane & 15, quarter = lane >> 4;
@@ -245,19 +256,20 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_tile_
 // k - 1, keys of block k) while the other has its exponentials, maxima and conversions. A barrier ends each half. Every wave
 // converts its share of the keys of k + 2 and the values of k + 1 in the second half of its turn k: they are complete before
 // the first reader's turn, and with three LDS buffers the one they go to was left by its last reader a half turn before.
-template <int D, int FMT>
+// Head size 128 alone: larger ones leave no room for two waves on a SIMD, at 64 three workgroups of the kernel above do better
+// (2048 rows of 8 heads on 30000: 1443 us, 1632 here).
+template <int FMT>
 __global__ __launch_bounds__(512, 2) void attention_paired_kernel(KvCall c) {
+  constexpr int D = 128;
   constexpr int kSteps = D / 32, kTiles = D / 16, kRows = 8 * 16 * kNQ;
   constexpr int kKeys = kBlock * D * 2, kValues = D * kBlock * 2;
   constexpr int kChunks = D / 64;                                       // 16-byte chunks of bf16 keys a thread stages
   __shared__ __attribute__((aligned(16))) uint8_t lds[3 * (kKeys + kValues)];
-  const int b = blockIdx.y;
+  const Place place = place_of(c, kRows);
+  const int head = place.head, b = place.b, part = place.part, r0 = place.r0;
   const KvSeq sq = attention_sequence(c, b);
-  const int head = int(blockIdx.x % unsigned(c.H)), part = int(blockIdx.x / unsigned(c.H) % unsigned(c.n_split));
-  const int rows = sq.n * c.G, tiles = (rows + kRows - 1) / kRows;
-  // a sequence's last tiles, which see most, first
-  const int r0 = (tiles - 1 - int(blockIdx.x / unsigned(c.H) / unsigned(c.n_split))) * kRows;
-  if (r0 < 0) return;
+  const int rows = sq.n * c.G;
+  if (r0 >= rows) return;
   const Share sh = share_of(c, sq, r0, kRows);
   if (part >= sh.parts) return;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, col = lane & 15, quarter = lane >> 4;
@@ -294,7 +306,7 @@ __global__ __launch_bounds__(512, 2) void attention_paired_kernel(KvCall c) {
     const int vg = blk * kBlock + 16 * piece;
     live = unsigned(vpage) < unsigned(c.num_pages) ? sq.len - vg : 0;
     const uint32_t from = live > 0 ? vpage : 0;
-    if (D == 128 || wave < D / 16) vc = ldg16(vp + uint64_t(from) * c.page_bytes + (vg & (P - 1)));
+    vc = ldg16(vp + uint64_t(from) * c.page_bytes + (vg & (P - 1)));
   };
   const auto load_scales = [&](int blk) {
     there = blk * kBlock + 16 * quarter <= most && unsigned(spage) < unsigned(c.num_pages);
@@ -310,11 +322,9 @@ __global__ __launch_bounds__(512, 2) void attention_paired_kernel(KvCall c) {
     }
   };
   const auto store_values = [&](uint8_t* to) {
-    if (D == 128 || wave < D / 16) {
-      if (__any(live < 16)) vc = live_codes(vc, live);
-      *reinterpret_cast<f16x8*>(to + value_at(tid >> 2, piece, 0)) = codes_f16<FMT>(vc[0], vc[1]);
-      *reinterpret_cast<f16x8*>(to + value_at(tid >> 2, piece, 1)) = codes_f16<FMT>(vc[2], vc[3]);
-    }
+    if (__any(live < 16)) vc = live_codes(vc, live);
+    *reinterpret_cast<f16x8*>(to + value_at(tid >> 2, piece, 0)) = codes_f16<FMT>(vc[0], vc[1]);
+    *reinterpret_cast<f16x8*>(to + value_at(tid >> 2, piece, 1)) = codes_f16<FMT>(vc[2], vc[3]);
   };
 
   bf16x8 qf[kNQ][kSteps];
@@ -426,11 +436,11 @@ __global__ __launch_bounds__(512, 2) void attention_paired_kernel(KvCall c) {
 template <int D, int FMT>
 hipError_t go(const KvCall& c, hipStream_t s) {
   const int64_t rows = int64_t(c.hi_n) * c.G;
-  const int tile = attention_tile_rows(c);
-  const dim3 grid(unsigned((rows + tile - 1) / tile) * unsigned(c.n_split) * unsigned(c.H), unsigned(c.B));
-  if constexpr (D == 64 || D == 128) {
-    if (tile == 256) {
-      hipLaunchKernelGGL((attention_paired_kernel<D, FMT>), grid, dim3(512), 0, s, c);
+  const int64_t tiles = (rows + c.tile_rows - 1) / c.tile_rows;
+  const dim3 grid(unsigned(c.H) * unsigned(c.n_split) * unsigned(tiles), unsigned(c.B));
+  if constexpr (D == 128) {
+    if (c.tile_rows == 2 * kTileRows) {
+      hipLaunchKernelGGL((attention_paired_kernel<FMT>), grid, dim3(512), 0, s, c);
       return hipGetLastError();
     }
   }
@@ -444,8 +454,6 @@ hipError_t pick(const KvCall& c, hipStream_t s) {
 }
 
 }  // namespace
-
-int attention_tile_rows(const KvCall& c) { return (c.D == 64 || c.D == 128) && int64_t(c.max_new) * c.G > kTileRows ? 256 : kTileRows; }
 
 hipError_t launch_attention_tiles(const KvCall& c, hipStream_t s) {
   switch (c.D) {

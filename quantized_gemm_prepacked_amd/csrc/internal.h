@@ -171,19 +171,19 @@ struct KvCall {
   uint32_t q_sign;                        // sm_scale < 0: the signs of two bf16
   void* out;
   int lo_n, hi_n;                         // one launch: sequences with that many new tokens,
+  int tile_rows;                          // rows of a workgroup of the tiled kernels,
   int n_split, each;                      // parts of the positions at most, and blocks of a part at least,
   bool by_token;                          // partial results by row of q (else by sequence and token),
   float* ws_o;                            // [row][part][D], and (maximum, sum) of each part
   float* ws_ml;
 };
 hipError_t launch_kv_append(const KvCall& c, hipStream_t s);
-int attention_tile_rows(const KvCall& c);    // rows of a workgroup of the tiled kernels
 int64_t attention_groups(const KvCall& c);   // workgroups without a split of the positions, at most
 // Sequences of up to `few` new tokens have a launch of their own, those with more (many) another.
 struct AttentionPlan {
   int few;
   bool many, few_by_token, few_wide;      // few_wide: 32 rows a workgroup, not 16
-  int few_split, few_each, many_split, many_each;
+  int few_split, few_each, many_split, many_each, tile_rows;
   size_t few_o, few_ml, many_o, many_ml, ws_bytes;
 };
 AttentionPlan plan_attention(const KvCall& c, int64_t max_kv);

@@ -203,6 +203,19 @@ def test_several_tokens(fmt, D, H, G, P, window):
 
 
 @pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("H,G,P,new,length,window", [(1, 4, 16, 256, 256, 0), (2, 8, 64, 129, 129, 0), (1, 16, 256, 70, 1000, 0), (1, 5, 32, 333, 700, 100),
+                                                     (2, 64, 16, 17, 65, 0), (1, 128, 128, 9, 640, 33), (1, 8, 16, 200, 90, 0)])
+def test_many_rows_of_one_long_sequence(fmt, H, G, P, new, length, window):
+    """More rows than a workgroup of 128 or 256 takes, a broken last tile, more tokens than positions; max_kv says that the past may be
+    long, whatever it is."""
+    g = np.random.default_rng([H, G, P, new])
+    c = kv_case(g, fmt, H, 128, P, [new], [length], peaky=0.6, behind=1)
+    if length == 700:
+        c["table"][0, 3], c["table"][0, 15] = -1, c["desc"].num_pages      # pages freed behind a window, and one in it
+    _check(c, normal_rows(g, c["T"], H * G, 128), window=window, max_kv=4096, what=f"{fmt} H={H} G={G} P={P} {new} on {length}")
+
+
+@pytest.mark.parametrize("fmt", list(KV))
 @pytest.mark.parametrize("new", [1, 4, 40])
 def test_rows_that_see_nothing(fmt, new):
     """Empty sequences, more queries than positions, no page left, pages freed in the middle: rows without a token are zeros, the
