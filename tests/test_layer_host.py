@@ -138,6 +138,21 @@ def test_attention_oracle_empty_rows_and_left_out():
     assert np.allclose(one[5, 0], v)
 
 
+def test_page_quotients_are_the_ieee_ones():
+    """The append's quotient, a product with fp32(1 / s) and one correction, for every mantissa of a bf16 value and of a page's scale:
+    the IEEE quotient (the fused operations in float64, where product and remainder are exact)."""
+    m = (np.arange(128, 256) / 128).astype(np.float32)
+    for unit in (np.float32(1) / np.float32(127), np.float32(1) / np.float32(448)):
+        for s in m * unit:
+            rs = np.float32(1) / s
+            q = m * rs
+            r = (m.astype(np.float64) - q.astype(np.float64) * np.float64(s)).astype(np.float32)
+            got = (q.astype(np.float64) + r.astype(np.float64) * np.float64(rs)).astype(np.float32)
+            assert np.array_equal(got, m / s)
+    # and the product alone is not always
+    assert any(not np.array_equal(m * (np.float32(1) / s), m / s) for s in m * (np.float32(1) / np.float32(127)))
+
+
 # ---- what the bounds can see ------------------------------------------------------------------
 @pytest.mark.parametrize("tokens", [40, 1000])
 def test_bounds_see_mistakes(tokens):
