@@ -45,41 +45,44 @@ __global__ __launch_bounds__(kWaves * 64) void attention_kernel(KvCall c) {
   const int shift = c.page_shift, P = 1 << shift;
   const int before = sq.len - sq.n;
 
-  // pages, then codes and scales, of the wave's next block
+  // codes and scales of one of the wave's blocks, and the pages of the block that is asked for next
+  struct Codes {
+    uint2 k[4][kSteps];
+    u32x4 v[kTiles];
+    float ks, vs;
+    bool there;      // the page of the 16 positions whose values the lane holds
+  };
   const auto* kp = static_cast<const uint8_t*>(c.k_pages);
   const auto* vp = static_cast<const uint8_t*>(c.v_pages);
   const int32_t* table = c.table + int64_t(b) * c.width;
   const int end = min(sh.first + (part + 1) * sh.each, sh.end);
   int blk = sh.first + part * sh.each + wave;
-  int kpage, vpage;               // of the 16 positions whose keys this lane loads, and whose values it holds
-  uint2 kc[4][kSteps];
-  u32x4 vc[kTiles];
-  float ks, vs;
+  int kpage, vpage;      // of the 16 positions whose keys this lane loads, and of those whose values it holds
   const auto load_pages = [&](int at) {
     const int kg = at * kBlock + 16 * (col >> 2), vg = at * kBlock + 16 * quarter;
     kpage = at < end && kg < sq.len ? table[kg >> shift] : -1;
     vpage = at < end && vg < sq.len ? table[vg >> shift] : -1;
   };
-  const auto load_keys = [&](int at) {
+  const auto load_keys = [&](int at, Codes& to) {
     const int kg = at * kBlock + 16 * (col >> 2);
-    const int page = kpage >= 0 && kpage < c.num_pages ? kpage : 0;
-    const uint8_t* p = kp + ((int64_t(page) * c.H + head) * P + (kg & (P - 1)) + (col & 3)) * D + quarter * (D / 4);
+    const uint32_t page = unsigned(kpage) < unsigned(c.num_pages) ? kpage : 0;
+    const uint8_t* p = kp + uint64_t(page) * c.page_bytes + ((head << shift) + (kg & (P - 1)) + (col & 3)) * D + quarter * (D / 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) kc[i][s] = *reinterpret_cast<const uint2*>(p + 4 * i * D + 8 * s);
+      for (int s = 0; s < kSteps; ++s) to.k[i][s] = *reinterpret_cast<const uint2*>(p + 4 * i * D + 8 * s);
   };
-  bool there = false;
-  const auto load_values = [&](int at) {
+  const auto load_values = [&](int at, Codes& to) {
     const int vg = at * kBlock + 16 * quarter;
-    there = vpage >= 0 && vpage < c.num_pages;
-    const int64_t page = there ? vpage : 0;
-    const uint8_t* p = vp + ((page * c.H + head) * D + col) * P + (vg & (P - 1));
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) vc[t] = ldg16(p + int64_t(16 * t) * P);
+    to.there = unsigned(vpage) < unsigned(c.num_pages);
     // (a page that does not exist stands for page 0, whose scales may be anything)
-    ks = c.k_scales[page * c.H + head];
-    vs = c.v_scales[page * c.H + head];
+    const uint32_t page = to.there ? vpage : 0;
+    const uint8_t* p = vp + uint64_t(page) * c.page_bytes + (((head * D + col) << shift) + (vg & (P - 1)));
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) to.v[t] = ldg16(p + ((16 * t) << shift));
+    const uint64_t scale = uint64_t(page) * unsigned(c.H) + unsigned(head);
+    to.ks = c.k_scales[scale];
+    to.vs = c.v_scales[scale];
   };
   load_pages(blk);
 
@@ -97,15 +100,11 @@ __global__ __launch_bounds__(kWaves * 64) void attention_kernel(KvCall c) {
   }
   const int pos_first = before + r0 / c.G, pos_last = before + (min(r0 + 16 * NQ, rows) - 1) / c.G;
 
-  if (blk < end) {
-    load_keys(blk);
-    load_values(blk);
-    load_pages(blk + kWaves);
-  }
   Rows<NQ, kTiles> st;
   st.clear();
-  for (; blk < end; blk += kWaves) {
-    const int base = blk * kBlock, vg = base + 16 * quarter;
+  // A block's turn. `keys_done` runs when its keys are used up.
+  const auto turn = [&](int at, Codes& x, auto keys_done) {
+    const int base = at * kBlock, vg = base + 16 * quarter;
     f32x4 score[NQ][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -113,20 +112,20 @@ __global__ __launch_bounds__(kWaves * 64) void attention_kernel(KvCall c) {
       for (int n = 0; n < NQ; ++n) score[n][i] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const bf16x8 kf = codes_bf16<FMT>(kc[i][s].x, kc[i][s].y);
+        const bf16x8 kf = codes_bf16<FMT>(x.k[i][s].x, x.k[i][s].y);
 #pragma unroll
         for (int n = 0; n < NQ; ++n) score[n][i] = mfma_bf16(kf, qf[n][s], score[n][i]);
       }
     }
-    if (blk + kWaves < end) load_keys(blk + kWaves);
-    float f = ks * c.scale_log2;
-    const float lv = there ? log2f(vs) : -INFINITY;
-    if (base + kBlock - 1 > pos_first || (c.window > 0 && base <= pos_last - c.window) || __any(!there)) {
-      mask_scores<NQ>(score, pos, vg, c.window, there, f);
+    keys_done();
+    float f = x.ks * c.scale_log2;
+    const float lv = x.there ? log2f(x.vs) : -INFINITY;
+    if (base + kBlock - 1 > pos_first || (c.window > 0 && base <= pos_last - c.window) || __any(!x.there)) {
+      mask_scores<NQ>(score, pos, vg, c.window, x.there, f);
       f = 1.0f;
-      const int live = there ? sq.len - vg : 0;
+      const int live = x.there ? sq.len - vg : 0;
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) vc[t] = live_codes(vc[t], live);
+      for (int t = 0; t < kTiles; ++t) x.v[t] = live_codes(x.v[t], live);
     }
     f16x8 weight[NQ][2];
     st.step(score, f, lv, weight);
@@ -134,12 +133,24 @@ __global__ __launch_bounds__(kWaves * 64) void attention_kernel(KvCall c) {
     for (int t = 0; t < kTiles; ++t)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const f16x8 vf = codes_f16<FMT>(vc[t][2 * u], vc[t][2 * u + 1]);
+        const f16x8 vf = codes_f16<FMT>(x.v[t][2 * u], x.v[t][2 * u + 1]);
 #pragma unroll
         for (int n = 0; n < NQ; ++n) st.acc[n][t] = mfma_f16(vf, weight[n][u], st.acc[n][t]);
       }
+  };
+  Codes x;
+  if (blk < end) {
+    load_keys(blk, x);
+    load_values(blk, x);
+    load_pages(blk + kWaves);
+  }
+  // the next block's keys into the registers of this one's as soon as they are used up, and so its values
+  for (; blk < end; blk += kWaves) {
+    turn(blk, x, [&] {
+      if (blk + kWaves < end) load_keys(blk + kWaves, x);
+    });
     if (blk + kWaves < end) {
-      load_values(blk + kWaves);
+      load_values(blk + kWaves, x);
       load_pages(blk + 2 * kWaves);
     }
   }
