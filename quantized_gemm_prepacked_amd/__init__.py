@@ -359,6 +359,8 @@ def _at(x, count, kind, dev, what):
 
 def _stream_at(stream, dev):
     """The stream's handle; a stream object has to belong to the current device, as the buffers do."""
+    if stream is None and dev >= 0:
+        return torch._C._cuda_getCurrentRawStream(dev)
     if stream is not None and getattr(stream, "device_index", dev) != dev:
         raise HQError(HQ_ERR_INVALID_ARGUMENT, "stream must be on the current device")
     return _stream(stream)
