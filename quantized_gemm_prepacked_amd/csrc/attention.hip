@@ -328,13 +328,16 @@ AttentionPlan plan_attention(const KvCall& c, int64_t max_kv) {
     room(p.few_by_token ? c.T : int64_t(c.B) * p.few, p.few_split, &p.few_o, &p.few_ml);
   }
   if (p.many) {
-    // The kernel of 256 rows a workgroup for one long sequence: it is a tenth faster where the card is full of even work (1024 x 8
-    // rows on 16000: 541 / 598 us, 4096 x 4 on 30000 2012 / 2222, 512 x 8 on 60000 1007 / 1122, a prompt of 8192 x 4 563 / 571),
-    // level at 256 x 4 on 8000 and 64 x 4 on 20000, and slower where tiles are few or uneven (a prompt of 2048 x 4 83 / 65, 4
-    // prompts of 4500 527 / 513, 4 x 512 x 8 on 16000 1019 / 915).
-    p.tile_rows = c.D == 128 && c.B == 1 && most >= 1024 && max_kv >= 4096 ? 2 * kTileRows : kTileRows;
-    // tiles there can be: of T rows, with one broken tile a sequence
-    const int64_t tiles = std::min((most + p.tile_rows - 1) / p.tile_rows * c.B, c.T * c.G / p.tile_rows + c.B) * c.H;
+    // Tiles there can be: of T rows, with one broken tile a sequence.
+    const auto tiles_of = [&](int64_t rows) { return std::min((most + rows - 1) / rows * c.B, c.T * c.G / rows + c.B) * c.H; };
+    // The kernel of 256 rows a workgroup for long sequences whose work fills the card: each tile sees about as many positions, or
+    // there are two tiles a CU (us with 128 rows a workgroup / with 256): 1024 x 8 rows on 30000 1104 / 897, 4 x 512 x 8 on 16000
+    // 554 / 456, 256 x 4 on 8000 67 / 62; prompts, 8 heads of the cache, of 8192 x 4 562 / 507, 4096 x 4 175 / 147, 2048 x 8 100 / 89.
+    // Fewer or shorter ones are better off with small tiles: prompts of 2048 x 4 62 / 70, of 4500 x 1 114 / 133, of 9000 x 1 233 / 250,
+    // 8 of 1000 x 4 74 / 83, of 8192 x 4 with a window of 1024 185 / 191.
+    const bool even = max_kv >= 2 * int64_t(c.max_new), full = tiles_of(2 * kTileRows) >= 512;
+    p.tile_rows = c.D == 128 && max_kv >= 2048 && c.T * c.G >= 2 * kTileRows * int64_t(c.B) && (even || full) ? 2 * kTileRows : kTileRows;
+    const int64_t tiles = tiles_of(p.tile_rows);
     split_of(tiles, p.tile_rows > kTileRows || c.D > 128 ? 256 : 512, 8, max_kv, &p.many_split, &p.many_each);
     room(c.T, p.many_split, &p.many_o, &p.many_ml);
   }

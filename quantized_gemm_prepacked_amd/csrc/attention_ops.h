@@ -67,13 +67,13 @@ __device__ __forceinline__ float row_sum(float v) {
 
 // Running softmax of the rows a lane holds. With x = sm_scale * log2(e) * q . k and s_v the scale of the position's values:
 //   sum = sum 2^(x - top)  (this lane's positions),   acc = sum 2^(x + log2 s_v - ref) * code,
-// with references top and ref within kSlack of the maxima of x and of x + log2 s_v seen so far: the maxima are taken over
-// a row's four lanes, and what was summed before is brought to new references, only in blocks where one moves by more than
-// that (the first and a few others), at the price of weights up to 2^kSlack.
+// with references top and ref below the maxima of x and of x + log2 s_v seen so far by little enough that a lane's 16 terms
+// add up to kMost at most: the sums that are made anyhow tell, so that the maxima are taken, over a row's four lanes, and
+// what was summed before is brought to new references, only in blocks where one has to move (the first and a few others).
 // The weights 2^(x + log2 s_v - ref) enter the product with the codes as fp16: each is off by 2^-11 of itself or 2^-25 of the
 // row's largest, whatever the scales (a bf16 weight, off by 2^-8, made the result's error half as large again as the
 // rounding of the result itself). Statistics and sums are fp32.
-constexpr float kSlack = 8.0f;
+constexpr float kMost = 256.0f;
 constexpr float kFar = -60.0f;
 constexpr float kNone = -3e38f;     // reference of a row that has seen nothing: its scores are -infinity, its sums 0
 
@@ -94,26 +94,19 @@ struct Rows {
 
   // A block's scores to weights. Scores are products of q and k codes, ks >= 0 makes them x (where masked they are -infinity or
   // x already, and ks is 1); lv = log2 of the values' scale, -infinity where that is 0 or there is no page.
+  // The weights are made with the references there are, and again where those move.
   __device__ __forceinline__ void step(const f32x4 (&score)[NQ][4], float ks, float lv, f16x8 (&weight)[NQ][2]) {
-    float m[NQ], start[NQ], e[NQ];
+    float part[NQ], more[NQ], e[NQ];
+    weigh(score, ks, lv, weight, part, more, e);
     bool rare = false;
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      m[n] = score[n][0][0];
-#pragma unroll
-      for (int k = 1; k < 16; ++k) m[n] = fmaxf(m[n], score[n][k >> 2][k & 3]);
-      m[n] *= ks;
-      start[n] = lv - ref[n];
-      e[n] = lv + (top[n] - ref[n]);      // log2 of weight / 2^(x - top)
-      rare |= !(m[n] <= top[n] + kSlack && m[n] + start[n] <= kSlack && e[n] > kFar);
-    }
-    const bool any_rare = __any(rare);
-    if (any_rare) {
+    for (int n = 0; n < NQ; ++n) rare |= !(part[n] <= kMost && more[n] <= kMost && e[n] > kFar);
+    if (__any(rare)) {
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        // new references; a row goes by its own maxima: what the tile's other rows hold does not change its bits
-        const float rm = row_max(m[n]), rw = row_max(m[n] + lv);
-        const bool moves = rm > top[n] + kSlack || rw > ref[n] + kSlack;
+        // new references; a row goes by its own sums: what the tile's other rows hold does not change its bits
+        const float m = block_max(score[n]) * ks, rm = row_max(m), rw = row_max(m + lv);
+        const bool moves = row_max(fmaxf(part[n], more[n])) > kMost;
         const float top1 = moves ? fmaxf(top[n], rm) : top[n], ref1 = moves ? fmaxf(ref[n], rw) : ref[n];
         if (__any(moves && top[n] > kNone)) {      // (where a row had seen nothing, sum and acc are 0)
           sum[n] *= exp2_fast(top[n] - top1);
@@ -125,43 +118,60 @@ struct Rows {
         }
         top[n] = top1;
         ref[n] = ref1;
-        start[n] = lv - ref1;
-        e[n] = lv + (top1 - ref1);
         // Scales so far apart (or 0) that a weight vanishes where its part of the sum does not: that part by itself.
-        if (__any(!(e[n] > kFar))) {
+        const bool far = !(lv + (top1 - ref1) > kFar);
+        if (__any(far)) {
           float s = 0.0f;
           const float at = top1 > kNone ? top1 : 0.0f;
 #pragma unroll
           for (int k = 0; k < 16; ++k) s += exp2_fast(fmaf(score[n][k >> 2][k & 3], ks, -at));
-          sum[n] += e[n] > kFar ? 0.0f : s;
+          sum[n] += far ? s : 0.0f;
         }
       }
+      weigh(score, ks, lv, weight, part, more, e);
     }
-    float p[NQ][16];
 #pragma unroll
-    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-      for (int k = 0; k < 16; ++k) p[n][k] = exp2_fast(fmaf(score[n][k >> 2][k & 3], ks, start[n]));
+    for (int n = 0; n < NQ; ++n) sum[n] += e[n] > kFar ? more[n] : 0.0f;
+  }
+
+  static __device__ __forceinline__ float block_max(const f32x4 (&x)[4]) {
+    const auto four = [](const f32x4& v) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); };
+    return fmaxf(fmaxf(four(x[0]), four(x[1])), fmaxf(four(x[2]), four(x[3])));
+  }
+
+  // Weights 2^(x + lv - ref), their sum over the lane's positions, that of 2^(x - top), and e = log2 of the first's unit to the second's.
+  __device__ __forceinline__ void weigh(const f32x4 (&score)[NQ][4], float ks, float lv, f16x8 (&weight)[NQ][2], float (&part)[NQ], float (&more)[NQ],
+                                        float (&e)[NQ]) const {
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      const float* v = p[n];
-      const float s = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7])) + (((v[8] + v[9]) + (v[10] + v[11])) + ((v[12] + v[13]) + (v[14] + v[15])));
-      sum[n] = fmaf(s, e[n] > kFar ? exp2_fast(-e[n]) : 0.0f, sum[n]);
-    }
+      const float start = lv - ref[n];
+      e[n] = lv + (top[n] - ref[n]);
+      float four[4];
 #pragma unroll
-    for (int n = 0; n < NQ; ++n)
+      for (int i = 0; i < 4; ++i) {
+        float p[4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        f16x8 w;
+        for (int r = 0; r < 4; ++r) p[r] = exp2_fast(fmaf(score[n][i][r], ks, start));
+        four[i] = (p[0] + p[1]) + (p[2] + p[3]);
+        u32x4 w = __builtin_bit_cast(u32x4, weight[n][i >> 1]);
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const f32x2 two = {p[n][8 * u + j], p[n][8 * u + j + 1]};
-          const f16x2 h = __builtin_convertvector(two, f16x2);
-          w[j] = h[0];
-          w[j + 1] = h[1];
+        for (int r = 0; r < 4; r += 2) {
+          const f32x2 two = {p[r], p[r + 1]};
+          w[2 * (i & 1) + r / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, f16x2));
         }
-        weight[n][u] = w;
+        weight[n][i >> 1] = __builtin_bit_cast(f16x8, w);
       }
+      part[n] = (four[0] + four[1]) + (four[2] + four[3]);
+      more[n] = part[n] * exp2_fast(-e[n]);
+    }
+    // (here, not behind the branch that may make them again)
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      u32x4 u = __builtin_bit_cast(u32x4, weight[n][0]), v = __builtin_bit_cast(u32x4, weight[n][1]);
+      asm volatile("" : "+v"(u), "+v"(v));
+      weight[n][0] = __builtin_bit_cast(f16x8, u);
+      weight[n][1] = __builtin_bit_cast(f16x8, v);
+    }
   }
 
   // What turns acc into sum 2^(x - top) * value.

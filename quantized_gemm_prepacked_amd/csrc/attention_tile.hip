@@ -253,9 +253,12 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_tile_
 }
 
 // Eight waves, 32 rows each, two on a SIMD: waves 0-3 and 4-7 half a turn apart, so that one wave of a SIMD multiplies (values of block
-// k - 1, keys of block k) while the other has its exponentials, maxima and conversions. A barrier ends each half. Every wave
-// converts its share of the keys of k + 2 and the values of k + 1 in the second half of its turn k: they are complete before
-// the first reader's turn, and with three LDS buffers the one they go to was left by its last reader a half turn before.
+// k - 1, keys of block k) while the other has its maxima and exponentials. A barrier ends each half. Between its matrix instructions
+// every wave converts its share of the keys of k + 1 and the values of k, and asks for the next: a half turn before their first
+// reader's turn, into the one of two LDS buffers that its last reader left a half turn before.
+// The multiplying wave goes first where both could issue (895 us for 1024 x 8 rows on 30000, 937 without). What bounds it is the
+// vector instructions' port: 150 a wave and block for the softmax, 90 for conversions and addresses; without its products that
+// call takes 653 us, without all but its products 618.
 // Head size 128 alone: larger ones leave no room for two waves on a SIMD, at 64 three workgroups of the kernel above do better
 // (2048 rows of 8 heads on 30000: 1443 us, 1632 here).
 template <int FMT>
@@ -263,8 +266,9 @@ __global__ __launch_bounds__(512, 2) void attention_paired_kernel(KvCall c) {
   constexpr int D = 128;
   constexpr int kSteps = D / 32, kTiles = D / 16, kRows = 8 * 16 * kNQ;
   constexpr int kKeys = kBlock * D * 2, kValues = D * kBlock * 2;
-  constexpr int kChunks = D / 64;                                       // 16-byte chunks of bf16 keys a thread stages
-  __shared__ __attribute__((aligned(16))) uint8_t lds[3 * (kKeys + kValues)];
+  constexpr int kProducts = 2 * kTiles + 4 * kSteps;
+  constexpr int kChunks = 2;                                            // 16-byte chunks of bf16 keys a thread stages
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * (kKeys + kValues)];
   const Place place = place_of(c, kRows);
   const int head = place.head, b = place.b, part = place.part, r0 = place.r0;
   const KvSeq sq = attention_sequence(c, b);
@@ -292,8 +296,10 @@ __global__ __launch_bounds__(512, 2) void attention_paired_kernel(KvCall c) {
   // waited for at the next barrier, with the LDS writes.
   int zero;
   asm volatile("v_mov_b32 %0, 0" : "=v"(zero));
-  const auto page_of = [&](int position) { return table[(min(position, most) + zero) >> shift]; };
-  const uint32_t key_offset = unsigned(((head << shift) + (key & 15)) * D + eighth * (D / 8));
+  const auto page_of = [&](int position) {
+    return *reinterpret_cast<const int32_t*>(reinterpret_cast<const uint8_t*>(table) + ((unsigned(min(position, most) + zero) >> shift) << 2));
+  };
+  uint32_t key_offset = unsigned(((head << shift) + (key & 15)) * D + eighth * (D / 8));
   const uint8_t* const vp = static_cast<const uint8_t*>(c.v_pages) + ((int64_t(head) * D + (tid >> 2)) << shift);
   const auto load_keys = [&](int blk) {
     const uint32_t from = __builtin_amdgcn_readfirstlane(kpage);
@@ -310,21 +316,18 @@ __global__ __launch_bounds__(512, 2) void attention_paired_kernel(KvCall c) {
   };
   const auto load_scales = [&](int blk) {
     there = blk * kBlock + 16 * quarter <= most && unsigned(spage) < unsigned(c.num_pages);
-    const uint64_t at = uint64_t(there ? spage : 0) * unsigned(c.H) + unsigned(head);
-    ks = c.k_scales[at];
-    vs = c.v_scales[at];
+    const uint32_t at = (unsigned(there ? spage : 0) * unsigned(c.H) + unsigned(head)) << 2;     // (below 2^32: a page's codes are at least 1024 a head)
+    ks = *reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(c.k_scales) + at);
+    vs = *reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(c.v_scales) + at);
   };
-  const auto store_keys = [&](uint8_t* to) {
-#pragma unroll
-    for (int s = 0; s < kChunks; ++s) {
-      const int chunk = eighth * kChunks + s;
-      *reinterpret_cast<bf16x8*>(to + key_at<D>(key_row, chunk / kSteps, chunk % kSteps)) = codes_bf16<FMT>(kc[s].x, kc[s].y);
-    }
+  // Places in LDS, of the buffers in turn: two of keys, then two of values. Chunk s of a key row, half u of a channel is at ^ 16 s.
+  uint32_t k_read = key_at<D>(col, quarter, 0), k_write = key_at<D>(key_row, eighth / 2, eighth % 2 * kChunks);
+  uint32_t v_read = 2 * kKeys + value_at(col, quarter, 0), v_write = 2 * kKeys + value_at(tid >> 2, piece, 0);
+  const auto store_keys = [&](int s) {
+    *reinterpret_cast<bf16x8*>(lds + (k_write ^ (16u * s))) = codes_bf16<FMT>(kc[s].x, kc[s].y);
   };
-  const auto store_values = [&](uint8_t* to) {
-    if (__any(live < 16)) vc = live_codes(vc, live);
-    *reinterpret_cast<f16x8*>(to + value_at(tid >> 2, piece, 0)) = codes_f16<FMT>(vc[0], vc[1]);
-    *reinterpret_cast<f16x8*>(to + value_at(tid >> 2, piece, 1)) = codes_f16<FMT>(vc[2], vc[3]);
+  const auto store_values = [&](int u) {
+    *reinterpret_cast<f16x8*>(lds + (v_write ^ (16u * u))) = codes_f16<FMT>(vc[2 * u], vc[2 * u + 1]);
   };
 
   bf16x8 qf[kNQ][kSteps];
@@ -341,91 +344,111 @@ __global__ __launch_bounds__(512, 2) void attention_paired_kernel(KvCall c) {
   }
   const int pos_first = before + w0 / c.G;
   const int pos_last = w0 < rows ? before + (min(w0 + 16 * kNQ, rows) - 1) / c.G : -1;
-  // whether one of the wave's rows sees a block
-  const auto sees = [&](int blk) { return blk * kBlock <= pos_last && (c.window == 0 || blk * kBlock + kBlock - 1 > pos_first - c.window); };
 
   Rows<kNQ, kTiles> st;
   st.clear();
   if (first < end) {
-    uint8_t* const values = lds + 3 * kKeys;
     kpage = page_of(first * kBlock + 16 * (wave >> 1));
     vpage = page_of(first * kBlock + 16 * piece);
     spage = page_of(first * kBlock + 16 * quarter);
     load_keys(first);
     load_values(first);
-    load_scales(first);
     kpage = page_of((first + 1) * kBlock + 16 * (wave >> 1));
     vpage = page_of((first + 1) * kBlock + 16 * piece);
-    spage = page_of((first + 1) * kBlock + 16 * quarter);
-    store_keys(lds);
-    store_values(values);
+    store_keys(0);
+    store_keys(1);
+    k_write ^= kKeys;
+    v_read ^= kValues;
     load_keys(first + 1);
     kpage = page_of((first + 2) * kBlock + 16 * (wave >> 1));
-    load_values(first + 1);
-    vpage = page_of((first + 2) * kBlock + 16 * piece);
-    store_keys(lds + kKeys);
-    load_keys(first + 2);
-    kpage = page_of((first + 3) * kBlock + 16 * (wave >> 1));
+    f32x4 score[kNQ][4];
+    f16x8 weight[kNQ][2] = {};          // of block k - 1; none before the first, whose place in LDS holds zeros
+    *reinterpret_cast<u32x4*>(lds + (v_write ^ kValues)) = u32x4{0, 0, 0, 0};
+    *reinterpret_cast<u32x4*>(lds + (v_write ^ kValues ^ 16u)) = u32x4{0, 0, 0, 0};
     lds_barrier();
     if (wave >= 4) lds_barrier();
-    f32x4 score[kNQ][4];
-    f16x8 weight[kNQ][2];
-    bool seen = false;                  // block k - 1, whose weights the wave has
-    int at = 0, next = 2;               // buffers of keys k and k + 2; block j's keys and values are in buffers j mod 3, k - 1 and k + 2 in the same
     for (int blk = first; blk <= end; ++blk) {
-      if (seen) {
-        const uint8_t* v = values + next * kValues;
+      // The turn's products in 32 steps, a 16-byte piece of LDS and two matrix instructions each: values of k - 1, then keys of k.
+      const auto read = [&](int j) {
+        return *reinterpret_cast<const u32x4*>(j < kProducts / 2 ? lds + (v_read ^ (16u * (j / kTiles))) + 16 * (j % kTiles) * 128
+                                                                 : lds + (k_read ^ (16u * ((j - kProducts / 2) / 4))) + 16 * (j % 4) * D * 2);
+      };
+      const auto multiply = [&](int j, u32x4 x) {
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const f16x8 vf = *reinterpret_cast<const f16x8*>(v + value_at(16 * t + col, quarter, u));
-#pragma unroll
-            for (int n = 0; n < kNQ; ++n) st.acc[n][t] = mfma_f16(vf, weight[n][u], st.acc[n][t]);
-          }
-        reads_ahead<2 * kTiles>();
-      }
-      seen = blk < end && sees(blk);
-      if (seen) {
-        const uint8_t* k = lds + at * kKeys;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-          for (int n = 0; n < kNQ; ++n) score[n][i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-          for (int s = 0; s < kSteps; ++s) {
-            const bf16x8 kf = *reinterpret_cast<const bf16x8*>(k + key_at<D>(16 * i + col, quarter, s));
-#pragma unroll
-            for (int n = 0; n < kNQ; ++n) score[n][i] = mfma_bf16(kf, qf[n][s], score[n][i]);
+        for (int n = 0; n < kNQ; ++n) {
+          if (j < kProducts / 2) {
+            st.acc[n][j % kTiles] = mfma_f16(__builtin_bit_cast(f16x8, x), weight[n][j / kTiles], st.acc[n][j % kTiles]);
+          } else {
+            const int i = j % 4, s = (j - kProducts / 2) / 4;
+            score[n][i] = mfma_bf16(__builtin_bit_cast(bf16x8, x), qf[n][s], s ? score[n][i] : f32x4{0, 0, 0, 0});
           }
         }
-        reads_ahead<4 * kSteps>();
+      };
+      // The wave's share of the staging, in pieces to go between (past the range's end too, where nothing reads what is stored).
+      const auto stage = [&](int piece_of_work) {
+        switch (piece_of_work) {
+          case 0:
+            load_scales(blk);
+            spage = page_of((blk + 1) * kBlock + 16 * quarter);
+            break;
+          case 1: store_keys(0); break;
+          case 2: store_keys(1); break;
+          case 3:
+            load_keys(blk + 2);
+            kpage = page_of((blk + 3) * kBlock + 16 * (wave >> 1));
+            break;
+          case 4: store_values(0); break;
+          case 5: store_values(1); break;
+          case 6:
+            load_values(blk + 1);
+            vpage = page_of((blk + 2) * kBlock + 16 * piece);
+            break;
+        }
+      };
+      asm volatile("" : "+v"(key_offset));      // (an offset to a scalar address, not widened ahead of the loop)
+      if (__any(live < 16)) vc = live_codes(vc, live);
+      __builtin_amdgcn_s_setprio(1);
+      // four steps at a time, the next four's pieces asked for before, the staging's vector instructions between
+      u32x4 x[4], y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = read(j);
+#pragma unroll
+      for (int r = 0; r < kProducts / 4; ++r) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (r + 1 < kProducts / 4) y[j] = read(4 * r + 4 + j);
+        if (r != 3 && r != 6) stage(r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) multiply(4 * r + j, x[j]);
+        if (r + 1 < kProducts / 4) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+        for (int j = 0; j < 4 * kNQ; ++j) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = y[j];
       }
+      __builtin_amdgcn_s_setprio(0);
       lds_barrier();
+      stage(3);
+      stage(6);
       if (blk < end) {
         const int base = blk * kBlock;
-        store_keys(lds + next * kKeys);
-        store_values(values + (at == 2 ? 0 : at + 1) * kValues);
-        load_keys(blk + 3);
-        load_values(blk + 2);
-        kpage = page_of((blk + 4) * kBlock + 16 * (wave >> 1));
-        vpage = page_of((blk + 3) * kBlock + 16 * piece);
-        if (seen) {
-          float f = ks * c.scale_log2;
-          const float lv = there ? log2f(vs) : -INFINITY;
-          if (base + kBlock - 1 > pos_first || (c.window > 0 && base <= pos_last - c.window) || __any(!there)) {
-            mask_scores<kNQ>(score, pos, base + 16 * quarter, c.window, there, f);
-            f = 1.0f;
-          }
-          st.step(score, f, lv, weight);
+        float f = ks * c.scale_log2;
+        const float lv = there ? log2f(vs) : -INFINITY;
+        if (base + kBlock - 1 > pos_first || (c.window > 0 && base <= pos_last - c.window) || __any(!there)) {
+          mask_scores<kNQ>(score, pos, base + 16 * quarter, c.window, there, f);
+          f = 1.0f;
         }
-        // (after the last use of this block's: into the same registers, without a copy that would wait for them)
-        load_scales(blk + 1);
-        spage = page_of((blk + 2) * kBlock + 16 * quarter);
+        st.step(score, f, lv, weight);
       }
       lds_barrier();
-      at = at == 2 ? 0 : at + 1;
-      next = next == 2 ? 0 : next + 1;
+      k_read ^= kKeys;
+      k_write ^= kKeys;
+      v_read ^= kValues;
+      v_write ^= kValues;
     }
     if (wave < 4) lds_barrier();
   }

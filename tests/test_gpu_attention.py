@@ -216,6 +216,18 @@ def test_many_rows_of_one_long_sequence(fmt, H, G, P, new, length, window):
 
 
 @pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("H,G,P,window", [(1, 4, 16, 0), (2, 8, 128, 0), (1, 16, 64, 70), (2, 3, 32, 500)])
+def test_many_rows_of_several_sequences(fmt, H, G, P, window):
+    """Long pieces of several sequences in one call, at both ends of their lengths, with single tokens, an empty sequence and one
+    that the arrays make impossible among them."""
+    g = np.random.default_rng([H, G, P, window])
+    new, lens = [300, 1, 190, 0, 257, 333, 40], [700, 900, 190, 5, 260, 1500, 1100]
+    c = kv_case(g, fmt, H, 128, P, new, lens, peaky=0.6, behind=3)
+    c["lens"][6] = c["table"].shape[1] * P + 1
+    _check(c, normal_rows(g, c["T"], H * G, 128), window=window, max_kv=4096, what=f"{fmt} H={H} G={G} P={P} window={window}")
+
+
+@pytest.mark.parametrize("fmt", list(KV))
 @pytest.mark.parametrize("new", [1, 4, 40])
 def test_rows_that_see_nothing(fmt, new):
     """Empty sequences, more queries than positions, no page left, pages freed in the middle: rows without a token are zeros, the
