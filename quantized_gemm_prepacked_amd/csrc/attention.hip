@@ -28,7 +28,7 @@ constexpr int kTileRows = 128;   // rows of a workgroup of the tiled kernel, of 
 constexpr int kMaxSplit = 128;
 
 template <int D, int FMT, int NQ>
-__global__ __launch_bounds__(kWaves * 64) void attention_kernel(KvCall c) {
+__global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kernel(KvCall c) {
   constexpr int kSteps = D / 32;      // matrix instructions of a dot product
   constexpr int kTiles = D / 16;      // 16-channel tiles of the output
   const int b = blockIdx.y;
@@ -88,15 +88,12 @@ __global__ __launch_bounds__(kWaves * 64) void attention_kernel(KvCall c) {
 
   // this lane's rows, one of each 16: query fragments and the last position seen
   bf16x8 qf[NQ][kSteps];
+  load_queries(c, sq, head, r0, rows, qf);
   int pos[NQ];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const int r = r0 + 16 * n + col;
-    const int i = r / c.G, g = r - i * c.G;
-    pos[n] = r < rows ? before + i : -1;
-    const auto* qp = static_cast<const uint16_t*>(c.q) + (int64_t(sq.first) + i) * c.q_stride + int64_t(head * c.G + g) * D + quarter * (D / 4);
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) qf[n][s] = r < rows ? query8(qp + 8 * s, c.q_sign) : bf16x8{};
+    pos[n] = r < rows ? before + r / c.G : -1;
   }
   const int pos_first = before + r0 / c.G, pos_last = before + (min(r0 + 16 * NQ, rows) - 1) / c.G;
 
@@ -144,6 +141,7 @@ __global__ __launch_bounds__(kWaves * 64) void attention_kernel(KvCall c) {
     load_values(blk, x);
     load_pages(blk + kWaves);
   }
+  sign_queries(c, qf);
   // the next block's keys into the registers of this one's as soon as they are used up, and so its values
   for (; blk < end; blk += kWaves) {
     turn(blk, x, [&] {

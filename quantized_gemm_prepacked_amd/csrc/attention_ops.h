@@ -234,12 +234,31 @@ __device__ __forceinline__ KvSeq attention_sequence(const KvCall& c, int b) {
   return q;
 }
 
-// 16-byte piece of a query row, negated where sm_scale is negative (its size alone is a factor of the keys' scale).
-__device__ __forceinline__ bf16x8 query8(const void* p, uint32_t sign) {
-  u32x4 v = ldg16(p);
+// A lane's part of its query rows, r0 + 16 n + l % 16: a quarter of the channels each. Rows past the last one hold that one, so that
+// the loads are in flight together, not each in a branch of its own; nothing of them is written.
+template <int NQ, int STEPS>
+__device__ __forceinline__ void load_queries(const KvCall& c, const KvSeq& sq, int head, int r0, int rows, bf16x8 (&q)[NQ][STEPS]) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] ^= sign;
-  return __builtin_bit_cast(bf16x8, v);
+  for (int n = 0; n < NQ; ++n) {
+    const int r = min(r0 + 16 * n + (lane & 15), rows - 1), i = r / c.G, g = r - i * c.G;
+    const auto* p = static_cast<const uint16_t*>(c.q) + (int64_t(sq.first) + i) * c.q_stride + int64_t(head * c.G + g) * (32 * STEPS) + (lane >> 4) * (8 * STEPS);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) q[n][s] = __builtin_bit_cast(bf16x8, ldg16(p + 8 * s));
+  }
+}
+// Negated where sm_scale is negative (its size alone is a factor of the keys' scale).
+template <int NQ, int STEPS>
+__device__ __forceinline__ void sign_queries(const KvCall& c, bf16x8 (&q)[NQ][STEPS]) {
+#pragma unroll
+  for (int n = 0; n < NQ; ++n)
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      u32x4 x = __builtin_bit_cast(u32x4, q[n][s]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] ^= c.q_sign;
+      q[n][s] = __builtin_bit_cast(bf16x8, x);
+    }
 }
 
 }  // namespace hq

@@ -178,6 +178,9 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_tile_
     kpage = page_of(at * kBlock + 16 * wave);
     vpage = page_of(at * kBlock + 16 * piece);
   };
+  const int w0 = r0 + wave * 16 * kNQ;      // the wave's first row
+  bf16x8 qf[kNQ][kSteps];
+  load_queries(c, sq, head, w0, rows, qf);
   if (blk < end) {
     load_code_pages(blk);
     spage = page_of(blk * kBlock + 16 * quarter);
@@ -187,20 +190,16 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_tile_
     spage = page_of((blk + 1) * kBlock + 16 * quarter);
   }
 
-  bf16x8 qf[kNQ][kSteps];
   int pos[kNQ];
-  const int w0 = r0 + wave * 16 * kNQ;      // the wave's first row
 #pragma unroll
   for (int n = 0; n < kNQ; ++n) {
     const int r = w0 + 16 * n + col;
-    const int i = r / c.G, g = r - i * c.G;
-    pos[n] = r < rows ? before + i : -1;
-    const auto* qp = static_cast<const uint16_t*>(c.q) + (int64_t(sq.first) + i) * c.q_stride + int64_t(head * c.G + g) * D + quarter * (D / 4);
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) qf[n][s] = r < rows ? query8(qp + 8 * s, c.q_sign) : bf16x8{};
+    pos[n] = r < rows ? before + r / c.G : -1;
   }
   const int pos_first = before + w0 / c.G;
   const int pos_last = w0 < rows ? before + (min(w0 + 16 * kNQ, rows) - 1) / c.G : -1;
+
+  sign_queries(c, qf);
 
   Rows<kNQ, kTiles> st;
   st.clear();
@@ -330,17 +329,14 @@ __global__ __launch_bounds__(512, 2) void attention_paired_kernel(KvCall c) {
     *reinterpret_cast<f16x8*>(lds + (v_write ^ (16u * u))) = codes_f16<FMT>(vc[2 * u], vc[2 * u + 1]);
   };
 
-  bf16x8 qf[kNQ][kSteps];
-  int pos[kNQ];
   const int w0 = r0 + wave * 16 * kNQ;      // the wave's first row
+  bf16x8 qf[kNQ][kSteps];
+  load_queries(c, sq, head, w0, rows, qf);
+  int pos[kNQ];
 #pragma unroll
   for (int n = 0; n < kNQ; ++n) {
     const int r = w0 + 16 * n + col;
-    const int i = r / c.G, g = r - i * c.G;
-    pos[n] = r < rows ? before + i : -1;
-    const auto* qp = static_cast<const uint16_t*>(c.q) + (int64_t(sq.first) + i) * c.q_stride + int64_t(head * c.G + g) * D + quarter * (D / 4);
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) qf[n][s] = r < rows ? query8(qp + 8 * s, c.q_sign) : bf16x8{};
+    pos[n] = r < rows ? before + r / c.G : -1;
   }
   const int pos_first = before + w0 / c.G;
   const int pos_last = w0 < rows ? before + (min(w0 + 16 * kNQ, rows) - 1) / c.G : -1;
@@ -365,6 +361,7 @@ __global__ __launch_bounds__(512, 2) void attention_paired_kernel(KvCall c) {
     f16x8 weight[kNQ][2] = {};          // of block k - 1; none before the first, whose place in LDS holds zeros
     *reinterpret_cast<u32x4*>(lds + (v_write ^ kValues)) = u32x4{0, 0, 0, 0};
     *reinterpret_cast<u32x4*>(lds + (v_write ^ kValues ^ 16u)) = u32x4{0, 0, 0, 0};
+    sign_queries(c, qf);
     lds_barrier();
     if (wave >= 4) lds_barrier();
     for (int blk = first; blk <= end; ++blk) {
