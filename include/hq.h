@@ -528,8 +528,8 @@ hq_status hq_moe_decode(const hq_quant_desc* desc, int64_t T, int32_t topk, int3
  *   other act_fmt y, y_scale = the codes and scales of v by the rule of hq_quantize_activations for
  *                 that format, in its layouts (the GEMM's `a` and `a_scale`), but fp32 scales are the
  *                 product fp32( max|v| * fp32(1 / Q) ), at most a unit in the last place off that
- *                 call's quotient; v is not rounded to bf16 on the way. y_bf16, if not NULL, receives bf16(v) as well (the router of an MoE
- *                 block reads it, where the experts read the codes).
+ *                 call's quotient; v is not rounded to bf16 on the way. y_bf16, if not NULL, receives
+ *                 bf16(v) as well (the router of an MoE block reads it, where the experts read the codes).
  * Since the sum is in binary64 a row's result does not depend on how the row is split over threads.
  * act_fmt       HQ_ACT_BF16, HQ_ACT_INT8_PER_TOKEN, HQ_ACT_FP8E4M3_PER_TOKEN,
  *               HQ_ACT_FP8E4M3_BLOCK128 (K % 128 == 0), HQ_ACT_MXFP8, HQ_ACT_MXFP4 (K % 32 == 0)
@@ -611,14 +611,16 @@ hq_status hq_kv_append(const hq_kv_desc* desc, int32_t B, int64_t T, int32_t max
  *   out[t, i] = bf16( sum_j p_j v_j / sum_j p_j ),  p_j = exp( sm_scale * q[t, i] . k_j ),
  * over the positions j <= pos(t) of t's sequence, with window > 0 only j > pos(t) - window. A row
  * that sees no token gets zeros. fp32 accumulation and statistics; p_j * scale (of v_j) enters the product
- * with the codes as an fp16, relative to the row's largest. Scales are not negative (hq_kv_append makes none). NaN in a query's row reaches that row alone; a NaN key the rows that see it.
+ * with the codes as an fp16, relative to the row's largest. Scales are not negative (hq_kv_append makes
+ * none). NaN in a query's row reaches that row alone, a NaN key the rows that see it; a NaN code among the
+ * values (hq_kv_append makes none) any row of its sequence.
  *   q        bf16, token rows q_stride elements apart (>= Hq * D, a multiple of 8), 16-byte aligned, T rows
  *   out      bf16 [T, Hq, D], 16-byte aligned; may be q where q_stride = Hq * D
  *   max_q    at least the largest number of query tokens of a sequence
  *   max_kv   about the largest kv_lens of the call, table_width * P where it is not known (graphs that
  *            are replayed as the sequences grow): it sets how many workgroups share a sequence, never what
  *            is computed. Results differ in their last bits with it.
- *   sm_scale finite; window 0 (none) or the number of positions seen, the token's own included
+ *   sm_scale finite (below 2.3e38); window 0 (none) or the number of positions seen, the token's own included
  *   ws       hq_attention_workspace_bytes(...) bytes (may be 0 / NULL), 16-byte aligned, contents irrelevant on
  *            entry. Calls that may run at the same time each need their own.
  * Hq a multiple of num_kv_heads, at most 128 times it. B == 0, T == 0 or max_q == 0 is a no-op.

@@ -1,11 +1,13 @@
 // attention_tile.hip -- attention over the paged 8-bit cache for many rows: prompts, pieces of prompts, many query heads to a
 // head of the cache.
 //
-// What bounds it is arithmetic: two products of 4 D operations a (row, position), 2^x, maxima and conversions beside them. A
+// What bounds it is arithmetic: two products of 2 D operations each a (row, position), 2^x, sums and conversions beside them. A
 // workgroup takes 128 rows of one head of the cache of one sequence, 32 for each of its four waves, and all waves walk
 // the same blocks of 64 positions. A block's codes are asked for from memory while the block before is worked on, converted
 // once by the whole workgroup (keys to bf16, values to fp16), and handed to the waves through two LDS buffers in turn, so
-// that there is one barrier a block. Products, lane layout and softmax are those of the few-row kernel.
+// that there is one barrier a block. Products, lane layout and softmax are those of the few-row kernel. Measured, with the kernel of
+// 256 rows below where it serves: 4 prompts of 4500, 32 heads on 8 of 128, e4m3: 476 us, 925 TFLOP/s; 1024 tokens, 64 heads
+// on 8, INT8, on 30000 positions: 871 us, 1.18 PFLOP/s (a bf16 matrix product of 8192 reaches 1.44, of 16384 1.62).
 //
 // Bank conflicts: gfx950 serves a 16-byte LDS read of a wave 16 lanes at a time, eight of one lane group and the other
 // eight of the next (lanes 0-3, 12-15 and 20-27; 4-11, 16-19 and 28-31; and so the upper half). Rows are stored with

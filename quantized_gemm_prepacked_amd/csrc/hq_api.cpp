@@ -845,19 +845,20 @@ hq_status hq_attention(const hq_kv_desc* desc, int32_t B, int64_t T, int32_t Hq,
   if (s != HQ_OK) return s;
   if (q_stride < int64_t(Hq) * c.D || q_stride > kMaxDim || q_stride % 8 != 0)
     return fail(HQ_ERR_INVALID_ARGUMENT, "q_stride=%lld: at least Hq * head_dim, a multiple of 8", (long long)q_stride);
-  if (!std::isfinite(sm_scale)) return fail(HQ_ERR_INVALID_ARGUMENT, "sm_scale must be finite");
+  c.scale_log2 = float(std::fabs(double(sm_scale)) * 1.4426950408889634);
+  if (!std::isfinite(c.scale_log2)) return fail(HQ_ERR_INVALID_ARGUMENT, "sm_scale must be finite, in units of log 2 too");
   if (window < 0) return fail(HQ_ERR_INVALID_ARGUMENT, "window=%d must not be negative", window);
   if (B == 0 || T == 0 || max_q == 0) return ok();
   if ((s = check_cache(cu, kv_lens, page_table, table_width, k_pages, v_pages, k_scales, v_scales, &c)) != HQ_OK) return s;
   if (!q || !out) return fail(HQ_ERR_INVALID_ARGUMENT, "q and out must be non-NULL");
   if (!aligned16(q) || !aligned16(out) || !aligned16(ws)) return fail(HQ_ERR_INVALID_ARGUMENT, "q, out and ws must be 16-byte aligned");
   if (out == q && q_stride != int64_t(Hq) * c.D) return fail(HQ_ERR_INVALID_ARGUMENT, "out may be q only where q_stride is Hq * head_dim");
-  c.window = window;   // with one the plan never has more parts than without, which is what the workspace is sized for
+  // (positions stay below 2^30, and differences to the window in 32 bits; with a window the plan never needs more room than without)
+  c.window = std::min(window, 1 << 30);
   const hq::AttentionPlan p = hq::plan_attention(c, max_kv);
   if (ws_bytes < p.ws_bytes || (p.ws_bytes && !ws)) return fail(HQ_ERR_WORKSPACE, "workspace %zu < required %zu", ws ? ws_bytes : size_t(0), p.ws_bytes);
   c.q = q;
   c.q_stride = q_stride;
-  c.scale_log2 = float(std::fabs(double(sm_scale)) * 1.4426950408889634);
   c.q_sign = sm_scale < 0.0f ? 0x80008000u : 0u;
   c.out = out;
   return check_hip(hq::launch_attention(c, p, static_cast<uint8_t*>(ws), static_cast<hipStream_t>(stream)), "hq_attention launch");

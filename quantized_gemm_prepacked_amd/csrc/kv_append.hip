@@ -3,6 +3,10 @@
 // One workgroup (one wave where there are only a few new tokens) takes one touched page of one sequence, one head, K or V: the largest
 // magnitude of the page's new tokens, the page's scale (a new one, or the held one times a power of two), the codes of the
 // new tokens, and where the scale grew the codes that were there. Nothing is shared between workgroups.
+//
+// What bounds it is the traffic, each new value read once and each code written once: 5 prompts of up to 4000 tokens (INT8, 8
+// heads of 128, 108 MB) take 25 us, 4.3 TB/s; one token of each of 48 sequences 4.8 us, a launch and the dependent
+// reads of lengths, page, scale and tokens.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

@@ -215,6 +215,22 @@ def test_many_rows_of_one_long_sequence(fmt, H, G, P, new, length, window):
     _check(c, normal_rows(g, c["T"], H * G, 128), window=window, max_kv=4096, what=f"{fmt} H={H} G={G} P={P} {new} on {length}")
 
 
+@pytest.mark.parametrize("H,G,D,max_kv", [(2, 1, 64, None), (1, 8, 128, 4096)])
+def test_widest_window(H, G, D, max_kv):
+    """The largest window there is, with more new tokens than positions: differences of the two leave 32 bits."""
+    g = np.random.default_rng(23)
+    c = kv_case(g, "fp8", H, D, 16, [4, 200, 40, 300], [2, 90, 40, 200], peaky=0.6)
+    _check(c, normal_rows(g, c["T"], H * G, D), window=2 ** 31 - 1, max_kv=max_kv, what=f"widest window D={D}")
+
+
+@pytest.mark.parametrize("window", [0, 1024])
+def test_workspace_does_not_ask_for_the_window(window):
+    """43 heads of 300 rows that are told of 4096 positions: more parts with the window's small tiles than without it."""
+    g = np.random.default_rng(22)
+    c = kv_case(g, "int8", 43, 128, 64, [300], [1500], peaky=0.6)
+    _check(c, normal_rows(g, c["T"], 43, 128), window=window, max_kv=4096, what=f"window={window}")
+
+
 @pytest.mark.parametrize("fmt", list(KV))
 @pytest.mark.parametrize("H,G,P,window", [(1, 4, 16, 0), (2, 8, 128, 0), (1, 16, 64, 70), (2, 3, 32, 500)])
 def test_many_rows_of_several_sequences(fmt, H, G, P, window):

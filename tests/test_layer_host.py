@@ -222,7 +222,7 @@ def test_append_refusals(change, status):
 
 @pytest.mark.parametrize("change,status", DESCS + ARRAYS + SEQUENCES + [
     (dict(Hq=0), INV), (dict(Hq=12), INV), (dict(Hq=1032), INV), (dict(max_kv=-1), INV), (dict(max_kv=(1 << 30) + 1), INV), (dict(stride=2040), INV),
-    (dict(stride=2052), INV), (dict(scale=math.nan), INV), (dict(scale=math.inf), INV), (dict(window=-1), INV), (dict(q=None), INV), (dict(out=None), INV),
+    (dict(stride=2052), INV), (dict(scale=math.nan), INV), (dict(scale=math.inf), INV), (dict(scale=-3e38), INV), (dict(window=-1), INV), (dict(q=None), INV), (dict(out=None), INV),
     (dict(q=8), INV), (dict(out=8), INV), (dict(ws=8), INV), (dict(ws=None), WSP), (dict(short=1), WSP), (dict(B=65535, T=1 << 24, most=1 << 24), UNS),
     (dict(q=48, out=48, stride=4096), INV),
 ])
@@ -255,6 +255,21 @@ def test_sizes():
     assert need(d, 1, 1, 12, 1, 2000) == 0                                                          # refused
     # room for rows, not for sequences times the longest: a prompt among single tokens
     assert need(d, 8, 40, 16, 33, 4096) <= need(d, 8, 8 * 33, 16, 33, 4096)
+
+
+def test_workspace_grows_with_the_context():
+    """A window shortens what a call plans for, as a smaller max_kv does; its workspace is sized without the window."""
+    g = np.random.default_rng(21)
+    shapes = [(43, 1, 1, 300, 300), (64, 2, 1, 129, 129), (5, 8, 3, 700, 300), (86, 1, 1, 300, 257)]
+    shapes += [(int(g.integers(1, 90)), int(2 ** g.integers(0, 5)), int(g.integers(1, 6)), int(g.integers(1, 4000)), int(g.integers(1, 2000))) for _ in range(300)]
+    for H, G, B, T, most in shapes:
+        for D in (64, 128, 256):
+            d = hq.make_kv_desc(0, H, D, 64, 100)
+            last = 0
+            for max_kv in sorted((0, 64, 65, 500, 1000, 1344, 2047, 2048, 2500, 4096, 5000, 2 * most - 1, 2 * most, 20000, 100000, 1 << 20)):
+                n = hq.hq_attention_workspace_bytes(d, B, T, H * G, most, max_kv)
+                assert n >= last, (H, G, B, T, most, D, max_kv)
+                last = n
 
 
 def test_norm_buffers_are_checked():
