@@ -200,7 +200,7 @@ hipError_t go(const RmsNormCall& a, hipStream_t s) {
 // Threads a row. Few rows leave most of the chip idle, so a row's latency counts and more threads with less each are better;
 // with many rows the loads in flight count, and the idle threads behind the row's end. Measured with a residual, in us:
 //   K 2048, INT8:    64 threads 4.8 at 67 rows, 5.7 at 1024, 14.1 at 4099; 256 threads 3.4, 5.9, 16.4
-//   K 4096, INT8:    256 threads 4.2 at 67 rows, 22.3 at 4099; 512 threads 4.0, 29.5; 64 threads 7.0, 25.9
+//   K 4096, INT8:    256 threads 3.8 at 1 row, 4.5 at 256, 5.3 at 512, 22.3 at 4099; 512 threads 3.6, 4.4, 6.0, 29.5; 64 threads 6.3, 7.3, 7.7, 25.9
 //   K 8192, MXFP8:   256 threads 4.3 at 67 rows, 8.6 at 512, 22.1 at 2048, 47.2 at 4099; 512 threads 3.7, 8.3, 25.4, 52.8
 //   K 8192, INT8:    256 threads 5.5 at 67 rows, 9.8 at 512, 14.3 at 1024; 512 threads 4.7, 9.3, 14.5
 //   K 14336, INT8:   512 threads 6.1 at 67 rows, 82.2 at 4099; 1024 threads 5.9, 82.2; 256 threads 7.7, 84.8
@@ -210,7 +210,7 @@ hipError_t pick(const RmsNormCall& a, hipStream_t s) {
   if (a.K <= 512) return go<ACT, 64, 1>(a, s);
   if (a.K <= 1024) return go<ACT, 64, 2>(a, s);
   if (a.K <= 2048) return many ? go<ACT, 64, 4>(a, s) : go<ACT, 256, 1>(a, s);
-  if (a.K <= 4096) return go<ACT, 256, 2>(a, s);
+  if (a.K <= 4096) return a.M <= 256 ? go<ACT, 512, 1>(a, s) : go<ACT, 256, 2>(a, s);
   if (a.K <= 8192) {
     if (!many) return go<ACT, 512, 2>(a, s);
     return a.K <= 6144 ? go<ACT, 256, 3>(a, s) : go<ACT, 256, 4>(a, s);

@@ -82,7 +82,7 @@ def _check(fmt, x, r, w, eps=1e-6, both=False):
 
 SIZES = [(1, 128), (1, 4096), (3, 512), (5, 640), (4, 1024), (7, 1152), (9, 2048), (2, 2176), (6, 4096), (3, 5120), (2, 7168), (3, 8192), (2, 8320), (2, 16384),
          (2, 16512), (1, 32768), (2, 33024), (1, 65536), (130, 256),
-         (1024, 1152), (1027, 2048), (1025, 6144), (1024, 6272), (1023, 8192)]
+         (1024, 1152), (1027, 2048), (1025, 6144), (1024, 6272), (1023, 8192), (256, 2304), (257, 4096)]
 
 
 @pytest.mark.parametrize("fmt", list(NORM))
