@@ -318,15 +318,17 @@ AttentionPlan plan_attention(const KvCall& c, int64_t max_kv) {
     at = *ml + (size_t(slots) * c.Hq * n_split * 8 + 15) / 16 * 16;
   };
   if (p.few) {
-    // two workgroups a CU, one where its registers leave room for no more (D = 256). With more, the last ones run alone: one
-    // token on 131072 positions with 512 / 768 / 1024 / 2048 workgroups 56.7 / 60.8 / 65.1 / 65.1 us; 16 tokens on 30000
-    // 72.9 / 82.2 / 87.3 / 81.9; D = 256, 4 tokens on 20000 with 256 / 512 / 1024: 33.6 / 42.5 / 48.1.
     const int resident = c.D > 192 ? 256 : 512;      // two workgroups a CU, one where its registers leave room for no more
-    split_of(int64_t(c.B) * c.H, resident, kWaves, max_kv, &p.few_split, &p.few_each);
-    // More than 16 rows: in two workgroups, which both read the keys and values, while the card is not full of them (32 rows, us in
-    // one / in two: D = 128, 1 sequence of 2000 11.8 / 10.2, 2 of 8000 16.7 / 15.6, 16 of 2000 25.8 / 28.0; D = 256, 4 of 3000
-    // 19.2 / 14.8, 8 of 3000 23.1 / 27.9).
-    p.few_wide = p.few * c.G > 16 && int64_t(c.B) * c.H * p.few_split >= resident;
+    const int64_t heads = int64_t(c.B) * c.H;
+    // More than 16 rows: in two workgroups, which both read the keys and values, where these fit on the card at once and a part is
+    // short, so that what counts is latency (4 tokens and 8 heads, us in one / in two; D = 128: 8 sequences of 3000 22.0 / 20.9, 2 of 8000
+    // 17.2 / 16.3; D = 256: 1 of 20000 24.7 / 20.6, 7 x 5 tokens in a window of 1024 19.7 / 17.0); in one where a part is long
+    // (16 of 5000 38.5 / 46.9, 2 of 30000 29.2 / 33.6) or there are more of them (40 of 3000: 47.1 / 52.3, D = 256 53.4 / 73.5).
+    split_of(2 * heads, resident, kWaves, max_kv, &p.few_split, &p.few_each);
+    if (p.few * c.G <= 16 || 2 * heads > resident || p.few_each > 16) {
+      split_of(heads, resident, kWaves, max_kv, &p.few_split, &p.few_each);
+      p.few_wide = p.few * c.G > 16 && 2 * heads * p.few_split > resident;
+    }
     p.few_by_token = c.T <= int64_t(c.B) * p.few;
     room(p.few_by_token ? c.T : int64_t(c.B) * p.few, p.few_split, &p.few_o, &p.few_ml);
   }

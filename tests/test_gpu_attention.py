@@ -272,6 +272,16 @@ def test_left_out(fmt):
     _check(c, q, max_kv=90)
 
 
+@pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("H,P,max_kv,window", [(64, 16, None, 0), (64, 32, None, 70), (1, 64, 1 << 20, 0)])
+def test_seventeen_to_thirty_two_rows(fmt, D, H, P, max_kv, window):
+    """Drafted tokens of heads that fill the card, and of one head with a past that may be long: all rows of a head in one workgroup."""
+    g = np.random.default_rng([D, H, P])
+    c = kv_case(g, fmt, H, D, P, [4, 1, 3, 0, 2, 4, 4], [4, 130, 65, 20, 1, 64, 203], peaky=0.6, behind=1)
+    _check(c, normal_rows(g, c["T"], H * 8, D), window=window, max_kv=max_kv, what=f"{fmt} D={D} H={H} P={P} window={window}")
+
+
 @pytest.mark.parametrize("max_kv", [0, 64, 300, 5000, 1 << 20])
 def test_any_number_of_parts(max_kv):
     """max_kv sets how the work is shared out, too small or too large, never what is computed."""
