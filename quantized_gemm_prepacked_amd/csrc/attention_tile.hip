@@ -6,7 +6,7 @@
 // the same blocks of 64 positions. A block's codes are asked for from memory while the block before is worked on, converted
 // once by the whole workgroup (keys to bf16, values to fp16), and handed to the waves through two LDS buffers in turn, so
 // that there is one barrier a block. Products, lane layout and softmax are those of the few-row kernel. Measured, with the kernel of
-// 256 rows below where it serves: 4 prompts of 4500, 32 heads on 8 of 128, e4m3: 476 us, 925 TFLOP/s; 1024 tokens, 64 heads
+// 256 rows below where it serves: 4 prompts of 4500, 32 heads on 8 of 128, e4m3: 465 us, 947 TFLOP/s; 1024 tokens, 64 heads
 // on 8, INT8, on 30000 positions: 871 us, 1.18 PFLOP/s (a bf16 matrix product of 8192 reaches 1.44, of 16384 1.62).
 //
 // Bank conflicts: gfx950 serves a 16-byte LDS read of a wave 16 lanes at a time, eight of one lane group and the other
@@ -257,9 +257,9 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_tile_
 // k - 1, keys of block k) while the other has its maxima and exponentials. A barrier ends each half. Between its matrix instructions
 // every wave converts its share of the keys of k + 1 and the values of k, and asks for the next: a half turn before their first
 // reader's turn, into the one of two LDS buffers that its last reader left a half turn before.
-// The multiplying wave goes first where both could issue (895 us for 1024 x 8 rows on 30000, 937 without). What bounds it is the
-// vector instructions' port: 150 a wave and block for the softmax, 90 for conversions and addresses; without its products that
-// call takes 653 us, without all but its products 618.
+// The multiplying wave goes first where both could issue (897 us for 1024 x 8 rows on 30000, 970 without). What bounds it is the
+// vector instructions' port: 150 a wave and block for the softmax, 90 for conversions and addresses, beside 64 matrix instructions;
+// without its products that call took 653 us of 895, without softmax 777, without staging 720, products and LDS reads alone 618.
 // Head size 128 alone: larger ones leave no room for two waves on a SIMD, at 64 three workgroups of the kernel above do better
 // (2048 rows of 8 heads on 30000: 1443 us, 1632 here).
 template <int FMT>
@@ -324,11 +324,15 @@ __global__ __launch_bounds__(512, 2) void attention_paired_kernel(KvCall c) {
   // Places in LDS, of the buffers in turn: two of keys, then two of values. Chunk s of a key row, half u of a channel is at ^ 16 s.
   uint32_t k_read = key_at<D>(col, quarter, 0), k_write = key_at<D>(key_row, eighth / 2, eighth % 2 * kChunks);
   uint32_t v_read = 2 * kKeys + value_at(col, quarter, 0), v_write = 2 * kKeys + value_at(tid >> 2, piece, 0);
+  // (opaque where they are converted: the conversions stay among the matrix instructions they stand between)
   const auto store_keys = [&](int s) {
+    asm volatile("" : "+v"(kc[s].x), "+v"(kc[s].y));
     *reinterpret_cast<bf16x8*>(lds + (k_write ^ (16u * s))) = codes_bf16<FMT>(kc[s].x, kc[s].y);
   };
   const auto store_values = [&](int u) {
-    *reinterpret_cast<f16x8*>(lds + (v_write ^ (16u * u))) = codes_f16<FMT>(vc[2 * u], vc[2 * u + 1]);
+    uint32_t lo = vc[2 * u], hi = vc[2 * u + 1];
+    asm volatile("" : "+v"(lo), "+v"(hi));
+    *reinterpret_cast<f16x8*>(lds + (v_write ^ (16u * u))) = codes_f16<FMT>(lo, hi);
   };
 
   const int w0 = r0 + wave * 16 * kNQ;      // the wave's first row
@@ -417,7 +421,7 @@ __global__ __launch_bounds__(512, 2) void attention_paired_kernel(KvCall c) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (r + 1 < kProducts / 4) y[j] = read(4 * r + 4 + j);
-        if (r != 3 && r != 6) stage(r);
+        stage(r);
 #pragma unroll
         for (int j = 0; j < 4; ++j) multiply(4 * r + j, x[j]);
         if (r + 1 < kProducts / 4) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
@@ -431,8 +435,6 @@ __global__ __launch_bounds__(512, 2) void attention_paired_kernel(KvCall c) {
       }
       __builtin_amdgcn_s_setprio(0);
       lds_barrier();
-      stage(3);
-      stage(6);
       if (blk < end) {
         const int base = blk * kBlock;
         float f = ks * c.scale_log2;

@@ -332,6 +332,37 @@ def test_bad_keys_reach_who_sees_them():
         assert np.isnan(got[sees]).all() and np.isfinite(got[~sees]).all() and sees.any() and (~sees).any()
 
 
+@pytest.mark.parametrize("fmt", list(KV))
+def test_bad_queries_and_keys_among_many_rows(fmt):
+    """NaN and infinity in two query rows of a long piece, then a NaN key in its middle: every other row keeps its bits."""
+    g = np.random.default_rng(24)
+    c = kv_case(g, fmt, 1, 128, 64, [300], [700])
+    q = normal_rows(g, 300, 4, 128)
+    up = lambda a: to_dev(a.view(np.int16)).view(torch.bfloat16)  # noqa: E731
+    clean = _attend(c, _device(c), up(q), 4, max_kv=4096)
+    assert np.isfinite(bf16_to_f64(clean)).all()
+    bad = q.copy()
+    bad[17, 1, 5], bad[100, 3, 0] = 0x7FC0, 0x7F80
+    got = _attend(c, _device(c), up(bad), 4, max_kv=4096)
+    others = np.ones((300, 4), bool)
+    others[17, 1] = others[100, 3] = False
+    assert np.array_equal(got[others], clean[others]) and np.isnan(bf16_to_f64(got[17, 1])).all() and not np.isfinite(bf16_to_f64(got[100, 3])).all()
+    if fmt == "fp8":
+        c["k_pages"][c["table"][0, 500 // 64], 0, 500 % 64, 77] = 0x7F
+        got = _attend(c, _device(c), up(q), 4, max_kv=4096)
+        sees = 400 + np.arange(300) >= 500
+        assert np.isnan(bf16_to_f64(got[sees])).all() and np.array_equal(got[~sees], clean[~sees])
+
+
+def test_pages_that_sequences_share():
+    """A prefix held once: the first pages of three sequences are the same, the sequences' own follow."""
+    g = np.random.default_rng(25)
+    for D, new, lens in ((64, [1, 40, 3], [130, 200, 70]), (128, [300, 1, 280], [500, 77, 400])):
+        c = kv_case(g, "int8", 2, D, 64, new, lens, peaky=0.6)
+        c["table"][1:, 0] = c["table"][0, 0]
+        _check(c, normal_rows(g, c["T"], 8, D), max_kv=4096, what=f"shared pages D={D}")
+
+
 def test_nothing_behind_the_end_is_read():
     """The slots behind a sequence's end hold NaN codes, the other pages NaN scales (kv_case); so do, here, freed pages."""
     g = np.random.default_rng(12)
