@@ -73,7 +73,8 @@ __device__ __forceinline__ float row_sum(float v) {
 // The weights 2^(x + log2 s_v - ref) enter the product with the codes as fp16: each is off by 2^-11 of itself or 2^-25 of the
 // row's largest, whatever the scales (a bf16 weight, off by 2^-8, made the result's error half as large again as the
 // rounding of the result itself). Statistics and sums are fp32.
-constexpr float kMost = 256.0f;
+constexpr float kMost = 256.0f;     // 2^kSlack
+constexpr float kSlack = 8.0f;
 constexpr float kFar = -60.0f;
 constexpr float kNone = -3e38f;     // reference of a row that has seen nothing: its scores are -infinity, its sums 0
 
@@ -106,7 +107,9 @@ struct Rows {
       for (int n = 0; n < NQ; ++n) {
         // new references; a row goes by its own sums: what the tile's other rows hold does not change its bits
         const float m = block_max(score[n]) * ks, rm = row_max(m), rw = row_max(m + lv);
-        const bool moves = row_max(fmaxf(part[n], more[n])) > kMost;
+        // (a lane whose weights vanish beside its part of the sum: by its maximum)
+        const bool far_now = !(e[n] > kFar);
+        const bool moves = row_max(far_now ? (m > top[n] + kSlack ? INFINITY : 0.0f) : fmaxf(part[n], more[n])) > kMost;
         const float top1 = moves ? fmaxf(top[n], rm) : top[n], ref1 = moves ? fmaxf(ref[n], rw) : ref[n];
         if (__any(moves && top[n] > kNone)) {      // (where a row had seen nothing, sum and acc are 0)
           sum[n] *= exp2_fast(top[n] - top1);

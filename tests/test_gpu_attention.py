@@ -519,3 +519,16 @@ def test_value_scales_far_apart(fmt):
             d["v_pages"] = np.where(zero[:, :, None, None], 0, c["v_pages"]).astype(np.uint8)
             d["k_scales"][live & (g.random(live.shape) < 0.1)] = 0
             _check(d, normal_rows(g, c["T"], 6, 64), what=f"{fmt} scales 2^{exponents}")
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("D,new,length,max_kv", [(64, 1, 1500, None), (128, 4, 1500, None), (128, 40, 700, None), (128, 300, 900, 4096)])
+def test_values_of_zero_first(fmt, D, new, length, max_kv):
+    """Whole blocks whose values are zero (scale 0) where a row, or a wave's part of it, begins: they count in the sum alone."""
+    g = np.random.default_rng([17, D, new])
+    for zeros in (slice(0, 8), slice(0, 24), slice(4, None), slice(None)):
+        c = kv_case(g, fmt, 2, D, 16, [new], [length], peaky=0.6)
+        pages = c["table"][0][c["table"][0] >= 0][zeros]
+        c["v_scales"][pages] = 0
+        c["v_pages"][pages] = 0
+        _check(c, normal_rows(g, new, 8, D), max_kv=max_kv, what=f"{fmt} D={D} new={new} zeros {zeros}")
