@@ -158,46 +158,48 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kerne
     }
   }
 
-  // the four waves' parts, joined 16 rows at a time
-  __shared__ float tops[kWaves][16], sums[kWaves][16];
+  // the four waves' parts, joined 16 rows at a time: sums to the largest of their references, which are far from the values' unit where
+  // that is, and the average from there in two steps
+  __shared__ float tops[kWaves][16], refs[kWaves][16], sums[kWaves][16];
   __shared__ float parts[kWaves][16][D + 4];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    const float l = row_sum(st.sum[n]), unit = st.unit(n);
+    const float l = row_sum(st.sum[n]);
     if (n) __syncthreads();
     if (quarter == 0) {
       tops[wave][col] = st.top[n];
+      refs[wave][col] = st.ref[n];
       sums[wave][col] = l;
     }
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      f32x4 o;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) o[r] = st.acc[n][t][r] * unit;
-      *reinterpret_cast<f32x4*>(&parts[wave][col][16 * t + 4 * quarter]) = o;
-    }
+    for (int t = 0; t < kTiles; ++t) *reinterpret_cast<f32x4*>(&parts[wave][col][16 * t + 4 * quarter]) = st.acc[n][t];
     __syncthreads();
     for (int e = threadIdx.x; e < 16 * (D / 4); e += kWaves * 64) {
       const int row = e / (D / 4), d = (e % (D / 4)) * 4;
       const int r = r0 + 16 * n + row;
       if (r >= rows) continue;
-      float m = tops[0][row];
+      float m = tops[0][row], ref = refs[0][row];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) m = fmaxf(m, tops[w][row]);
+      for (int w = 1; w < kWaves; ++w) {
+        m = fmaxf(m, tops[w][row]);
+        ref = fmaxf(ref, refs[w][row]);
+      }
       float total = 0.0f;
       f32x4 o = {0, 0, 0, 0};
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        const float f = exp2_fast(tops[w][row] - m);
-        total += f * sums[w][row];
+        total += exp2_fast(tops[w][row] - m) * sums[w][row];
+        const float f = exp2_fast(refs[w][row] - ref);
         const f32x4 x = *reinterpret_cast<const f32x4*>(&parts[w][row][d]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[j] += f * x[j];
       }
+      const float inv = inverse(total), unit = exp2f(ref - m) * (sh.parts == 1 ? 1.0f : kKept);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = o[j] * inv * unit;
       const int i = r / c.G, h = head * c.G + r % c.G;
       if (sh.parts == 1) {
-        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-        const uint2 w = {f32x2_to_bf16x2_rne(o[0] * inv, o[1] * inv), f32x2_to_bf16x2_rne(o[2] * inv, o[3] * inv)};
+        const uint2 w = {f32x2_to_bf16x2_rne(o[0], o[1]), f32x2_to_bf16x2_rne(o[2], o[3])};
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(c.out) + ((int64_t(sq.first) + i) * c.Hq + h) * D + d) = w;
       } else {
         const int64_t at = part_row(c, sq, b, i, h) + part;
@@ -226,17 +228,9 @@ __global__ __launch_bounds__(kWaves * 64) void attention_join_kernel(KvCall c, i
   const float2 none = make_float2(-INFINITY, 0.0f);
   const auto* all = reinterpret_cast<const float2*>(c.ws_ml) + at;
   const float2 ml0 = lane < sh.parts ? all[lane] : none, ml1 = lane + 64 < sh.parts ? all[lane + 64] : none;
-  float m = fmaxf(ml0.x, ml1.x);
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-  const float f0 = exp2_fast(ml0.x - m), f1 = exp2_fast(ml1.x - m);
-  float total = f0 * ml0.y + f1 * ml1.y;
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) total += __shfl_xor(total, off, 64);
-  float o[kEach] = {};
-  constexpr int kAhead = 4;   // parts asked for together
-  for (int s0 = wave; s0 < sh.parts; s0 += kAhead * kWaves) {
-    float x[kAhead][kEach];
+  constexpr int kAhead = 4;   // parts asked for together, the first of them before the shares are known
+  float x[kAhead][kEach];
+  const auto load = [&](int s0) {
 #pragma unroll
     for (int a = 0; a < kAhead; ++a)
 #pragma unroll
@@ -244,6 +238,20 @@ __global__ __launch_bounds__(kWaves * 64) void attention_join_kernel(KvCall c, i
         const int s = s0 + a * kWaves;
         x[a][j] = s < sh.parts && (D % 64 == 0 || lane + 64 * j < D) ? c.ws_o[(at + s) * D + lane + 64 * j] : 0.0f;
       }
+  };
+  load(wave);
+  float m = fmaxf(ml0.x, ml1.x);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+  float f0 = exp2_fast(ml0.x - m) * ml0.y, f1 = exp2_fast(ml1.x - m) * ml1.y, total = f0 + f1;
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) total += __shfl_xor(total, off, 64);
+  const float whole = inverse(total) * (1.0f / kKept);
+  f0 *= whole;
+  f1 *= whole;
+  float o[kEach] = {};
+  for (int s0 = wave; s0 < sh.parts; s0 += kAhead * kWaves) {
+    if (s0 != wave) load(s0);
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       const int s = s0 + a * kWaves;
@@ -256,10 +264,8 @@ __global__ __launch_bounds__(kWaves * 64) void attention_join_kernel(KvCall c, i
 #pragma unroll
   for (int j = 0; j < kEach; ++j) parts[wave][lane + 64 * j] = o[j];
   __syncthreads();
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   auto* out = static_cast<uint16_t*>(c.out) + ((int64_t(sq.first) + i) * c.Hq + h) * D;
-  for (int d = threadIdx.x; d < D; d += kWaves * 64)
-    out[d] = f32_to_bf16_rne(((parts[0][d] + parts[1][d]) + (parts[2][d] + parts[3][d])) * inv);
+  for (int d = threadIdx.x; d < D; d += kWaves * 64) out[d] = f32_to_bf16_rne((parts[0][d] + parts[1][d]) + (parts[2][d] + parts[3][d]));
 }
 
 template <int D>

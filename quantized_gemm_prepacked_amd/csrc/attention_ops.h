@@ -181,6 +181,12 @@ struct Rows {
   __device__ __forceinline__ float unit(int n) const { return ref[n] > kNone ? exp2f(ref[n] - top[n]) : 0.0f; }
 };
 
+// Parts hand on averages, not sums: a sum of values near the largest bf16 leaves fp32's range where their average does not. They
+// are kept as a quarter, since a code rounded up and its scale may be twice that bf16; the join gives each its share of the total, which
+// is 1 at most, times 4. 0 for rows that have seen nothing.
+constexpr float kKept = 0.25f;
+__device__ __forceinline__ float inverse(float total) { return total == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(total); }   // (off by 2^-23 at most)
+
 // Scores of positions that row `pos` (a position) does not see become -infinity, the others x. vg: the lane's first position.
 template <int NQ>
 __device__ __forceinline__ void mask_scores(f32x4 (&score)[NQ][4], const int (&pos)[NQ], int vg, int window, bool there, float ks) {

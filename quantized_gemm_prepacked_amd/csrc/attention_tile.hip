@@ -82,16 +82,17 @@ __device__ __forceinline__ void write_rows(const KvCall& c, const KvSeq& sq, con
 #pragma unroll
   for (int n = 0; n < kNQ; ++n) {
     const int r = w0 + 16 * n + col;
-    const float total = row_sum(st.sum[n]), unit = st.unit(n);
+    // the average, in two steps: sum and unit may each be far from 1
+    const float total = row_sum(st.sum[n]), inv = inverse(total), unit = st.unit(n) * (sh.parts == 1 ? 1.0f : kKept);
     if (r >= rows) continue;
     const int i = r / c.G, h = head * c.G + r % c.G;
     if (sh.parts == 1) {
-      const float inv = total == 0.0f ? 0.0f : unit / total;
       auto* out = static_cast<uint16_t*>(c.out) + ((int64_t(sq.first) + i) * c.Hq + h) * D + 4 * quarter;
 #pragma unroll
       for (int t = 0; t < D / 16; ++t) {
         const f32x4& o = st.acc[n][t];
-        *reinterpret_cast<uint2*>(out + 16 * t) = make_uint2(f32x2_to_bf16x2_rne(o[0] * inv, o[1] * inv), f32x2_to_bf16x2_rne(o[2] * inv, o[3] * inv));
+        *reinterpret_cast<uint2*>(out + 16 * t) =
+            make_uint2(f32x2_to_bf16x2_rne(o[0] * inv * unit, o[1] * inv * unit), f32x2_to_bf16x2_rne(o[2] * inv * unit, o[3] * inv * unit));
       }
     } else {
       const int64_t to = part_row(c, sq, b, i, h) + part;
@@ -99,7 +100,7 @@ __device__ __forceinline__ void write_rows(const KvCall& c, const KvSeq& sq, con
       for (int t = 0; t < D / 16; ++t) {
         f32x4 o;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = st.acc[n][t][j] * unit;
+        for (int j = 0; j < 4; ++j) o[j] = st.acc[n][t][j] * inv * unit;
         *reinterpret_cast<f32x4*>(c.ws_o + to * D + 16 * t + 4 * quarter) = o;
       }
       if (quarter == 0) *reinterpret_cast<float2*>(c.ws_ml + 2 * to) = make_float2(st.top[n], total);

@@ -174,7 +174,7 @@ struct KvCall {
   int tile_rows;                          // rows of a workgroup of the tiled kernels,
   int n_split, each;                      // parts of the positions at most, and blocks of a part at least,
   bool by_token;                          // partial results by row of q (else by sequence and token),
-  float* ws_o;                            // [row][part][D], and (maximum, sum) of each part
+  float* ws_o;                            // averages [row][part][D], and (reference of the maximum, sum) of each part
   float* ws_ml;
 };
 hipError_t launch_kv_append(const KvCall& c, hipStream_t s);

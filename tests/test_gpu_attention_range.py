@@ -1,0 +1,49 @@
+"""Attention over the paged cache at the ends of its number ranges, against float64: values near the largest bf16."""
+import numpy as np
+import pytest
+
+import oracle
+
+from gpu_harness import bf16_to_f64, say, to_dev
+from layer_harness import KV, check_attention, kv_case, normal_rows
+from test_gpu_attention import _attend, _device
+
+import torch
+
+pytestmark = pytest.mark.gpu
+
+# (D, G, new, length, max_kv) that take: four waves' join, the split positions' join, 32 rows a workgroup, 128 rows in one part and in
+# several, 256 rows in one part and in several
+PATHS = [(64, 4, 1, 300, 64), (128, 4, 4, 1500, 1500), (256, 6, 5, 700, 700), (64, 4, 40, 700, 64), (128, 4, 40, 2900, 2900), (96, 3, 50, 2000, 2000),
+         (128, 4, 300, 400, 2048), (128, 4, 300, 1300, 4096)]
+
+
+def _run(c, q, max_kv, sm=None):
+    D = c["D"]
+    sm = D ** -0.5 if sm is None else sm
+    got = bf16_to_f64(_attend(c, _device(c), to_dev(q.view(np.int16)).view(torch.bfloat16), q.shape[1], sm=sm, max_kv=max_kv))
+    ref = oracle.ref_attention(c["fmt"], q, c["cu"], c["lens"], c["table"], c["k_pages"], c["v_pages"], c["k_scales"], c["v_scales"], sm, 0, np.zeros(q.shape))
+    return got, ref
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("D,G,new,length,max_kv", PATHS)
+def test_values_near_the_largest(fmt, D, G, new, length, max_kv):
+    """Averages of values whose sums pass fp32's range: all of the largest bf16 (as an infinity is stored), of both signs, and scales up
+    to 2^118."""
+    g = np.random.default_rng([D, new, length])
+    c = kv_case(g, fmt, 2, D, 16, [new], [length], peaky=0.01)
+    q = normal_rows(g, new, 2 * G, D)
+    largest = float(oracle.decode_bf16(np.array([0x7F7F], np.uint16))[0])
+    plain, pages, live = c["v_pages"], c["v_scales"].copy(), ~np.isnan(c["v_scales"])
+    top, low = (0x7E, 0xFE) if fmt == "fp8" else (127, 0x81)
+    for what in ("largest", "both signs", "far scales"):
+        if what == "far scales":
+            c["v_pages"] = plain
+            c["v_scales"] = np.where(live, np.ldexp(pages, g.integers(100, 124, pages.shape)), np.nan).astype(np.float32)
+        else:
+            sign = g.random(plain.shape) < (0.5 if what == "both signs" else 0.0)
+            c["v_pages"] = np.where(sign, low, top).astype(np.uint8)
+            c["v_scales"] = np.where(live, np.float32(largest) * (np.float32(1) / np.float32(448 if fmt == "fp8" else 127)), np.nan).astype(np.float32)
+        got, ref = _run(c, q, max_kv)
+        check_attention(got, *ref, D, length, f"{fmt} D={D} new={new} on {length}: {what}", say)
