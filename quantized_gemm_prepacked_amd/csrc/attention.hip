@@ -160,7 +160,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kerne
 
   // the four waves' parts, joined 16 rows at a time: sums to the largest of their references, which are far from the values' unit where
   // that is, and the average from there in two steps
-  __shared__ float tops[kWaves][16], refs[kWaves][16], sums[kWaves][16];
+  __shared__ float tops[kWaves][16], rels[kWaves][16], sums[kWaves][16];
   __shared__ float parts[kWaves][16][D + 4];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
@@ -168,43 +168,40 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kerne
     if (n) __syncthreads();
     if (quarter == 0) {
       tops[wave][col] = st.top[n];
-      refs[wave][col] = st.ref[n];
+      rels[wave][col] = st.rel[n];
       sums[wave][col] = l;
     }
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) *reinterpret_cast<f32x4*>(&parts[wave][col][16 * t + 4 * quarter]) = st.acc[n][t];
     __syncthreads();
+    // a lane's own row and wave: its factor, and what makes the row's sum an average
+    const float top = row_max(tops[quarter][col]), below = tops[quarter][col] - top, at = below + rels[quarter][col], ref = row_max(at);
+    const float factor = exp2_fast(at - ref), total = row_sum(exp2_fast(below) * sums[quarter][col]);
+    const float inv = inverse(total), unit = exp2f(ref) * (sh.parts == 1 ? 1.0f : kKept);
     for (int e = threadIdx.x; e < 16 * (D / 4); e += kWaves * 64) {
       const int row = e / (D / 4), d = (e % (D / 4)) * 4;
       const int r = r0 + 16 * n + row;
-      if (r >= rows) continue;
-      float m = tops[0][row], ref = refs[0][row];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) {
-        m = fmaxf(m, tops[w][row]);
-        ref = fmaxf(ref, refs[w][row]);
-      }
-      float total = 0.0f;
       f32x4 o = {0, 0, 0, 0};
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        total += exp2_fast(tops[w][row] - m) * sums[w][row];
-        const float f = exp2_fast(refs[w][row] - ref);
+        const float f = __shfl(factor, row + 16 * w, 64);
         const f32x4 x = *reinterpret_cast<const f32x4*>(&parts[w][row][d]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[j] += f * x[j];
       }
-      const float inv = inverse(total), unit = exp2f(ref - m) * (sh.parts == 1 ? 1.0f : kKept);
+      const float by = __shfl(inv, row, 64), to = __shfl(unit, row, 64);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = o[j] * inv * unit;
+      for (int j = 0; j < 4; ++j) o[j] = o[j] * by * to;
+      const float2 ml = make_float2(__shfl(top, row, 64), __shfl(total, row, 64));
+      if (r >= rows) continue;
       const int i = r / c.G, h = head * c.G + r % c.G;
       if (sh.parts == 1) {
         const uint2 w = {f32x2_to_bf16x2_rne(o[0], o[1]), f32x2_to_bf16x2_rne(o[2], o[3])};
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(c.out) + ((int64_t(sq.first) + i) * c.Hq + h) * D + d) = w;
       } else {
-        const int64_t at = part_row(c, sq, b, i, h) + part;
-        *reinterpret_cast<f32x4*>(c.ws_o + at * D + d) = o;
-        if (d == 0) *reinterpret_cast<float2*>(c.ws_ml + 2 * at) = make_float2(m, total);
+        const int64_t to_row = part_row(c, sq, b, i, h) + part;
+        *reinterpret_cast<f32x4*>(c.ws_o + to_row * D + d) = o;
+        if (d == 0) *reinterpret_cast<float2*>(c.ws_ml + 2 * to_row) = ml;
       }
     }
   }

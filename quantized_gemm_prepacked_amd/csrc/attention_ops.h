@@ -66,28 +66,30 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 // Running softmax of the rows a lane holds. With x = sm_scale * log2(e) * q . k and s_v the scale of the position's values:
-//   sum = sum 2^(x - top)  (this lane's positions),   acc = sum 2^(x + log2 s_v - ref) * code,
-// with references top and ref below the maxima of x and of x + log2 s_v seen so far by little enough that a lane's 16 terms
+//   sum = sum 2^(x - top)  (this lane's positions),   acc = sum 2^(x + log2 s_v - top - rel) * code,
+// with references top and top + rel below the maxima of x and of x + log2 s_v seen so far by little enough that a lane's 16 terms
 // add up to kMost at most: the sums that are made anyhow tell, so that the maxima are taken, over a row's four lanes, and
 // what was summed before is brought to new references, only in blocks where one has to move (the first and a few others).
-// The weights 2^(x + log2 s_v - ref) enter the product with the codes as fp16: each is off by 2^-11 of itself or 2^-25 of the
+// The second reference is kept from the first: scores may be of any size, also one at which log2 s_v is lost beside them.
+// The weights 2^(x + log2 s_v - top - rel) enter the product with the codes as fp16: each is off by 2^-11 of itself or 2^-25 of the
 // row's largest, whatever the scales (a bf16 weight, off by 2^-8, made the result's error half as large again as the
 // rounding of the result itself). Statistics and sums are fp32.
 constexpr float kMost = 256.0f;     // 2^kSlack
 constexpr float kSlack = 8.0f;
 constexpr float kFar = -60.0f;
-constexpr float kNone = -3e38f;     // reference of a row that has seen nothing: its scores are -infinity, its sums 0
+constexpr float kLarge = 4096.0f;   // (below, a fused product is within 2^-12 of the rounded one)
+constexpr float kNone = -3e38f;     // top of a row that has seen nothing: its scores are -infinity, its sums 0
 
 template <int NQ, int TILES>
 struct Rows {
   f32x4 acc[NQ][TILES];
-  float top[NQ], ref[NQ], sum[NQ];
+  float top[NQ], rel[NQ], sum[NQ];
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      top[n] = ref[n] = kNone;
-      sum[n] = 0.0f;
+      top[n] = kNone;
+      rel[n] = sum[n] = 0.0f;
 #pragma unroll
       for (int t = 0; t < TILES; ++t) acc[n][t] = f32x4{0, 0, 0, 0};
     }
@@ -96,42 +98,63 @@ struct Rows {
   // A block's scores to weights. Scores are products of q and k codes, ks >= 0 makes them x (where masked they are -infinity or
   // x already, and ks is 1); lv = log2 of the values' scale, -infinity where that is 0 or there is no page.
   // The weights are made with the references there are, and again where those move.
-  __device__ __forceinline__ void step(const f32x4 (&score)[NQ][4], float ks, float lv, f16x8 (&weight)[NQ][2]) {
-    float part[NQ], more[NQ], e[NQ];
-    weigh(score, ks, lv, weight, part, more, e);
+  __device__ __forceinline__ void step(f32x4 (&score)[NQ][4], float ks, float lv, f16x8 (&weight)[NQ][2]) {
+    float part[NQ], more[NQ], e[NQ];      // e: log2 of the weights' unit to that of the sum's terms
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      e[n] = lv - rel[n];
+      weigh(score[n], ks, e[n] - top[n], e[n], weight[n], part[n], more[n]);
+    }
+    settle(weight);
     bool rare = false;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) rare |= !(part[n] <= kMost && more[n] <= kMost && e[n] > kFar);
     if (__any(rare)) {
+#pragma clang fp contract(off)
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         // new references; a row goes by its own sums: what the tile's other rows hold does not change its bits
-        const float m = block_max(score[n]) * ks, rm = row_max(m), rw = row_max(m + lv);
+        const float m = block_max(score[n]) * ks, rm = row_max(m);
         // (a lane whose weights vanish beside its part of the sum: by its maximum)
         const bool far_now = !(e[n] > kFar);
-        const bool moves = row_max(far_now ? (m > top[n] + kSlack ? INFINITY : 0.0f) : fmaxf(part[n], more[n])) > kMost;
-        const float top1 = moves ? fmaxf(top[n], rm) : top[n], ref1 = moves ? fmaxf(ref[n], rw) : ref[n];
+        const bool moves = row_max((far_now ? m > top[n] + kSlack : !(part[n] <= kMost && more[n] <= kMost)) ? 1.0f : 0.0f) > 0.0f;
+        const float top1 = moves ? fmaxf(top[n], rm) : top[n];
+        const float old = rel[n] + (top[n] - top1), rw = row_max((m - top1) + lv);
+        const float rel1 = moves ? fmaxf(old, rw) : rel[n];
         if (__any(moves && top[n] > kNone)) {      // (where a row had seen nothing, sum and acc are 0)
           sum[n] *= exp2_fast(top[n] - top1);
-          const float shrink = exp2_fast(ref[n] - ref1);
+          const float shrink = exp2_fast(old - rel1);
 #pragma unroll
           for (int t = 0; t < TILES; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[n][t][r] *= shrink;
         }
         top[n] = top1;
-        ref[n] = ref1;
+        rel[n] = rel1;
+        e[n] = lv - rel1;
+        // Large scores go by their products' distances from the new reference, rounded before: 0 for the one that set it, where the
+        // fused form leaves the rounding of the reference (2^40 for scores of 2^64).
+        const bool large = moves && !(fabsf(top1) < kLarge);
+        const float unit = large ? 1.0f : ks, from = large ? 0.0f : -top1;
+        if (__any(large)) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float x = score[n][k >> 2][k & 3];
+            score[n][k >> 2][k & 3] = large ? x * ks - top1 : x;
+          }
+        }
         // Scales so far apart (or 0) that a weight vanishes where its part of the sum does not: that part by itself.
-        const bool far = !(lv + (top1 - ref1) > kFar);
+        const bool far = !(e[n] > kFar);
         if (__any(far)) {
           float s = 0.0f;
-          const float at = top1 > kNone ? top1 : 0.0f;
+          const float at = top1 > kNone ? from : 0.0f;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) s += exp2_fast(fmaf(score[n][k >> 2][k & 3], ks, -at));
+          for (int k = 0; k < 16; ++k) s += exp2_fast(fmaf(score[n][k >> 2][k & 3], unit, at));
           sum[n] += far ? s : 0.0f;
         }
+        weigh(score[n], unit, e[n] + from, e[n], weight[n], part[n], more[n]);
       }
-      weigh(score, ks, lv, weight, part, more, e);
+      settle(weight);
     }
 #pragma unroll
     for (int n = 0; n < NQ; ++n) sum[n] += e[n] > kFar ? more[n] : 0.0f;
@@ -142,32 +165,29 @@ struct Rows {
     return fmaxf(fmaxf(four(x[0]), four(x[1])), fmaxf(four(x[2]), four(x[3])));
   }
 
-  // Weights 2^(x + lv - ref), their sum over the lane's positions, that of 2^(x - top), and e = log2 of the first's unit to the second's.
-  __device__ __forceinline__ void weigh(const f32x4 (&score)[NQ][4], float ks, float lv, f16x8 (&weight)[NQ][2], float (&part)[NQ], float (&more)[NQ],
-                                        float (&e)[NQ]) const {
+  // Weights 2^(score * ks + start), their sum over the lane's positions, and that of 2^(x - top), which is 2^-e times the first.
+  static __device__ __forceinline__ void weigh(const f32x4 (&score)[4], float ks, float start, float e, f16x8 (&weight)[2], float& part, float& more) {
+    float four[4];
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const float start = lv - ref[n];
-      e[n] = lv + (top[n] - ref[n]);
-      float four[4];
+    for (int i = 0; i < 4; ++i) {
+      float p[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float p[4];
+      for (int r = 0; r < 4; ++r) p[r] = exp2_fast(fmaf(score[i][r], ks, start));
+      four[i] = (p[0] + p[1]) + (p[2] + p[3]);
+      u32x4 w = __builtin_bit_cast(u32x4, weight[i >> 1]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) p[r] = exp2_fast(fmaf(score[n][i][r], ks, start));
-        four[i] = (p[0] + p[1]) + (p[2] + p[3]);
-        u32x4 w = __builtin_bit_cast(u32x4, weight[n][i >> 1]);
-#pragma unroll
-        for (int r = 0; r < 4; r += 2) {
-          const f32x2 two = {p[r], p[r + 1]};
-          w[2 * (i & 1) + r / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, f16x2));
-        }
-        weight[n][i >> 1] = __builtin_bit_cast(f16x8, w);
+      for (int r = 0; r < 4; r += 2) {
+        const f32x2 two = {p[r], p[r + 1]};
+        w[2 * (i & 1) + r / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, f16x2));
       }
-      part[n] = (four[0] + four[1]) + (four[2] + four[3]);
-      more[n] = part[n] * exp2_fast(-e[n]);
+      weight[i >> 1] = __builtin_bit_cast(f16x8, w);
     }
-    // (here, not behind the branch that may make them again)
+    part = (four[0] + four[1]) + (four[2] + four[3]);
+    more = part * exp2_fast(-e);
+  }
+
+  // (weights made here, not behind the branch that may make them again)
+  static __device__ __forceinline__ void settle(f16x8 (&weight)[NQ][2]) {
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       u32x4 u = __builtin_bit_cast(u32x4, weight[n][0]), v = __builtin_bit_cast(u32x4, weight[n][1]);
@@ -178,7 +198,7 @@ struct Rows {
   }
 
   // What turns acc into sum 2^(x - top) * value.
-  __device__ __forceinline__ float unit(int n) const { return ref[n] > kNone ? exp2f(ref[n] - top[n]) : 0.0f; }
+  __device__ __forceinline__ float unit(int n) const { return exp2f(rel[n]); }
 };
 
 // Parts hand on averages, not sums: a sum of values near the largest bf16 leaves fp32's range where their average does not. They

@@ -1,4 +1,5 @@
-"""Attention over the paged cache at the ends of its number ranges, against float64: values near the largest bf16."""
+"""Attention over the paged cache at the ends of its number ranges, against float64: values near the largest bf16,
+scores of any size."""
 import numpy as np
 import pytest
 
@@ -47,3 +48,39 @@ def test_values_near_the_largest(fmt, D, G, new, length, max_kv):
             c["v_scales"] = np.where(live, np.float32(largest) * (np.float32(1) / np.float32(448 if fmt == "fp8" else 127)), np.nan).astype(np.float32)
         got, ref = _run(c, q, max_kv)
         check_attention(got, *ref, D, length, f"{fmt} D={D} new={new} on {length}: {what}", say)
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("D,G,new,length,max_kv", PATHS)
+def test_scores_of_any_size(fmt, D, G, new, length, max_kv):
+    """Scores so large that fp32 tells only the largest apart, with values' scales up to 2^far from their mean: a row is the value of its
+    largest score, rounded once. Rows whose two largest are nearer than the scores' rounding (2^-22 (D + 8) of the products' size, each) and
+    40 + 2 far log 2 are left out; there are few. So every other weight is at most e^-40 4^-far, `length` of them add up to that many times
+    the largest value at most, and 2^-8 (the result), 2^-11 (its weight as an fp16) and 2^-20 (the fp32 steps) of the value itself come on
+    top."""
+    g = np.random.default_rng([1, D, new, length])
+    c = kv_case(g, fmt, 2, D, 16, [new], [length])
+    live = ~np.isnan(c["v_scales"])
+    sm, at = 0.3, np.arange(length)
+    pages = c["table"][0, at // 16]
+    val = oracle.decode_e4m3 if fmt == "fp8" else (lambda a: oracle.decode_int8(a.view(np.int8)))
+    plain = c["v_scales"]
+    for bits, far in ((12, 0), (20, 0), (27, 0), (30, 20), (48, 0), (64, 90), (110, 90)):
+        c["v_scales"] = np.where(live, np.ldexp(plain, g.integers(-far, far + 1, plain.shape)), np.nan).astype(np.float32)
+        q = normal_rows(g, new, 2 * G, D, 2.0 ** bits)
+        got, ref = _run(c, q, max_kv, sm)
+        qv, checked, worst = oracle.decode_bf16(q), 0, 0.0
+        for h in range(2):
+            k = val(c["k_pages"][pages, h, at % 16]) * c["k_scales"][pages, h].astype(np.float64)[:, None]
+            v = val(c["v_pages"][pages, h, :, at % 16]) * c["v_scales"][pages, h].astype(np.float64)[:, None]
+            s = sm * np.einsum("thd,jd->thj", qv[:, h * G:h * G + G], k)
+            s = np.where(at > (length - new + np.arange(new))[:, None, None], -np.inf, s)
+            order = np.sort(s, -1)
+            sure = order[..., -1] - order[..., -2] > 2 * 2.0 ** -22 * (D + 8) * ref[4][:, h * G:h * G + G] + 40 + 2 * far * np.log(2)
+            want, have = v[s.argmax(-1)][sure], got[:, h * G:h * G + G][sure]
+            assert np.isfinite(have).all(), f"2^{bits}"
+            bound = (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20) * np.abs(want) + length * np.exp(-40) * 4.0 ** -far * np.abs(v).max() + 2.0 ** -134
+            worst = max([worst, *(np.abs(have - want) / bound).ravel()])
+            checked += sure.sum()
+        say(f"  {fmt} D={D} new={new} on {length}, q of 2^{bits}: {checked} of {2 * G * new} rows, worst {worst:.3f} of its bound")
+        assert worst <= 1.0 and checked >= 0.8 * 2 * G * new, f"2^{bits}"
