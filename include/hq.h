@@ -610,9 +610,9 @@ hq_status hq_kv_append(const hq_kv_desc* desc, int32_t B, int64_t T, int32_t max
  * num_kv_heads) of the cache):
  *   out[t, i] = bf16( sum_j p_j v_j / sum_j p_j ),  p_j = exp( sm_scale * q[t, i] . k_j ),
  * over the positions j <= pos(t) of t's sequence, with window > 0 only j > pos(t) - window. A row
- * that sees no token gets zeros. fp32 accumulation and statistics (scores of any size up to 2^127; a row with one
- * past that is unspecified); p_j * scale (of v_j) enters the product
- * with the codes as an fp16, relative to the row's largest. Scales are not negative (hq_kv_append makes
+ * that sees no token gets zeros. fp32 accumulation and statistics: scores may be of any size below 2^127 in units
+ * of log 2 (a row with one past that is unspecified). p_j * scale (of v_j) enters the product with the codes as an
+ * fp16, off by 2^-11 of itself or 2^-35 of the row's largest. Scales are not negative (hq_kv_append makes
  * none). NaN in a query's row reaches that row alone, a NaN key the rows that see it; a NaN code among the
  * values (hq_kv_append makes none) any row of its sequence.
  *   q        bf16, token rows q_stride elements apart (>= Hq * D, a multiple of 8), 16-byte aligned, T rows

@@ -158,8 +158,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kerne
     }
   }
 
-  // the four waves' parts, joined 16 rows at a time: sums to the largest of their references, which are far from the values' unit where
-  // that is, and the average from there in two steps
+  // the four waves' parts, joined 16 rows at a time: sums to the largest of their references, and the average from there
   __shared__ float tops[kWaves][16], rels[kWaves][16], sums[kWaves][16];
   __shared__ float parts[kWaves][16][D + 4];
 #pragma unroll
@@ -177,7 +176,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kerne
     // a lane's own row and wave: its factor, and what makes the row's sum an average
     const float top = row_max(tops[quarter][col]), below = tops[quarter][col] - top, at = below + rels[quarter][col], ref = row_max(at);
     const float factor = exp2_fast(at - ref), total = row_sum(exp2_fast(below) * sums[quarter][col]);
-    const float inv = inverse(total), unit = exp2f(ref) * (sh.parts == 1 ? 1.0f : kKept);
+    const float by = lowered(total), to = unit(ref) * (sh.parts == 1 ? 1.0f : kKept);
     for (int e = threadIdx.x; e < 16 * (D / 4); e += kWaves * 64) {
       const int row = e / (D / 4), d = (e % (D / 4)) * 4;
       const int r = r0 + 16 * n + row;
@@ -189,9 +188,9 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kerne
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[j] += f * x[j];
       }
-      const float by = __shfl(inv, row, 64), to = __shfl(unit, row, 64);
+      const float row_by = __shfl(by, row, 64), row_to = __shfl(to, row, 64);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = o[j] * by * to;
+      for (int j = 0; j < 4; ++j) o[j] = o[j] * row_by * row_to;
       const float2 ml = make_float2(__shfl(top, row, 64), __shfl(total, row, 64));
       if (r >= rows) continue;
       const int i = r / c.G, h = head * c.G + r % c.G;
@@ -199,9 +198,9 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kerne
         const uint2 w = {f32x2_to_bf16x2_rne(o[0], o[1]), f32x2_to_bf16x2_rne(o[2], o[3])};
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(c.out) + ((int64_t(sq.first) + i) * c.Hq + h) * D + d) = w;
       } else {
-        const int64_t to_row = part_row(c, sq, b, i, h) + part;
-        *reinterpret_cast<f32x4*>(c.ws_o + to_row * D + d) = o;
-        if (d == 0) *reinterpret_cast<float2*>(c.ws_ml + 2 * to_row) = ml;
+        const int64_t slot = part_row(c, sq, b, i, h) + part;
+        *reinterpret_cast<f32x4*>(c.ws_o + slot * D + d) = o;
+        if (d == 0) *reinterpret_cast<float2*>(c.ws_ml + 2 * slot) = ml;
       }
     }
   }

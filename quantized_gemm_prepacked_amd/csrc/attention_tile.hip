@@ -82,8 +82,7 @@ __device__ __forceinline__ void write_rows(const KvCall& c, const KvSeq& sq, con
 #pragma unroll
   for (int n = 0; n < kNQ; ++n) {
     const int r = w0 + 16 * n + col;
-    // the average, in two steps: sum and unit may each be far from 1
-    const float total = row_sum(st.sum[n]), inv = inverse(total), unit = st.unit(n) * (sh.parts == 1 ? 1.0f : kKept);
+    const float total = row_sum(st.sum[n]), by = lowered(total), to = unit(st.rel[n]) * (sh.parts == 1 ? 1.0f : kKept);
     if (r >= rows) continue;
     const int i = r / c.G, h = head * c.G + r % c.G;
     if (sh.parts == 1) {
@@ -92,18 +91,18 @@ __device__ __forceinline__ void write_rows(const KvCall& c, const KvSeq& sq, con
       for (int t = 0; t < D / 16; ++t) {
         const f32x4& o = st.acc[n][t];
         *reinterpret_cast<uint2*>(out + 16 * t) =
-            make_uint2(f32x2_to_bf16x2_rne(o[0] * inv * unit, o[1] * inv * unit), f32x2_to_bf16x2_rne(o[2] * inv * unit, o[3] * inv * unit));
+            make_uint2(f32x2_to_bf16x2_rne(o[0] * by * to, o[1] * by * to), f32x2_to_bf16x2_rne(o[2] * by * to, o[3] * by * to));
       }
     } else {
-      const int64_t to = part_row(c, sq, b, i, h) + part;
+      const int64_t at = part_row(c, sq, b, i, h) + part;
 #pragma unroll
       for (int t = 0; t < D / 16; ++t) {
         f32x4 o;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = st.acc[n][t][j] * inv * unit;
-        *reinterpret_cast<f32x4*>(c.ws_o + to * D + 16 * t + 4 * quarter) = o;
+        for (int j = 0; j < 4; ++j) o[j] = st.acc[n][t][j] * by * to;
+        *reinterpret_cast<f32x4*>(c.ws_o + at * D + 16 * t + 4 * quarter) = o;
       }
-      if (quarter == 0) *reinterpret_cast<float2*>(c.ws_ml + 2 * to) = make_float2(st.top[n], total);
+      if (quarter == 0) *reinterpret_cast<float2*>(c.ws_ml + 2 * at) = make_float2(st.top[n], total);
     }
   }
 }

@@ -1,5 +1,5 @@
 """Attention over the paged cache at the ends of its number ranges, against float64: values near the largest bf16,
-scores of any size."""
+scores of any size, rows most of whose weight is on a token of value 0."""
 import numpy as np
 import pytest
 
@@ -84,3 +84,38 @@ def test_scores_of_any_size(fmt, D, G, new, length, max_kv):
             checked += sure.sum()
         say(f"  {fmt} D={D} new={new} on {length}, q of 2^{bits}: {checked} of {2 * G * new} rows, worst {worst:.3f} of its bound")
         assert worst <= 1.0 and checked >= 0.8 * 2 * G * new, f"2^{bits}"
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("D,G,new,length,max_kv", [(64, 4, 1, 30000, 64), (128, 4, 4, 20000, 64), (64, 4, 40, 20000, 64), (128, 2, 40, 9000, 64), (256, 1, 40, 9000, 64),
+                                                   (128, 4, 64, 20000, 2048)])
+@pytest.mark.parametrize("share", [0.9, 0.99, 0.999])
+def test_first_token_takes_the_weight(fmt, D, G, new, length, max_kv, share):
+    """A first token with `share` of a row's weight and a value of 0: the row is what the others leave. The result's rounding to bf16, uniform
+    within a step of 2^-7 of the binade, is 2^-7 / sqrt(28) of the whole's size (the mean square of 1 .. 2 is 7 / 3); the roundings of
+    the weights stay below the same, so that twice that is never passed."""
+    g = np.random.default_rng([2, D, new, length])
+    c = kv_case(g, fmt, 1, D, 32, [new], [length], peaky=0.3)
+    q, sm, first = normal_rows(g, new, G, D), D ** -0.5, c["table"][0, 0]
+    q[..., 0] = 0x4200                                 # 32
+    c["k_pages"][..., 0] = 0                           # channel 0: the first token's alone
+    c["k_pages"][first] = 0
+    c["v_pages"][first, :, :, 0] = 0
+    c["k_pages"][first, 0, 0, 0] = 0x68 if fmt == "fp8" else 64         # 64
+    c["k_scales"][first] = 0
+    val = oracle.decode_e4m3 if fmt == "fp8" else (lambda a: oracle.decode_int8(a.view(np.int8)))
+    at = np.arange(length)
+    page = c["table"][0, at // 32]
+    k = val(c["k_pages"][page, 0, at % 32]) * c["k_scales"][page, 0].astype(np.float64)[:, None]
+    v = val(c["v_pages"][page, 0, :, at % 32]) * c["v_scales"][page, 0].astype(np.float64)[:, None]
+    score = sm * np.einsum("tgd,jd->tgj", oracle.decode_bf16(q), k)
+    others = np.log(np.exp(score[0, 0]).sum())
+    scale = np.float32((others + np.log(share / (1 - share))) / (sm * 32 * 64))
+    c["k_scales"][first] = scale                       # (the first page's other keys are zeros)
+    score[..., 0] = sm * 32 * 64 * float(scale)
+    weight = np.exp(np.where(at > (length - new + np.arange(new))[:, None, None], -np.inf, score))
+    ref = weight @ v / weight.sum(-1, keepdims=True)
+    got = bf16_to_f64(_attend(c, _device(c), to_dev(q.view(np.int16)).view(torch.bfloat16), G, sm=sm, max_kv=max_kv))
+    error = float(np.linalg.norm(got - ref) / np.linalg.norm(ref))
+    say(f"  {fmt} D={D} new={new} on {length}, {share}: {error / (2.0 ** -7 / 28 ** 0.5):.3f} of the rounding to bf16")
+    assert error <= 2 * 2.0 ** -7 / 28 ** 0.5
