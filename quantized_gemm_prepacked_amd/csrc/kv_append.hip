@@ -28,9 +28,9 @@ __device__ __forceinline__ uint32_t counted(uint32_t h) {
   return m > 0x7F80u ? 0u : min(m, 0x7F7Fu);
 }
 
-// fp32(v / s) of a bf16 v and a scale of this cache, from rs = fp32(1 / s): a product and one correction by the exact remainder.
-// Scales are fp32(bf16 * fp32(1 / 127 or 1 / 448)) times powers of two: 128 mantissas, and bf16 has 128, so that all quotients'
-// mantissas can be tried out, and the result is the IEEE quotient for every one.
+// fp32(v / s) of a bf16 v, from rs = fp32(1 / s): a product and one correction by the remainder. A bf16 has 128 mantissas and
+// a scale, which may come from a page that was filled elsewhere, 2^23: the result is the IEEE quotient for every pair (all 2^30 tried on
+// a CPU).
 __device__ __forceinline__ float page_quotient(float v, float s, float rs) {
   const float q = v * rs;
   return fmaf(fmaf(-q, s, v), rs, q);

@@ -325,3 +325,22 @@ def test_stream_of_another_device():
                  lambda st: hq.hq_attention(d, 1, 1, 8, 1, 16, 16, 1024, 16, 16, 16, 1, 16, 16, 16, 16, 0.1, 0, 48, stream=st)):
         with pytest.raises(hq.HQError, match="stream must be on the current device"):
             call(Stream())
+
+
+def test_page_quotients_at_any_scale():
+    """The same quotient for scales of any mantissa, as pages hold that were filled elsewhere. The fused last step in float64: the sum of two exact
+    terms, rounded there, decides the fp32 rounding but where that left it half way between two fp32."""
+    g = np.random.default_rng(31)
+    v = (np.arange(128, 256) / 128).astype(np.float32)
+    ends = np.concatenate([np.arange(512), (1 << 23) - 1 - np.arange(512), (1 << 22) - 256 + np.arange(512)])
+    for bits in np.array_split(np.unique(np.concatenate([ends, g.integers(0, 1 << 23, 100000)])), 20):
+        s = ((np.uint32(0x3F800000) | bits.astype(np.uint32)).view(np.float32))[:, None]
+        rs = np.float32(1) / s
+        q = v * rs
+        r = (v.astype(np.float64) - q.astype(np.float64) * s.astype(np.float64)).astype(np.float32)     # (exact before it is rounded)
+        step = r.astype(np.float64) * rs.astype(np.float64)                   # exact
+        z = q.astype(np.float64) + step
+        lost = step - (z - q.astype(np.float64))                              # exact: the sum's own rounding
+        half = (z.view(np.uint64) & 0x1FFFFFFF) == 0x10000000
+        z = np.where(half & (lost != 0), np.nextafter(z, np.where(lost > 0, np.inf, -np.inf)), z)
+        assert np.array_equal(z.astype(np.float32), v / s)
