@@ -554,7 +554,9 @@ hq_status hq_rms_norm(int32_t act_fmt, int64_t M, int64_t K, const void* x, cons
  *   v_pages   codes [num_pages, num_kv_heads, D, P]   (a token's values lie P bytes apart)
  *   k_scales, v_scales   fp32 [num_pages, num_kv_heads]; value = code * scale
  * A page is contiguous in all four: pages are copied, moved or given to another sequence by plain
- * copies of these ranges. Contents on entry do not matter before a page's first append.
+ * copies of these ranges. Contents on entry do not matter to a page's first append if that begins at its
+ * first slot. One that begins behind it (the tokens before were never stored) keeps the slots before and goes by
+ * the page's scales: set them to 0, and the codes of those slots too, where there is nothing.
  * A call's sequences b = 0 .. B-1:
  *   cu       int32 [B + 1]: the new tokens of b are the rows cu[b] .. cu[b+1]-1 of k, v, q and out
  *   kv_lens  int32 [B]: tokens of b in the cache, the new ones included: the new ones have positions
