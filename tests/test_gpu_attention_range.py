@@ -1,15 +1,16 @@
 """Attention over the paged cache at the ends of its number ranges, against float64: values near the largest bf16,
-scores of any size, rows most of whose weight is on a token of value 0."""
+scores of any size, rows most of whose weight is on a token of value 0, and
+caches past 4 GiB."""
 import numpy as np
 import pytest
+import torch
 
 import oracle
+import quantized_gemm_prepacked_amd as hq
 
-from gpu_harness import bf16_to_f64, say, to_dev
+from gpu_harness import DEV, bf16_to_f64, say, to_dev
 from layer_harness import KV, check_attention, kv_case, normal_rows
 from test_gpu_attention import _attend, _device
-
-import torch
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +120,34 @@ def test_first_token_takes_the_weight(fmt, D, G, new, length, max_kv, share):
     error = float(np.linalg.norm(got - ref) / np.linalg.norm(ref))
     say(f"  {fmt} D={D} new={new} on {length}, {share}: {error / (2.0 ** -7 / 28 ** 0.5):.3f} of the rounding to bf16")
     assert error <= 2 * 2.0 ** -7 / 28 ** 0.5
+
+
+@pytest.mark.parametrize("fmt", list(KV))
+def test_many_rows_past_32_bits(fmt):
+    """A cache of more than 4 GiB of codes, its first and last pages, read by every kernel: one token, 24 rows, 128 and 256 rows a workgroup."""
+    P, H, D, pages = 256, 8, 128, 20000
+    desc = hq.make_kv_desc(KV[fmt], H, D, P, pages)
+    assert hq.hq_kv_cache_bytes(desc) > 1 << 32
+    g = np.random.default_rng(32)
+    kp = torch.zeros((pages, H, P, D), dtype=torch.uint8, device=DEV)
+    vp = torch.zeros((pages, H, D, P), dtype=torch.uint8, device=DEV)
+    ks, vs = torch.zeros((pages, H), device=DEV), torch.zeros((pages, H), device=DEV)
+    table = np.array([[pages - 1, 0], [pages - 2, 16385]], np.int32)
+    lens, cu = np.array([300, 257], np.int32), np.array([0, 300, 557], np.int32)
+    up = lambda a: to_dev(a.view(np.int16)).view(torch.bfloat16)  # noqa: E731
+    k, v = normal_rows(g, 557, H, D), normal_rows(g, 557, H, D)
+    dlens, dtable = to_dev(lens), to_dev(table)
+    hq.hq_kv_append(desc, 2, 557, 300, up(k), up(v), H * D, to_dev(cu), dlens, dtable, 2, kp, vp, ks, vs)
+    at = torch.from_numpy(table.ravel().astype(np.int64)).to(DEV)
+    parts = [t[at].cpu().numpy() for t in (kp, vp, ks, vs)]
+    mapped = np.arange(4, dtype=np.int32).reshape(2, 2)
+    for new, max_kv in (([1, 1], 300), ([24, 3], 300), ([40, 200], 300), ([300, 257], 4096)):
+        T, most = sum(new), max(new)
+        qcu, q = np.array([0, new[0], T], np.int32), normal_rows(g, T, H, D)
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=DEV)
+        n = hq.hq_attention_workspace_bytes(desc, 2, T, H, most, max_kv)
+        hq.hq_attention(desc, 2, T, H, most, max_kv, up(q), H * D, to_dev(qcu), dlens, dtable, 2, kp, vp, ks, vs, 0.1, 0, out,
+                        torch.empty(max(n, 1), dtype=torch.uint8, device=DEV), n)
+        torch.cuda.synchronize()
+        ref = oracle.ref_attention(fmt, q, qcu, lens, mapped, *parts, 0.1, 0, np.zeros(q.shape))
+        check_attention(out.double().cpu().numpy(), *ref, D, 300, f"{fmt} past 32 bits, {new} tokens", say)
