@@ -530,7 +530,8 @@ hq_status hq_moe_decode(const hq_quant_desc* desc, int64_t T, int32_t topk, int3
  *                 product fp32( max|v| * fp32(1 / Q) ), at most a unit in the last place off that
  *                 call's quotient; v is not rounded to bf16 on the way. y_bf16, if not NULL, receives
  *                 bf16(v) as well (the router of an MoE block reads it, where the experts read the codes).
- * Since the sum is in binary64 a row's result does not depend on how the row is split over threads.
+ * The number of rows decides how many threads share a row, and with that the order of the binary64 sum: a row's sums in
+ * two orders differ by less than 2^-45 of it, so that r, rounded to 2^-24, differs in fewer than one row of a million.
  * act_fmt       HQ_ACT_BF16, HQ_ACT_INT8_PER_TOKEN, HQ_ACT_FP8E4M3_PER_TOKEN,
  *               HQ_ACT_FP8E4M3_BLOCK128 (K % 128 == 0), HQ_ACT_MXFP8, HQ_ACT_MXFP4 (K % 32 == 0)
  * x, residual, residual_out, y_bf16: bf16 [M, K] row-major; weight bf16 [K]; all 16-byte aligned, as y;
@@ -612,11 +613,11 @@ hq_status hq_kv_append(const hq_kv_desc* desc, int32_t B, int64_t T, int32_t max
  * num_kv_heads) of the cache):
  *   out[t, i] = bf16( sum_j p_j v_j / sum_j p_j ),  p_j = exp( sm_scale * q[t, i] . k_j ),
  * over the positions j <= pos(t) of t's sequence, with window > 0 only j > pos(t) - window. A row
- * that sees no token gets zeros. fp32 accumulation and statistics: scores may be of any size below 2^127 in units
- * of log 2 (a row with one past that is unspecified). p_j * scale (of v_j) enters the product with the codes as an
- * fp16, off by 2^-11 of itself or 2^-35 of the row's largest. Scales are not negative (hq_kv_append makes
- * none). NaN in a query's row reaches that row alone, a NaN key the rows that see it; a NaN code among the
- * values (hq_kv_append makes none) any row of its sequence.
+ * that sees no token gets zeros. fp32 accumulation and statistics: sums of q times codes, and
+ * scores in units of log 2, may be of any size below 2^127 (a row with one past that is unspecified). p_j * scale (of
+ * v_j) enters the product with the codes as an fp16, off by 2^-11 of itself or 2^-35 of the row's largest. Scales are
+ * not negative (hq_kv_append makes none). NaN in a query's row reaches that row alone, a NaN key the rows that see it;
+ * a NaN code among the values (hq_kv_append makes none) any row of its sequence.
  *   q        bf16, token rows q_stride elements apart (>= Hq * D, a multiple of 8), 16-byte aligned, T rows
  *   out      bf16 [T, Hq, D], 16-byte aligned; may be q where q_stride = Hq * D
  *   max_q    at least the largest number of query tokens of a sequence

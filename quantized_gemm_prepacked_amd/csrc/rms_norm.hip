@@ -2,10 +2,9 @@
 // the following GEMM behind: h = bf16(x + residual), v = (h * r) * weight with r = 1 / sqrt(mean h^2 +
 // eps), written as bf16 or as codes and scales by the rules of act_quant.hip, applied to the unrounded v.
 //
-// The sum of squares is in binary64. Squares of bf16 values are exact there and the sum's error is
-// below 2^-40 of a code's step, so r, and with it every code, is the same however a row is spread
-// over threads; the conversion and the add run at the vector units' ordinary rate, far below what the
-// loads take.
+// The sum of squares is in binary64. Squares of bf16 values are exact there, and a sum has 86 roundings at most (64 terms a thread, 6 and 16
+// joins): two orders of it, for another number of threads, differ by less than 2 * 86 * 2^-53 of it, and r, rounded to 2^-24, differs in
+// fewer than one row of a million. The conversion and the add run at the vector units' ordinary rate, far below what the loads take.
 //
 // A row is held in registers between its passes (sum, maximum, codes): each thread keeps C chunks of
 // eight bf16 sums h, so memory is read and written once. What bounds it is that traffic: 8192 rows of
