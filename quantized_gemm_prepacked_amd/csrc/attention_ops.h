@@ -86,6 +86,7 @@ constexpr float kMostWeights = 65504.0f;      // the largest fp16
 constexpr float kFar = -60.0f;
 constexpr float kLarge = 4096.0f;   // (below, a fused product is within 2^-12 of the rounded one)
 constexpr float kNone = -3e38f;     // top of a row that has seen nothing: its scores are -infinity, its sums 0
+constexpr float kLeast = -1e37f;    // rel of a row that has seen no value but 0: lv - rel - top stays finite whatever the scores are
 
 template <int NQ, int TILES>
 struct Rows {
@@ -126,7 +127,7 @@ struct Rows {
         const bool far_now = !(e[n] > kFar);
         const bool moves = row_max((far_now ? m > top[n] + kSlack : !(part[n] <= kMostWeights && more[n] <= kMost)) ? 1.0f : 0.0f) > 0.0f;
         const float top1 = moves ? fmaxf(top[n], rm) : top[n];
-        const float old = rel[n] + (top[n] - top1), rw = row_max((m - top1) + lv) - kRaise;
+        const float old = fmaxf(rel[n] + (top[n] - top1), kLeast), rw = row_max((m - top1) + lv) - kRaise;
         const float rel1 = moves ? fmaxf(old, rw) : rel[n];
         if (__any(moves && top[n] > kNone)) {      // (where a row had seen nothing, sum and acc are 0)
           sum[n] *= exp2_fast(top[n] - top1);

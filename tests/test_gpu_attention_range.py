@@ -88,6 +88,22 @@ def test_scores_of_any_size(fmt, D, G, new, length, max_kv):
 
 
 @pytest.mark.parametrize("fmt", list(KV))
+@pytest.mark.parametrize("D,G,new,length,max_kv", PATHS)
+def test_largest_scores_on_values_of_zero(fmt, D, G, new, length, max_kv):
+    """Rows' largest scores of 2^124 to 2^127, and values of zero (scale 0) where a row begins, or everywhere: rows of a value, zeros, nothing else."""
+    g = np.random.default_rng([3, D, new, length])
+    c = kv_case(g, fmt, 2, D, 16, [new], [length])
+    q = normal_rows(g, new, 2 * G, D, 2.0 ** 100)
+    sm = 2.0 ** 23 / D ** 0.5
+    for zeros in (slice(0, 6), slice(None)):
+        c["v_scales"][c["table"][0][c["table"][0] >= 0][zeros]] = 0
+        got, ref = _run(c, q, max_kv, sm)
+        largest = np.abs(ref[0]).max()
+        assert np.isfinite(got).all() and (np.abs(got) <= largest * (1 + 2.0 ** -7)).all(), zeros
+        assert zeros != slice(None) or (got == 0).all()
+
+
+@pytest.mark.parametrize("fmt", list(KV))
 @pytest.mark.parametrize("D,G,new,length,max_kv", [(64, 4, 1, 30000, 64), (128, 4, 4, 20000, 64), (64, 4, 40, 20000, 64), (128, 2, 40, 9000, 64), (256, 1, 40, 9000, 64),
                                                    (128, 4, 64, 20000, 2048)])
 @pytest.mark.parametrize("share", [0.9, 0.99, 0.999])
