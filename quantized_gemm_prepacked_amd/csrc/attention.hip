@@ -13,10 +13,10 @@
 // The next block's keys are asked for when this one's are used up, and so the values: the loads of one block are in flight
 // while the other is worked on, in the same registers (a whole block ahead in registers of its own was no faster).
 //
-// Measured (a 2 GiB copy moves 5.05 TB/s, a read stream 6.13): one token, 32 heads on 8, 131071 positions: 269 MB in 48 us and
-// 5 us for the join, 5.6 TB/s; 64 tokens on lengths up to 8000 (INT8, 64 heads on 8): 139 us, 4.9 TB/s, 5.75 where all
-// lengths are alike, the rest is the longest sequences' tail. One token on 100 positions: 4.5 us, a launch and three
-// dependent trips to memory.
+// Measured (a 2 GiB copy moves 5.05 TB/s, a read stream 6.13; kernels alone, in a trace): one token, 32 heads on 8, 131071
+// positions: 269 MB in 50 us, 5.4 TB/s, and 5 us for the join; 64 tokens on lengths up to 8000 (INT8, 64 heads on 8): 141 us, 4.8
+// TB/s, the rest is the longest sequences' tail. One token on 100 positions: 5.3 us, a launch and three dependent trips to memory.
+// 32 rows at head sizes 192 and 256 spill up to 4 registers.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -293,8 +293,9 @@ int64_t attention_groups(const KvCall& c) { return (int64_t(c.max_new) * c.G + k
 
 namespace {
 // Parts of the positions: no more workgroups than run at once, each with at least `least` blocks. With more, the last ones
-// run alone: one token on 131072 positions with 512 / 768 / 1024 / 2048 workgroups 56.7 / 60.8 / 65.1 / 65.1 us; 16 tokens on
-// 30000 72.9 / 82.2 / 87.3 / 81.9; D = 256, 4 tokens on 20000 with 256 / 512 / 1024: 33.6 / 42.5 / 48.1.
+// run alone: one token on 131071 positions with 256 / 512 / 768 / 1024 workgroups 57.9 / 57.5 / 59.3 / 60.1 us; 16 tokens on up to
+// 30000 140.5 / 139.6 / 158.6 / 142.2 (134.3 with 2048); D = 64, 16 on up to 10000 38.0 / 31.4 / 32.6 / 32.4; D = 192, 32 on up to 4000 65.2 /
+// 66.4 / 70.8 / 69.1; D = 256, 4 tokens on 20000 with 256 / 512 / 1024: 23.8 / 32.1 / 38.4.
 void split_of(int64_t groups, int64_t wanted, int64_t least, int64_t max_kv, int* n_split, int* each) {
   const int64_t blocks = std::max<int64_t>((max_kv + kBlock - 1) / kBlock, 1);
   int64_t n = std::max<int64_t>(wanted / groups, 1);
@@ -323,9 +324,9 @@ AttentionPlan plan_attention(const KvCall& c, int64_t max_kv) {
     const int resident = c.D > 192 ? 256 : 512;      // two workgroups a CU, one where its registers leave room for no more
     const int64_t heads = int64_t(c.B) * c.H;
     // More than 16 rows: in two workgroups, which both read the keys and values, where these fit on the card at once and a part is
-    // short, so that what counts is latency (4 tokens and 8 heads, us in one / in two; D = 128: 8 sequences of 3000 22.0 / 20.9, 2 of 8000
-    // 17.2 / 16.3; D = 256: 1 of 20000 24.7 / 20.6, 7 x 5 tokens in a window of 1024 19.7 / 17.0); in one where a part is long
-    // (16 of 5000 38.5 / 46.9, 2 of 30000 29.2 / 33.6) or there are more of them (40 of 3000: 47.1 / 52.3, D = 256 53.4 / 73.5).
+    // short, so that what counts is latency (4 tokens and 8 heads, us in one / in two; D = 128: 8 sequences of 3000 22.2 / 21.9, 2 of 8000
+    // 17.1 / 16.7; D = 256: 7 x 5 tokens of 6 heads in a window of 1024 20.8 / 17.6); in one where a part is long (16 of 5000 38.1 / 47.4,
+    // 2 of 30000 26.8 / 32.7; D = 256: 1 of 20000 29.0 / 29.8) or there are more of them (40 of 3000: 54.7 / 62.6, D = 256 92.0 / 117.5).
     split_of(2 * heads, resident, kWaves, max_kv, &p.few_split, &p.few_each);
     if (p.few * c.G <= 16 || 2 * heads > resident || p.few_each > 16) {
       split_of(heads, resident, kWaves, max_kv, &p.few_split, &p.few_each);
@@ -338,10 +339,10 @@ AttentionPlan plan_attention(const KvCall& c, int64_t max_kv) {
     // Tiles there can be: of T rows, with one broken tile a sequence.
     const auto tiles_of = [&](int64_t rows) { return std::min((most + rows - 1) / rows * c.B, c.T * c.G / rows + c.B) * c.H; };
     // The kernel of 256 rows a workgroup for long sequences whose work fills the card: each tile sees about as many positions, or
-    // there are two tiles a CU (us with 128 rows a workgroup / with 256): 1024 x 8 rows on 30000 1104 / 897, 4 x 512 x 8 on 16000
-    // 554 / 456, 256 x 4 on 8000 67 / 62; prompts, 8 heads of the cache, of 8192 x 4 562 / 507, 4096 x 4 175 / 147, 2048 x 8 100 / 89.
-    // Fewer or shorter ones are better off with small tiles: prompts of 2048 x 4 62 / 70, of 4500 x 1 114 / 133, of 9000 x 1 233 / 250,
-    // 8 of 1000 x 4 74 / 83, of 8192 x 4 with a window of 1024 185 / 191.
+    // there are two tiles a CU (us with 128 rows a workgroup / with 256): 1024 x 8 rows on 30000 1056 / 863, 4 x 512 x 8 on 16000
+    // 524 / 434, 256 x 4 on 8000 65 / 61; prompts, 8 heads of the cache, of 8192 x 4 545 / 485, 4096 x 4 162 / 137, 2048 x 8 91 / 82.
+    // Fewer or shorter ones are better off with small tiles: prompts of 2048 x 4 60 / 66, of 4500 x 1 110 / 126, of 9000 x 1 224 / 234,
+    // 8 of 1000 x 4 70 / 80, of 8192 x 4 with a window of 1024 180 / 185.
     const bool even = max_kv >= 2 * int64_t(c.max_new), full = tiles_of(2 * kTileRows) >= 512;
     p.tile_rows = c.D == 128 && max_kv >= 2048 && c.T * c.G >= 2 * kTileRows * int64_t(c.B) && (even || full) ? 2 * kTileRows : kTileRows;
     // Room for either kernel: which one it is goes by the window too, the workspace's size does not.

@@ -6,8 +6,10 @@
 // the same blocks of 64 positions. A block's codes are asked for from memory while the block before is worked on, converted
 // once by the whole workgroup (keys to bf16, values to fp16), and handed to the waves through two LDS buffers in turn, so
 // that there is one barrier a block. Products, lane layout and softmax are those of the few-row kernel. Measured, with the kernel of
-// 256 rows below where it serves: 4 prompts of 4500, 32 heads on 8 of 128, e4m3: 465 us, 947 TFLOP/s; 1024 tokens, 64 heads
-// on 8, INT8, on 30000 positions: 871 us, 1.18 PFLOP/s (a bf16 matrix product of 8192 reaches 1.44, of 16384 1.62).
+// 256 rows below where it serves: 4 prompts of 4500, 32 heads on 8 of 128, e4m3: 468 us, 940 TFLOP/s; 1024 tokens, 64 heads
+// on 8, INT8, on 30000 positions: 874 us, 1.17 PFLOP/s (a bf16 matrix product of 8192 reaches 1.44, of 16384 1.62). 4 prompts of up to 4500 and
+// that piece with this kernel's other head sizes, in TFLOP/s: 64: 690 and 670, 96: 730 and 820, 192: 500 and 590, 256: 490 and 580 (192 and 256
+// leave room for one workgroup a CU, one wave a SIMD, so that nothing hides softmax and barriers).
 //
 // Bank conflicts: gfx950 serves a 16-byte LDS read of a wave 16 lanes at a time, eight of one lane group and the other
 // eight of the next (lanes 0-3, 12-15 and 20-27; 4-11, 16-19 and 28-31; and so the upper half). Rows are stored with
@@ -35,7 +37,7 @@ __device__ __forceinline__ void lds_barrier() {
 
 // A workgroup's part of the work. One sequence after the other, its last tiles first, which see most. Heads next to each other: with
 // eight of them a head's workgroups run on one XCD, whose L2 then holds one head of one or two sequences (with all sequences' tiles
-// in turn instead, 4 prompts of 4500 take 690 us, not 505).
+// in turn instead, 4 prompts of 4500 took 690 us at a build where they take 505 so).
 struct Place {
   int head, b, part, r0;
 };
@@ -257,9 +259,9 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_tile_
 // k - 1, keys of block k) while the other has its maxima and exponentials. A barrier ends each half. Between its matrix instructions
 // every wave converts its share of the keys of k + 1 and the values of k, and asks for the next: a half turn before their first
 // reader's turn, into the one of two LDS buffers that its last reader left a half turn before.
-// The multiplying wave goes first where both could issue (897 us for 1024 x 8 rows on 30000, 970 without). What bounds it is the
+// The multiplying wave goes first where both could issue (1024 x 8 rows on 30000 at one build: 897 us, 970 without). What bounds it is the
 // vector instructions' port: 150 a wave and block for the softmax, 90 for conversions and addresses, beside 64 matrix instructions;
-// without its products that call took 653 us of 895, without softmax 777, without staging 720, products and LDS reads alone 618.
+// without its products that build took 653 us, without softmax 777, without staging 720, products and LDS reads alone 618.
 // Head size 128 alone: larger ones leave no room for two waves on a SIMD, at 64 three workgroups of the kernel above do better
 // (2048 rows of 8 heads on 30000: 1443 us, 1632 here).
 template <int FMT>

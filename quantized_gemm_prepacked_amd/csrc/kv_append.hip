@@ -5,8 +5,10 @@
 // new tokens, and where the scale grew the codes that were there. Nothing is shared between workgroups.
 //
 // What bounds it is the traffic, each new value read once and each code written once: 5 prompts of up to 4000 tokens (INT8, 8
-// heads of 128, 108 MB) take 25 us, 4.3 TB/s; one token of each of 48 sequences 4.8 us, a launch and the dependent
-// reads of lengths, page, scale and tokens.
+// heads of 128, 108 MB) take 25 us, 4.3 TB/s; one token of each of 48 sequences 4.5 us, a launch and the dependent
+// reads of lengths, page, scale and tokens. Where a page's scale grows, its codes go through one wave (a few new tokens) or workgroup
+// one dword (keys) or byte (values) a thread after another: 48 e4m3 tokens into pages of 16 / 64 / 256 slots of 128 channels 9 / 29 / 138 us, where
+// they fit 3.4 / 3.8 / 3.8.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

@@ -9,7 +9,8 @@
 // A row is held in registers between its passes (sum, maximum, codes): each thread keeps C chunks of
 // eight bf16 sums h, so memory is read and written once. What bounds it is that traffic: 8192 rows of
 // 8192 to INT8 with a residual move 470 MB in 86 us, 5.5 TB/s, where a copy reaches 5.0. One row of
-// 4096 takes 2.6 us to bf16, a launch and two dependent trips to memory.
+// 4096 takes 3.6 us to e4m3, a launch, two dependent trips to memory and two reductions. Rows past 32768 columns are 8 chunks a thread, which spill
+// 15 to 28 registers: 512 of 40960 to INT8 61 us, 2.4 TB/s (of 32768, 4 chunks: 34 us, 3.4 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "device_ops.h"
@@ -198,11 +199,11 @@ hipError_t go(const RmsNormCall& a, hipStream_t s) {
 
 // Threads a row. Few rows leave most of the chip idle, so a row's latency counts and more threads with less each are better;
 // with many rows the loads in flight count, and the idle threads behind the row's end. Measured with a residual, in us:
-//   K 2048, INT8:    64 threads 4.8 at 67 rows, 5.7 at 1024, 14.1 at 4099; 256 threads 3.4, 5.9, 16.4
-//   K 4096, INT8:    256 threads 3.8 at 1 row, 4.5 at 256, 5.3 at 512, 22.3 at 4099; 512 threads 3.6, 4.4, 6.0, 29.5; 64 threads 6.3, 7.3, 7.7, 25.9
-//   K 8192, MXFP8:   256 threads 4.3 at 67 rows, 8.6 at 512, 22.1 at 2048, 47.2 at 4099; 512 threads 3.7, 8.3, 25.4, 52.8
-//   K 8192, INT8:    256 threads 5.5 at 67 rows, 9.8 at 512, 14.3 at 1024; 512 threads 4.7, 9.3, 14.5
-//   K 14336, INT8:   512 threads 6.1 at 67 rows, 82.2 at 4099; 1024 threads 5.9, 82.2; 256 threads 7.7, 84.8
+//   K 2048, INT8:    64 threads 5.4 at 67 rows, 6.6 at 1024, 14.6 at 4099; 256 threads 4.1, 6.9, 17.0
+//   K 4096, INT8:    256 threads 4.4 at 1 row, 5.1 at 256, 6.5 at 512, 26.6 at 4099; 512 threads 4.3, 5.1, 7.1, 31.6; 64 threads 6.9, 8.0, 8.8, 30.7
+//   K 8192, MXFP8:   256 threads 4.8 at 67 rows, 9.2 at 512, 26.6 at 2048, 46.5 at 4099; 512 threads 4.4, 9.0, 29.8, 52.1
+//   K 8192, INT8:    256 threads 6.1 at 67 rows, 10.4 at 512, 14.8 at 1024; 512 threads 5.3, 10.0, 14.5
+//   K 14336, INT8:   512 threads 6.7 at 67 rows, 79.4 at 4099; 1024 threads 6.5, 79.9; 256 threads 8.0, 81.2
 template <int ACT>
 hipError_t pick(const RmsNormCall& a, hipStream_t s) {
   const bool many = a.M >= 1024;
