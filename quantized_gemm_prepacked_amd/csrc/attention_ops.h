@@ -204,7 +204,6 @@ struct Rows {
       weight[n][1] = __builtin_bit_cast(f16x8, v);
     }
   }
-
 };
 
 // Parts hand on averages, not sums: a sum of values near the largest bf16 leaves fp32's range where their average does not. They
